@@ -515,6 +515,147 @@ arResult_t arGetGroupPlan(arComm_t comm, int index, arPlan_t* plan);
 arResult_t arAllReduceNoAlloc(const void* const* sendbufs, void* const* recvbufs, int nranks, int nChannels,
                               size_t count, arDataType_t dtype, arRedOp_t op, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of a training or serving step around its AllReduce: the norm a
+ * layer applies to every rank's rows, whose weights' gradient is a sum over
+ * all of them; and the global norm and clipping of the reduced gradients.
+ * Like arAllReduceNoAlloc these calls need no communicator: each only
+ * enqueues kernels on `stream`, in which no workgroup waits for another, and
+ * allocates nothing, so any call may be captured into a HIP graph, the first
+ * included.  Scratch memory is the caller's: `workspace` (device, 16-byte
+ * aligned, at least the bytes the matching ...Workspace call reports) is
+ * written before it is read in every call and carries nothing from one call
+ * to the next; calls that may run at the same time (other streams, two graphs
+ * replayed side by side) each need their own.  Results do not depend on
+ * timing: every sum has a fixed order, in 32 bits or more, and is rounded
+ * once at the end.  dtype is arFloat32, arFloat16 or arBfloat16.  Pointers
+ * need element alignment only.  Calls made while the thread has a group open
+ * (arGroupStart) return arInvalidUsage and enqueue nothing: they do not queue.
+ */
+
+/*
+ * arLayerNorm -- layer norm of every rank's rows in one launch (ranks beyond
+ * 32 in further launches of 32):  with m the mean of a row of `cols` values
+ * and v the mean of (x - m)^2,  rstd = 1 / sqrt(v + eps)  and
+ * y = (x - m) * rstd * gamma + beta.
+ *  x, y        (host arrays of nranks device pointers) rank r's rows[r] rows of
+ *              `cols` elements of `dtype`, row i at i * xStride (yStride)
+ *              elements; the elements between rows are neither read nor
+ *              written.  y[r] == x[r] with equal strides is allowed (in place);
+ *              otherwise an output must not overlap any other buffer.
+ *  gamma, beta (host arrays, either may be NULL: 1 and 0) rank r's copy of the
+ *              weights, `cols` elements of `wtype` (dtype or arFloat32).
+ *  mean, rstd  (host arrays, both or neither NULL) rank r's rows[r] float
+ *              statistics, for arLayerNormBackward.
+ *  rows        (host, nranks) rows of each rank; a rank may have 0 (its
+ *              pointers are not looked at then, those of dgamma and dbeta in
+ *              arLayerNormBackward apart).
+ *  nranks      1..AR_MAX_RANKS.
+ *  cols        1..2^30; strides at least cols.
+ *  eps         finite, >= 0.
+ * Errors: arInvalidArgument (nothing enqueued), arInvalidUsage in an open
+ * group, arHipError, arSystemError.
+ */
+arResult_t arLayerNorm(const void* const* x, const void* const* gamma, const void* const* beta, void* const* y,
+                       float* const* mean, float* const* rstd, const size_t* rows, int nranks, size_t cols,
+                       size_t xStride, size_t yStride, float eps, arDataType_t dtype, arDataType_t wtype,
+                       void* stream);
+
+/*
+ * arLayerNormBackward -- the gradients of arLayerNorm, those of the weights
+ * summed over every rank's rows and written to every rank (the result of an
+ * AllReduce over the ranks' own sums, formed once in 32 bits).  With
+ * h = (x - mean) * rstd, q = dy * gamma and sums over a row:
+ *   dx = rstd * (q - sum(q) / cols - h * sum(q h) / cols),
+ *   dgamma = sum over all rows of dy * h,   dbeta = sum over all rows of dy.
+ *  dy, x, dx   (host arrays) as x and y of arLayerNorm, each with its row
+ *              stride; dx may be NULL (only the weights' gradients), and dx[r]
+ *              may be dy[r] or x[r] with equal strides.
+ *  gamma       (host array or NULL: 1) as in arLayerNorm.
+ *  mean, rstd  (host arrays) the statistics arLayerNorm wrote.
+ *  dgamma, dbeta (host arrays, either may be NULL) nranks buffers of `cols`
+ *              elements of `wtype`; written with zeros when no rank has a row.
+ *  workspace, workspaceBytes  see above; may be NULL / 0 when dgamma and dbeta
+ *              both are.
+ * Other arguments and errors as arLayerNorm; also arInvalidArgument when the
+ * workspace is too small or all of dx, dgamma and dbeta are NULL.
+ */
+arResult_t arLayerNormBackward(const void* const* dy, const void* const* x, const void* const* gamma,
+                               const float* const* mean, const float* const* rstd, void* const* dx,
+                               void* const* dgamma, void* const* dbeta, const size_t* rows, int nranks, size_t cols,
+                               size_t dyStride, size_t xStride, size_t dxStride, arDataType_t dtype,
+                               arDataType_t wtype, void* workspace, size_t workspaceBytes, void* stream);
+
+/* arLayerNormBackwardWorkspace -- the workspace bytes of an
+ * arLayerNormBackward with these rows and columns (a pure function). */
+arResult_t arLayerNormBackwardWorkspace(const size_t* rows, int nranks, size_t cols, size_t* bytes);
+
+/* A list of gradient tensors, laid out on the device once and used every step. */
+typedef struct arTensorList* arTensorList_t;
+
+/*
+ * arTensorListCreate -- lay a list of tensors out for arGradNorm and
+ * arGradClip on the current device: all of a model's gradients, or all ranks'
+ * shards of them after a ReduceScatter.  The work is cut into spans of about
+ * equal bytes, so a list of many small tensors and a few large ones keeps the
+ * whole GPU busy.
+ *  list      (host, out) receives the handle.
+ *  nTensors  0..2^20.
+ *  src       (host array) device pointer of each tensor, counts[i] contiguous
+ *            elements of dtypes[i]; may be NULL where counts[i] is 0.  One
+ *            tensor may be listed twice (and then counts twice) if it is not
+ *            written.
+ *  dst       (host array or NULL) where arGradClip writes each tensor: src[i]
+ *            itself (in place) or memory that overlaps no other tensor.  NULL:
+ *            the list is only for arGradNorm.
+ * The arrays are copied; the tensors themselves are the caller's and must stay
+ * where they are while the list is used.  Allocates device memory (32 bytes a
+ * tensor or span) and copies to it synchronously: not for capture.
+ * Errors: arInvalidArgument (bad pointers, counts, types; outputs that
+ * overlap), arHipError, arSystemError.
+ */
+arResult_t arTensorListCreate(arTensorList_t* list, int nTensors, const void* const* src, void* const* dst,
+                              const size_t* counts, const arDataType_t* dtypes);
+
+/* arTensorListWorkspace -- the workspace bytes of arGradNorm and arGradClip on
+ * this list. */
+arResult_t arTensorListWorkspace(arTensorList_t list, size_t* bytes);
+
+/* arTensorListDestroy -- free the list's device memory (waits for work that
+ * uses it).  Graphs that captured calls on it must not be replayed again. */
+arResult_t arTensorListDestroy(arTensorList_t list);
+
+typedef enum {
+  arNorm2 = 0,       /* sqrt of the sum of squares */
+  arNormMax = 1      /* largest absolute value */
+} arNormKind_t;
+
+/*
+ * arGradNorm -- norm = |scale| * (norm over all elements of all tensors of the
+ * list), written to the float `norm` points at (device).
+ *  scale   finite; 1/N for the mean of gradients that arSum added over N ranks,
+ *          or the inverse of a loss scale.
+ * Squares are formed and summed in 64 bits: no value of any type overflows or
+ * vanishes.  A NaN or infinity among the values gives a NaN or infinite norm.
+ * An empty list has norm 0.  The device must be the list's (arInvalidUsage).
+ */
+arResult_t arGradNorm(arTensorList_t list, arNormKind_t kind, float scale, float* norm, void* workspace,
+                      size_t workspaceBytes, void* stream);
+
+/*
+ * arGradClip -- arGradNorm, then every tensor scaled to its dst:
+ *   dst = src * (scale * c),   c = 1 if norm + eps <= maxNorm, else maxNorm / (norm + eps).
+ * The factor scale * c is formed in 64 bits and rounded to a float once; the
+ * products are rounded once to the tensor's type.  norm (device, may be NULL)
+ * receives the norm before clipping.  A NaN norm makes every output NaN, an
+ * infinite one (with a finite maxNorm) makes finite values 0 and infinities
+ * NaN.  Tensors in place whose factor is exactly 1 are left unread and
+ * unwritten.  maxNorm >= 0 (may be infinite), eps finite and >= 0.
+ * arInvalidUsage on a list made without dst.
+ */
+arResult_t arGradClip(arTensorList_t list, arNormKind_t kind, float scale, float maxNorm, float eps, float* norm,
+                      void* workspace, size_t workspaceBytes, void* stream);
+
 const char* arGetErrorString(arResult_t result);
 
 /* Library limits. */

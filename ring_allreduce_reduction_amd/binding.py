@@ -26,6 +26,8 @@ arSum, arMax, arMin, arProbe = 0, 1, 2, 3
     0, 1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13)
 AR_MAX_RANKS, AR_MAX_CHANNELS = 128, 64
 arFuncAllReduce, arFuncReduceScatter, arFuncAllGather = 0, 1, 2
+arNorm2, arNormMax = 0, 1
+NORM_BY_NAME = {"2": arNorm2, "max": arNormMax}
 FUNC_BY_NAME = {"allreduce": arFuncAllReduce, "reducescatter": arFuncReduceScatter,
                 "allgather": arFuncAllGather}
 
@@ -105,6 +107,16 @@ def lib():
         L.arCommFootprint.argtypes = [vp, ctypes.POINTER(c_sz)]
         L.arTuneTableTime.argtypes = [c_int, c_sz, c_int, c_int, ctypes.POINTER(c_f)]
         L.arAllReduceNoAlloc.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(vp), c_int, c_int, c_sz, c_int, c_int, vp]
+        vps, szs = ctypes.POINTER(vp), ctypes.POINTER(c_sz)
+        L.arLayerNorm.argtypes = [vps, vps, vps, vps, vps, vps, szs, c_int, c_sz, c_sz, c_sz, c_f, c_int, c_int, vp]
+        L.arLayerNormBackward.argtypes = [vps, vps, vps, vps, vps, vps, vps, vps, szs, c_int, c_sz, c_sz, c_sz, c_sz,
+                                          c_int, c_int, vp, c_sz, vp]
+        L.arLayerNormBackwardWorkspace.argtypes = [szs, c_int, c_sz, szs]
+        L.arTensorListCreate.argtypes = [vps, c_int, vps, vps, szs, ctypes.POINTER(c_int)]
+        L.arTensorListWorkspace.argtypes = [vp, szs]
+        L.arTensorListDestroy.argtypes = [vp]
+        L.arGradNorm.argtypes = [vp, c_int, c_f, vp, vp, c_sz, vp]
+        L.arGradClip.argtypes = [vp, c_int, c_f, c_f, c_f, vp, vp, c_sz, vp]
         L.arDestroy.argtypes = [vp]
         L.arSetDebug.argtypes = [vp, c_int, ctypes.c_int64]
         L.arGetErrorString.argtypes = [c_int]
@@ -114,7 +126,9 @@ def lib():
                    "arSetAlgo", "arTuneAlgo", "arTuneEvalAlgo", "arTuneGetAlgoModel", "arTuneSetAlgoModel",
                    "arGroupStart", "arGroupEnd", "arGroupAggregate", "arGetGroupPlan",
                    "arCommGetAsyncError", "arCommAbort", "arCommCount", "arDestroy", "arSetDebug",
-                   "arAllReduceNoAlloc", "arTuneTableTime", "arCommFootprint"):
+                   "arAllReduceNoAlloc", "arTuneTableTime", "arCommFootprint", "arLayerNorm", "arLayerNormBackward",
+                   "arLayerNormBackwardWorkspace", "arTensorListCreate", "arTensorListWorkspace",
+                   "arTensorListDestroy", "arGradNorm", "arGradClip"):
             getattr(L, fn).restype = c_int
         _lib = L
     return _lib
@@ -415,6 +429,266 @@ def arSetDebug(comm, knob, value):
 
 def arDestroy(comm):
     _check(lib().arDestroy(comm), "arDestroy")
+
+
+# ---------------------------------------------------------------- operators around the AllReduce
+
+_FLOAT_DTYPES = {torch.float32: arFloat32, torch.float16: arFloat16, torch.bfloat16: arBfloat16}
+
+
+def _on_device(tensors):
+    """Every tensor of a call lives on torch's current device: the kernels run there."""
+    dev = None
+    for t in tensors:
+        if t.device.type != "cuda":
+            raise ValueError("operator tensors must be device tensors, got one on %s" % t.device)
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.device.index != dev:
+            raise ValueError("a tensor is on %s, the current device is cuda:%d" % (t.device, dev))
+
+
+def _workspace(nbytes, stream):
+    """A workspace from the pool of the stream that uses it, so that it may be reused on that stream once the
+    caller lets go of it (under capture: from the graph's own pool)."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+def _check_workspace(workspace, nbytes):
+    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError("the workspace must be contiguous and hold %d bytes" % nbytes)
+    if workspace.data_ptr() % 16:
+        raise ValueError("the workspace must be 16-byte aligned")
+
+
+def _row_views(what, tensors, n, cols, dtype, rows=None):
+    """(rows, stride) of the ranks' row buffers: each (..., cols), contiguous or 2-D with unit column stride and
+    a row stride that all ranks share."""
+    if len(tensors) != n:
+        raise ValueError("need %d %s buffers, got %d" % (n, what, len(tensors)))
+    out, stride = [], None
+    for r, t in enumerate(tensors):
+        shape = t.shape
+        if not shape or shape[-1] != cols:
+            raise ValueError("%s buffer %d has shape %s, expected rows of %d" % (what, r, tuple(shape), cols))
+        if t.dtype != dtype:
+            raise ValueError("%s buffer %d is %s, expected %s like the others" % (what, r, t.dtype, dtype))
+        k = shape[0] if len(shape) == 2 else t.numel() // cols
+        if rows is not None and k != rows[r]:
+            raise ValueError("%s buffer %d has %d rows, expected %d" % (what, r, k, rows[r]))
+        if k > 1 or not t.is_contiguous():
+            if t.is_contiguous():
+                s = cols
+            elif len(shape) == 2 and (cols == 1 or t.stride(1) == 1) and (k <= 1 or t.stride(0) >= cols):
+                s = t.stride(0) if k > 1 else None
+            else:
+                raise ValueError("%s buffer %d must have contiguous rows" % (what, r))
+            if s is not None:
+                if stride is None:
+                    stride = s
+                elif stride != s:
+                    raise ValueError("%s buffer %d has row stride %d, the others %d" % (what, r, s, stride))
+        out.append(k)
+    return out, (cols if stride is None else stride)
+
+
+def _flat_bufs(what, tensors, n, sizes, dtype):
+    if len(tensors) != n:
+        raise ValueError("need %d %s buffers, got %d" % (n, what, len(tensors)))
+    for r, t in enumerate(tensors):
+        if t.dtype != dtype:
+            raise ValueError("%s buffer %d is %s, expected %s" % (what, r, t.dtype, dtype))
+        if not t.is_contiguous() or t.numel() != sizes[r]:
+            raise ValueError("%s buffer %d must hold %d contiguous elements" % (what, r, sizes[r]))
+
+
+def _norm_types(xs, weights):
+    """The element types of rows and weights, and the shared width."""
+    if not xs:
+        raise ValueError("need at least one rank")
+    x = xs[0]
+    if x.dtype not in _FLOAT_DTYPES or x.dim() < 1:
+        raise ValueError("rows must be float32, float16 or bfloat16 tensors of at least one dimension")
+    if x.shape[-1] < 1:
+        raise ValueError("rows must have at least one column")
+    wt = x.dtype
+    for w in weights:
+        if w:
+            wt = w[0].dtype
+            break
+    if wt != x.dtype and wt != torch.float32:
+        raise ValueError("weights must be %s or float32, got %s" % (x.dtype, wt))
+    return x.dtype, wt, x.shape[-1]
+
+
+def _arr(tensors):
+    return None if tensors is None else (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
+
+
+def arLayerNorm(xs, ys, gammas=None, betas=None, means=None, rstds=None, eps=1e-5, stream=None):
+    """Layer norm of every rank's rows.  xs, ys: one tensor per rank, (..., cols), contiguous or 2-D with padded
+    rows (one row stride for all ranks of a list); gammas, betas: the ranks' weights, of the rows' type or
+    float32; means, rstds: float32 tensors of one element per row, for arLayerNormBackward.  ys may be xs."""
+    n = len(xs)
+    dt, wt, cols = _norm_types(xs, (gammas, betas))
+    rows, xs_stride = _row_views("input", xs, n, cols, dt)
+    _, ys_stride = _row_views("output", ys, n, cols, dt, rows)
+    if (means is None) != (rstds is None):
+        raise ValueError("give both means and rstds or neither")
+    seen = list(xs) + list(ys)
+    for what, w in (("gamma", gammas), ("beta", betas)):
+        if w is not None:
+            _flat_bufs(what, w, n, [cols] * n, wt)
+            seen += w
+    if means is not None:
+        _flat_bufs("mean", means, n, rows, torch.float32)
+        _flat_bufs("rstd", rstds, n, rows, torch.float32)
+        seen += list(means) + list(rstds)
+    _on_device(seen)
+    _check(lib().arLayerNorm(_arr(xs), _arr(gammas), _arr(betas), _arr(ys), _arr(means), _arr(rstds),
+                             (ctypes.c_size_t * n)(*rows), n, cols, xs_stride, ys_stride, float(eps),
+                             _FLOAT_DTYPES[dt], _FLOAT_DTYPES[wt], ctypes.c_void_p(_stream_handle(stream))),
+           "arLayerNorm")
+
+
+def arLayerNormBackwardWorkspace(rows, cols):
+    """Bytes of workspace of an arLayerNormBackward over ranks with these rows."""
+    b = ctypes.c_size_t()
+    _check(lib().arLayerNormBackwardWorkspace((ctypes.c_size_t * len(rows))(*rows), len(rows), int(cols),
+                                              ctypes.byref(b)), "arLayerNormBackwardWorkspace")
+    return b.value
+
+
+def arLayerNormBackward(dys, xs, means, rstds, gammas=None, dxs=None, dgammas=None, dbetas=None, workspace=None,
+                        stream=None):
+    """The gradients of arLayerNorm from its inputs and statistics: dxs (may be dys or xs, or None), and dgammas /
+    dbetas (or None), each rank's copy of the sums over all ranks' rows.  workspace: a device tensor of
+    arLayerNormBackwardWorkspace bytes that no other running call uses; None allocates one."""
+    n = len(xs)
+    dt, wt, cols = _norm_types(xs, (gammas, dgammas, dbetas))
+    rows, xs_stride = _row_views("input", xs, n, cols, dt)
+    _, dys_stride = _row_views("output gradient", dys, n, cols, dt, rows)
+    dxs_stride = cols if dxs is None else _row_views("input gradient", dxs, n, cols, dt, rows)[1]
+    _flat_bufs("mean", means, n, rows, torch.float32)
+    _flat_bufs("rstd", rstds, n, rows, torch.float32)
+    seen = list(xs) + list(dys) + list(means) + list(rstds) + (list(dxs) if dxs is not None else [])
+    for what, w in (("gamma", gammas), ("gamma gradient", dgammas), ("beta gradient", dbetas)):
+        if w is not None:
+            _flat_bufs(what, w, n, [cols] * n, wt)
+            seen += w
+    _on_device(seen)
+    need, ws = 0, None
+    if dgammas is not None or dbetas is not None:
+        need = arLayerNormBackwardWorkspace(rows, cols)
+        if workspace is None:
+            workspace = _workspace(need, stream)
+        _on_device((workspace,))
+        _check_workspace(workspace, need)
+        ws = workspace.data_ptr()
+    _check(lib().arLayerNormBackward(_arr(dys), _arr(xs), _arr(gammas), _arr(means), _arr(rstds), _arr(dxs),
+                                     _arr(dgammas), _arr(dbetas), (ctypes.c_size_t * n)(*rows), n, cols, dys_stride,
+                                     xs_stride, dxs_stride, _FLOAT_DTYPES[dt], _FLOAT_DTYPES[wt], ws, need,
+                                     ctypes.c_void_p(_stream_handle(stream))), "arLayerNormBackward")
+
+
+def arTensorListCreate(srcs, dsts=None):
+    """A list handle over contiguous device tensors; dsts: where arGradClip writes (srcs itself: in place)."""
+    n = len(srcs)
+    if dsts is not None and len(dsts) != n:
+        raise ValueError("need %d outputs, got %d" % (n, len(dsts)))
+    dtypes = []
+    for i, t in enumerate(srcs):
+        if t.dtype not in _FLOAT_DTYPES:
+            raise ValueError("tensor %d is %s" % (i, t.dtype))
+        dtypes.append(_FLOAT_DTYPES[t.dtype])
+        for what, q in (("tensor", t),) + ((("output", dsts[i]),) if dsts is not None else ()):
+            if not q.is_contiguous() or q.dtype != t.dtype or q.numel() != t.numel():
+                raise ValueError("%s %d must hold %d contiguous elements of %s" % (what, i, t.numel(), t.dtype))
+    _on_device(srcs)
+    _on_device(dsts or ())
+    h = ctypes.c_void_p()
+    _check(lib().arTensorListCreate(ctypes.byref(h), n, _arr(srcs), _arr(dsts),
+                                    (ctypes.c_size_t * n)(*[t.numel() for t in srcs]), (ctypes.c_int * n)(*dtypes)),
+           "arTensorListCreate")
+    return h
+
+
+def arTensorListWorkspace(handle):
+    b = ctypes.c_size_t()
+    _check(lib().arTensorListWorkspace(handle, ctypes.byref(b)), "arTensorListWorkspace")
+    return b.value
+
+
+def arTensorListDestroy(handle):
+    _check(lib().arTensorListDestroy(handle), "arTensorListDestroy")
+
+
+class TensorList:
+    """Owns one list handle and keeps its tensors alive.  Work that uses the list must have been enqueued before
+    it is closed; closing waits for the device."""
+
+    def __init__(self, srcs, dsts=None):
+        self.handle = None
+        self.tensors = (list(srcs), None if dsts is None else list(dsts))
+        self.handle = arTensorListCreate(*self.tensors)
+        self.workspace_bytes = arTensorListWorkspace(self.handle)
+
+    def workspace(self):
+        """Bytes of workspace a call on this list needs."""
+        return self.workspace_bytes
+
+    def close(self):
+        if self.handle is not None:
+            arTensorListDestroy(self.handle)
+            self.handle = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _norm_call_args(lst, kind, norm, workspace, stream):
+    if not isinstance(lst, TensorList) or lst.handle is None:
+        raise ValueError("need an open TensorList")
+    if norm is not None:
+        if norm.dtype != torch.float32 or norm.numel() != 1:
+            raise ValueError("norm must be a float32 tensor of one element")
+        _on_device((norm,))
+    if workspace is None:
+        workspace = _workspace(lst.workspace_bytes, stream)
+    else:
+        _on_device((workspace,))
+        _check_workspace(workspace, lst.workspace_bytes)
+    return (NORM_BY_NAME[kind] if isinstance(kind, str) else int(kind), None if norm is None else norm.data_ptr(),
+            workspace.data_ptr(), ctypes.c_void_p(_stream_handle(stream)))
+
+
+def arGradNorm(lst, norm, kind=arNorm2, scale=1.0, workspace=None, stream=None):
+    """norm (float32, one element) = |scale| * the norm over every element of the TensorList's tensors.
+    workspace: a device tensor of lst.workspace() bytes that no other running call uses; None allocates one."""
+    k, p, w, s = _norm_call_args(lst, kind, norm, workspace, stream)
+    _check(lib().arGradNorm(lst.handle, k, float(scale), p, w, lst.workspace_bytes, s), "arGradNorm")
+
+
+def arGradClip(lst, norm, maxNorm, eps=1e-6, kind=arNorm2, scale=1.0, workspace=None, stream=None):
+    """The norm, and every tensor times scale * min(1, maxNorm / (norm + eps)) into the list's outputs.  norm may
+    be None."""
+    k, p, w, s = _norm_call_args(lst, kind, norm, workspace, stream)
+    _check(lib().arGradClip(lst.handle, k, float(scale), float(maxNorm), float(eps), p, w, lst.workspace_bytes, s),
+           "arGradClip")
 
 
 class Comm:

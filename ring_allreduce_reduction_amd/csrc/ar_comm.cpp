@@ -17,21 +17,9 @@
 #include <new>
 #include <vector>
 
-#include <rocprofiler-sdk-roctx/roctx.h>
-
+#include "ar_api.h"
 #include "ar_internal.h"
 #include "ar_tune_table.h"
-
-// A ROCTx range around an API call, as the pages mark each API entry with an
-// NVTX range ["NCCL 原始碼解讀：一個 AllReduce 的 GPU 旅程", ch.3 §3.1, ch.6, the
-// ncclAllReduce call chain]: rocprofv3 --marker-trace records one per call
-// (host time of the call: argument checks, planning and the enqueue).
-struct ApiRange {
-  explicit ApiRange(const char* name) { roctxRangePushA(name); }
-  ~ApiRange() { roctxRangePop(); }
-  ApiRange(const ApiRange&) = delete;
-  ApiRange& operator=(const ApiRange&) = delete;
-};
 
 using namespace ar;
 
@@ -1683,12 +1671,14 @@ arResult_t launchGroup(arComm* c) {
 }
 }  // namespace
 
-extern "C" {
+bool ar::groupOpen() { return tGroupDepth > 0; }
 
-static arResult_t noteGroupError(arResult_t r) {
+arResult_t ar::noteGroupError(arResult_t r) {
   if (r != arSuccess && tGroupDepth > 0 && tGroupError == arSuccess) tGroupError = r;
   return r;
 }
+
+extern "C" {
 
 arResult_t arAllReduce(arComm_t c, const void* const* sendbufs, void* const* recvbufs, size_t count,
                        arDataType_t dtype, arRedOp_t op, void* stream) {
