@@ -46,16 +46,30 @@ struct NormArgs {
   int nSpans;
 };
 
+// A thread's running value.  Squares add up in 64 bits: a product of two
+// floats is exact there, and no square overflows or vanishes.  The largest
+// absolute value is kept as its bits, which order as the values do with
+// infinity above all numbers and NaN above infinity.
+template <int KIND> struct Running;
+template <> struct Running<arNorm2> {
+  typedef double type;
+  static __device__ __forceinline__ double add(double acc, float g) { return fma((double)g, (double)g, acc); }
+  static __device__ __forceinline__ double join(double a, double b) { return a + b; }
+  static __device__ __forceinline__ double value(double a) { return a; }
+};
+template <> struct Running<arNormMax> {
+  typedef uint32_t type;
+  static __device__ __forceinline__ uint32_t add(uint32_t acc, float g) {
+    return max(acc, __float_as_uint(g) & 0x7fffffffu);
+  }
+  static __device__ __forceinline__ uint32_t join(uint32_t a, uint32_t b) { return max(a, b); }
+  static __device__ __forceinline__ double value(uint32_t a) { return (double)__uint_as_float(a); }
+};
+
 template <int KIND>
 __device__ __forceinline__ double join(double a, double b) {
   if (KIND == arNorm2) return a + b;
   return b > a || b != b ? b : a;      // a NaN stays
-}
-
-template <int KIND>
-__device__ __forceinline__ double add(double acc, float g) {
-  const double d = (double)g;
-  return KIND == arNorm2 ? fma(d, d, acc) : join<KIND>(acc, fabs(d));
 }
 
 // Combines one value per thread, in a fixed order; every thread receives it.
@@ -71,26 +85,47 @@ __device__ __forceinline__ double blockJoin(double v, double* lds) {
   return s;
 }
 
+// Four 16-byte loads a thread in flight; element e of every vector adds to
+// sum e % 4, so that four chains of additions run side by side.
 template <int KIND, int DT>
-__device__ __forceinline__ double addSegment(double acc, const Segment& g) {
-  const typename Elem<DT>::type* p = (const typename Elem<DT>::type*)g.src;
-  for (int64_t i = threadIdx.x; i < g.count; i += kNormBlock) acc = add<KIND>(acc, (float)p[i]);
-  return acc;
+__device__ __forceinline__ void addSegment(typename Running<KIND>::type (&acc)[4], const Segment& g) {
+  typedef typename Elem<DT>::type T;
+  constexpr int V = kVec<DT>, UN = 4;
+  const T* p = (const T*)g.src;
+  const int64_t nv = g.count / V;
+  int64_t i = threadIdx.x;
+  for (; i + (UN - 1) * kNormBlock < nv; i += UN * kNormBlock) {
+    typename VecOf<T, V>::type x[UN];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) x[u] = loadVec<T, V>(p + (i + u * kNormBlock) * V);
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e % 4] = Running<KIND>::add(acc[e % 4], (float)x[u][e]);
+  }
+  for (; i < nv; i += kNormBlock) {
+    const typename VecOf<T, V>::type x = loadVec<T, V>(p + i * V);
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e % 4] = Running<KIND>::add(acc[e % 4], (float)x[e]);
+  }
+  i = nv * V + threadIdx.x;
+  if (i < g.count) acc[0] = Running<KIND>::add(acc[0], (float)p[i]);
 }
 
 template <int KIND>
 __global__ void __launch_bounds__(kNormBlock) normSpans(const NormArgs a) {
   __shared__ double lds[kNormBlock / 64];
-  double acc = 0.0;
+  typedef Running<KIND> R;
+  typename R::type acc[4] = {0, 0, 0, 0};
   const int end = a.first[blockIdx.x + 1];
   for (int s = a.first[blockIdx.x]; s < end; ++s) {
     const Segment g = a.segments[s];
-    if (g.dtype == arFloat32) acc = addSegment<KIND, arFloat32>(acc, g);
-    else if (g.dtype == arFloat16) acc = addSegment<KIND, arFloat16>(acc, g);
-    else acc = addSegment<KIND, arBfloat16>(acc, g);
+    if (g.dtype == arFloat32) addSegment<KIND, arFloat32>(acc, g);
+    else if (g.dtype == arFloat16) addSegment<KIND, arFloat16>(acc, g);
+    else addSegment<KIND, arBfloat16>(acc, g);
   }
-  acc = blockJoin<KIND>(acc, lds);
-  if (threadIdx.x == 0) a.partial[blockIdx.x] = acc;
+  const double all = blockJoin<KIND>(R::value(R::join(R::join(acc[0], acc[1]), R::join(acc[2], acc[3]))), lds);
+  if (threadIdx.x == 0) a.partial[blockIdx.x] = all;
 }
 
 // The norm from the partials, the same in every workgroup that asks.
@@ -112,9 +147,26 @@ __global__ void __launch_bounds__(kNormBlock) normFinish(const NormArgs a) {
 template <int DT>
 __device__ __forceinline__ void scaleSegment(const Segment& g, float f) {
   typedef typename Elem<DT>::type T;
+  constexpr int V = kVec<DT>, UN = 4;
+  typedef typename VecOf<T, V>::type Vec;
   const T* p = (const T*)g.src;
   T* q = (T*)g.dst;
-  for (int64_t i = threadIdx.x; i < g.count; i += kNormBlock) q[i] = (T)((float)p[i] * f);
+  const int64_t nv = g.count / V;
+  int64_t i = threadIdx.x;
+  for (; i + (UN - 1) * kNormBlock < nv; i += UN * kNormBlock) {
+    Vec x[UN];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) x[u] = loadVec<T, V>(p + (i + u * kNormBlock) * V);
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+      storeVec<T, V>(q + (i + u * kNormBlock) * V,
+                     __builtin_convertvector(__builtin_convertvector(x[u], FloatVec<V>) * f, Vec));
+  }
+  for (; i < nv; i += kNormBlock)
+    storeVec<T, V>(q + i * V,
+                   __builtin_convertvector(__builtin_convertvector(loadVec<T, V>(p + i * V), FloatVec<V>) * f, Vec));
+  i = nv * V + threadIdx.x;
+  if (i < g.count) q[i] = (T)((float)p[i] * f);
 }
 
 template <int KIND>
@@ -124,8 +176,10 @@ __global__ void __launch_bounds__(kNormBlock) clipSpans(const NormArgs a) {
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.norm != nullptr) a.norm[0] = (float)n;
   const double c = n + a.eps <= a.maxNorm ? 1.0 : a.maxNorm / (n + a.eps);
   const float f = (float)(a.scale * c);
-  const int end = a.first[blockIdx.x + 1];
-  for (int s = a.first[blockIdx.x]; s < end; ++s) {
+  // from the last span back: what the norm read last is what the caches still hold
+  const int span = a.nSpans - 1 - (int)blockIdx.x;
+  const int end = a.first[span + 1];
+  for (int s = a.first[span]; s < end; ++s) {
     const Segment g = a.segments[s];
     if (f == 1.0f && g.src == g.dst) continue;   // nothing would change
     if (g.dtype == arFloat32) scaleSegment<arFloat32>(g, f);

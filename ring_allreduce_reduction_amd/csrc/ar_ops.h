@@ -19,6 +19,30 @@ template <> struct Elem<arBfloat16> { typedef __bf16 type; };
 
 inline bool opsFloatType(int dtype) { return dtype == arFloat32 || dtype == arFloat16 || dtype == arBfloat16; }
 
+// 16 bytes of elements.  Only element alignment is assumed: global memory
+// takes 16-byte accesses at any element address here, so rows of odd width
+// and views at odd offsets use the same loads as aligned ones.
+template <int DT> constexpr int kVec = 16 / (int)sizeof(typename Elem<DT>::type);
+
+template <typename T, int V>
+struct VecOf {
+  typedef T type __attribute__((ext_vector_type(V)));
+  typedef T packed __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+};
+
+template <int V>
+using FloatVec = float __attribute__((ext_vector_type(V)));
+
+template <typename T, int V>
+__device__ __forceinline__ typename VecOf<T, V>::type loadVec(const T* p) {
+  return *(const typename VecOf<T, V>::packed*)p;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void storeVec(T* p, typename VecOf<T, V>::type v) {
+  *(typename VecOf<T, V>::packed*)p = v;
+}
+
 // Sum over a wavefront; every lane receives it.  A butterfly: each of the 64
 // lanes adds the same pairs, so the order is fixed.
 __device__ __forceinline__ float waveSum(float v) {
