@@ -596,8 +596,8 @@ typedef struct arTensorList* arTensorList_t;
 /*
  * arTensorListCreate -- lay a list of tensors out for arGradNorm and
  * arGradClip on the current device: all of a model's gradients, or all ranks'
- * shards of them after a ReduceScatter.  The work is cut into spans of about
- * equal bytes, so a list of many small tensors and a few large ones keeps the
+ * shards of them after a ReduceScatter.  The tensors are cut into tiles of at
+ * most 32 KiB, so a list of many small tensors and a few large ones keeps the
  * whole GPU busy.
  *  list      (host, out) receives the handle.
  *  nTensors  0..2^20.
@@ -610,7 +610,7 @@ typedef struct arTensorList* arTensorList_t;
  *            the list is only for arGradNorm.
  * The arrays are copied; the tensors themselves are the caller's and must stay
  * where they are while the list is used.  Allocates device memory (32 bytes a
- * tensor or span) and copies to it synchronously: not for capture.
+ * tile) and copies to it synchronously: not for capture.
  * Errors: arInvalidArgument (bad pointers, counts, types; outputs that
  * overlap), arHipError, arSystemError.
  */

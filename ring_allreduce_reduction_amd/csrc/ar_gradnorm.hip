@@ -2,8 +2,8 @@
 //
 //   norm = |s| sqrt(sum g^2)  or  |s| max |g|,   out = g (s min(1, M / (norm + eps))).
 //
-// The list is cut into spans of about equal cost, one workgroup each.  The
-// first kernel leaves one partial per span; what follows combines the
+// The list is cut into tiles; workgroup b takes tiles b, b + grid, ...  The
+// first kernel leaves one partial per workgroup; what follows combines the
 // partials in a fixed order.
 #include <math.h>
 #include <string.h>
@@ -20,30 +20,55 @@
 namespace ar {
 namespace {
 
+// Bound by memory: 2 flops a value for the norm, 3 to scale it.  The factor
+// depends on every value, so a list past the caches is read twice.
 constexpr int kNormBlock = 256;
-constexpr int kMaxSpans = 8 * kOpsCUs;
-constexpr size_t kSpanBytes = 16 * 1024;      // a span's cost at least
-constexpr size_t kSegmentCost = 2 * 1024;     // what a segment costs beside its bytes
+// Tiles of 32 KiB, two workgroups a CU: the workgroups sweep the list as one
+// window that moves through memory.  8 x 256 MiB fp32: 315 us (6.8 TB/s; a
+// bare read of as much runs at 7.1); 4 workgroups a CU 324, 8 334; one
+// contiguous span a workgroup instead of tiles 319-380 by the count, one a
+// wavefront 348; cached instead of non-temporal loads 370.
+constexpr int kNormGrid = 2 * kOpsCUs;
+constexpr size_t kTileMax = 32 * 1024;
+// Short lists take shorter tiles, down to one 16-byte vector a thread, so that
+// every workgroup still has at least eight or the list is all in flight at once.
+constexpr size_t kTileMin = 4096;
+constexpr int kTilesEach = 8;
+// The second pass writes as much as it reads and likes more workgroups: 8 x
+// 128 MiB bf16 norm and clip 513 us with 16 a CU, 532 with 8, 550 with 4.
+constexpr int kClipGrid = 16 * kOpsCUs;
+// What the norm reads last it reads through the caches, and the second pass
+// begins there: 453 MB fp16 220-235 us against 262 all non-temporal, 246 all
+// cached; 128, 192, 256 and 384 MB kept 239, 234, 235, 240.
+constexpr size_t kKeepBytes = (size_t)224 << 20;
+// Lists of few tiles run in one workgroup and one launch.  Called back to back
+// from the host a launch less saves 3 us (8.6 -> 5.5); replayed from a graph
+// the norm of 16, 64, 128 tiles takes 3.1, 4.7, 7.0 us against 4.4 in two
+// launches, norm and clip of 8, 16, 32 tiles 4.2, 5.4, 7.6 against 5.3.
+constexpr int kSmallBlock = 1024;
+constexpr int kSmallNormTiles = 64;
+constexpr int kSmallClipTiles = 16;
 
-// A piece of one tensor inside one span.
-struct Segment {
+// A piece of one tensor.
+struct Tile {
   const void* src;
   void* dst;
-  int64_t count;
+  int count;
   int dtype;
-  int pad;
+  int64_t pad;
 };
-static_assert(sizeof(Segment) == 32, "Segment layout");
+static_assert(sizeof(Tile) == 32, "Tile layout");
 
 constexpr uint64_t kListMagic = 0x41524c4953543031ull;   // "ARLIST01"
 
 struct NormArgs {
-  const Segment* segments;
-  const int* first;        // span s has segments [first[s], first[s + 1])
-  double* partial;         // one per span
+  const Tile* tiles;
+  double* partial;         // one per workgroup of normTiles
   float* norm;             // may be null when clipping
   double scale, maxNorm, eps;
-  int nSpans;
+  int nTiles;
+  int nPartial;
+  int keepFrom;            // tiles from here on are read again soon: through the caches
 };
 
 // A thread's running value.  Squares add up in 64 bits: a product of two
@@ -85,46 +110,66 @@ __device__ __forceinline__ double blockJoin(double v, double* lds) {
   return s;
 }
 
-// Four 16-byte loads a thread in flight; element e of every vector adds to
-// sum e % 4, so that four chains of additions run side by side.
-template <int KIND, int DT>
-__device__ __forceinline__ void addSegment(typename Running<KIND>::type (&acc)[4], const Segment& g) {
+// GROUP threads (a workgroup or a wavefront) add a tile: UN 16-byte loads a thread in flight; element e of
+// every vector adds to sum e % 4, so that four chains of additions run side
+// by side.
+template <int KIND, int DT, bool KEEP, int GROUP>
+__device__ __forceinline__ void addTile(typename Running<KIND>::type (&acc)[4], const Tile& g) {
   typedef typename Elem<DT>::type T;
   constexpr int V = kVec<DT>, UN = 4;
   const T* p = (const T*)g.src;
-  const int64_t nv = g.count / V;
-  int64_t i = threadIdx.x;
-  for (; i + (UN - 1) * kNormBlock < nv; i += UN * kNormBlock) {
+  const int nv = g.count / V;
+  int i = threadIdx.x % GROUP;
+  for (; i + (UN - 1) * GROUP < nv; i += UN * GROUP) {
     typename VecOf<T, V>::type x[UN];
 #pragma unroll
-    for (int u = 0; u < UN; ++u) x[u] = loadVec<T, V>(p + (i + u * kNormBlock) * V);
+    for (int u = 0; u < UN; ++u) {
+      const T* q = p + (i + u * GROUP) * V;
+      x[u] = KEEP ? loadVec<T, V>(q) : loadStream<T, V>(q);
+    }
 #pragma unroll
     for (int u = 0; u < UN; ++u)
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[e % 4] = Running<KIND>::add(acc[e % 4], (float)x[u][e]);
   }
-  for (; i < nv; i += kNormBlock) {
+  for (; i < nv; i += GROUP) {
     const typename VecOf<T, V>::type x = loadVec<T, V>(p + i * V);
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e % 4] = Running<KIND>::add(acc[e % 4], (float)x[e]);
   }
-  i = nv * V + threadIdx.x;
+  i = nv * V + threadIdx.x % GROUP;
   if (i < g.count) acc[0] = Running<KIND>::add(acc[0], (float)p[i]);
 }
 
+template <int KIND, bool KEEP, int GROUP>
+__device__ __forceinline__ void addTyped(typename Running<KIND>::type (&acc)[4], const Tile& g) {
+  if (g.dtype == arFloat32) addTile<KIND, arFloat32, KEEP, GROUP>(acc, g);
+  else if (g.dtype == arFloat16) addTile<KIND, arFloat16, KEEP, GROUP>(acc, g);
+  else addTile<KIND, arBfloat16, KEEP, GROUP>(acc, g);
+}
+
+// Combines a thread's four sums over the workgroup.
 template <int KIND>
-__global__ void __launch_bounds__(kNormBlock) normSpans(const NormArgs a) {
-  __shared__ double lds[kNormBlock / 64];
+__device__ __forceinline__ double joinAll(const typename Running<KIND>::type (&acc)[4], double* lds) {
   typedef Running<KIND> R;
-  typename R::type acc[4] = {0, 0, 0, 0};
-  const int end = a.first[blockIdx.x + 1];
-  for (int s = a.first[blockIdx.x]; s < end; ++s) {
-    const Segment g = a.segments[s];
-    if (g.dtype == arFloat32) addSegment<KIND, arFloat32>(acc, g);
-    else if (g.dtype == arFloat16) addSegment<KIND, arFloat16>(acc, g);
-    else addSegment<KIND, arBfloat16>(acc, g);
+  return blockJoin<KIND>(R::value(R::join(R::join(acc[0], acc[1]), R::join(acc[2], acc[3]))), lds);
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(kNormBlock) normTiles(const NormArgs a) {
+  __shared__ double lds[kNormBlock / kWave];
+  typename Running<KIND>::type acc[4] = {0, 0, 0, 0};
+  int t = blockIdx.x;
+  Tile g = a.tiles[t];
+  while (t < a.nTiles) {
+    const int next = t + (int)gridDim.x;
+    const Tile ahead = a.tiles[next < a.nTiles ? next : t];
+    if (t < a.keepFrom) addTyped<KIND, false, kNormBlock>(acc, g);
+    else addTyped<KIND, true, kNormBlock>(acc, g);
+    g = ahead;
+    t = next;
   }
-  const double all = blockJoin<KIND>(R::value(R::join(R::join(acc[0], acc[1]), R::join(acc[2], acc[3]))), lds);
+  const double all = joinAll<KIND>(acc, lds);
   if (threadIdx.x == 0) a.partial[blockIdx.x] = all;
 }
 
@@ -132,60 +177,88 @@ __global__ void __launch_bounds__(kNormBlock) normSpans(const NormArgs a) {
 template <int KIND>
 __device__ __forceinline__ double normOf(const NormArgs& a, double* lds) {
   double acc = 0.0;
-  for (int s = threadIdx.x; s < a.nSpans; s += kNormBlock) acc = join<KIND>(acc, a.partial[s]);
+  for (int s = threadIdx.x; s < a.nPartial; s += kNormBlock) acc = join<KIND>(acc, a.partial[s]);
   acc = blockJoin<KIND>(acc, lds);
   return fabs(a.scale) * (KIND == arNorm2 ? sqrt(acc) : acc);
 }
 
 template <int KIND>
 __global__ void __launch_bounds__(kNormBlock) normFinish(const NormArgs a) {
-  __shared__ double lds[kNormBlock / 64];
+  __shared__ double lds[kNormBlock / kWave];
   const double n = normOf<KIND>(a, lds);
   if (threadIdx.x == 0) a.norm[0] = (float)n;
 }
 
-template <int DT>
-__device__ __forceinline__ void scaleSegment(const Segment& g, float f) {
+template <int DT, int GROUP>
+__device__ __forceinline__ void scaleTile(const Tile& g, float f) {
   typedef typename Elem<DT>::type T;
   constexpr int V = kVec<DT>, UN = 4;
   typedef typename VecOf<T, V>::type Vec;
   const T* p = (const T*)g.src;
   T* q = (T*)g.dst;
-  const int64_t nv = g.count / V;
-  int64_t i = threadIdx.x;
-  for (; i + (UN - 1) * kNormBlock < nv; i += UN * kNormBlock) {
+  const int nv = g.count / V;
+  int i = threadIdx.x % GROUP;
+  for (; i + (UN - 1) * GROUP < nv; i += UN * GROUP) {
     Vec x[UN];
 #pragma unroll
-    for (int u = 0; u < UN; ++u) x[u] = loadVec<T, V>(p + (i + u * kNormBlock) * V);
+    for (int u = 0; u < UN; ++u) x[u] = loadStream<T, V>(p + (i + u * GROUP) * V);
 #pragma unroll
     for (int u = 0; u < UN; ++u)
-      storeVec<T, V>(q + (i + u * kNormBlock) * V,
-                     __builtin_convertvector(__builtin_convertvector(x[u], FloatVec<V>) * f, Vec));
+      storeStream<T, V>(q + (i + u * GROUP) * V,
+                        __builtin_convertvector(__builtin_convertvector(x[u], FloatVec<V>) * f, Vec));
   }
-  for (; i < nv; i += kNormBlock)
-    storeVec<T, V>(q + i * V,
-                   __builtin_convertvector(__builtin_convertvector(loadVec<T, V>(p + i * V), FloatVec<V>) * f, Vec));
-  i = nv * V + threadIdx.x;
+  for (; i < nv; i += GROUP)
+    storeStream<T, V>(q + i * V, __builtin_convertvector(
+                                     __builtin_convertvector(loadStream<T, V>(p + i * V), FloatVec<V>) * f, Vec));
+  i = nv * V + threadIdx.x % GROUP;
   if (i < g.count) q[i] = (T)((float)p[i] * f);
 }
 
+template <int GROUP>
+__device__ __forceinline__ void scaleTyped(const Tile& g, float f) {
+  if (f == 1.0f && g.src == g.dst) return;   // nothing would change
+  if (g.dtype == arFloat32) scaleTile<arFloat32, GROUP>(g, f);
+  else if (g.dtype == arFloat16) scaleTile<arFloat16, GROUP>(g, f);
+  else scaleTile<arBfloat16, GROUP>(g, f);
+}
+
+// The factor of every value, from the norm: 64 bits, rounded once.
+__device__ __forceinline__ float clipFactor(const NormArgs& a, double norm) {
+  const double c = norm + a.eps <= a.maxNorm ? 1.0 : a.maxNorm / (norm + a.eps);
+  return (float)(a.scale * c);
+}
+
 template <int KIND>
-__global__ void __launch_bounds__(kNormBlock) clipSpans(const NormArgs a) {
-  __shared__ double lds[kNormBlock / 64];
+__global__ void __launch_bounds__(kNormBlock) clipTiles(const NormArgs a) {
+  __shared__ double lds[kNormBlock / kWave];
   const double n = normOf<KIND>(a, lds);
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.norm != nullptr) a.norm[0] = (float)n;
-  const double c = n + a.eps <= a.maxNorm ? 1.0 : a.maxNorm / (n + a.eps);
-  const float f = (float)(a.scale * c);
-  // from the last span back: what the norm read last is what the caches still hold
-  const int span = a.nSpans - 1 - (int)blockIdx.x;
-  const int end = a.first[span + 1];
-  for (int s = a.first[span]; s < end; ++s) {
-    const Segment g = a.segments[s];
-    if (f == 1.0f && g.src == g.dst) continue;   // nothing would change
-    if (g.dtype == arFloat32) scaleSegment<arFloat32>(g, f);
-    else if (g.dtype == arFloat16) scaleSegment<arFloat16>(g, f);
-    else scaleSegment<arBfloat16>(g, f);
+  const float f = clipFactor(a, n);
+  // from the last tile back: what the norm read last is what the caches still hold
+  int t = a.nTiles - 1 - (int)blockIdx.x;
+  Tile g = a.tiles[t];
+  while (t >= 0) {
+    const int next = t - (int)gridDim.x;
+    const Tile ahead = a.tiles[next >= 0 ? next : t];
+    scaleTyped<kNormBlock>(g, f);
+    g = ahead;
+    t = next;
   }
+}
+
+// The whole of a short list in one workgroup: its wavefronts take tiles in turn.
+template <int KIND, bool CLIP>
+__global__ void __launch_bounds__(kSmallBlock) smallList(const NormArgs a) {
+  __shared__ double lds[kSmallBlock / kWave];
+  typename Running<KIND>::type acc[4] = {0, 0, 0, 0};
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
+  for (int t = wave; t < a.nTiles; t += kSmallBlock / kWave) addTyped<KIND, true, kWave>(acc, a.tiles[t]);
+  const double all = joinAll<KIND>(acc, lds);
+  const double n = fabs(a.scale) * (KIND == arNorm2 ? sqrt(all) : all);
+  if (threadIdx.x == 0 && a.norm != nullptr) a.norm[0] = (float)n;
+  if (!CLIP) return;
+  const float f = clipFactor(a, n);
+  for (int t = wave; t < a.nTiles; t += kSmallBlock / kWave) scaleTyped<kWave>(a.tiles[t], f);
 }
 
 }  // namespace
@@ -194,10 +267,10 @@ __global__ void __launch_bounds__(kNormBlock) clipSpans(const NormArgs a) {
 struct arTensorList {
   uint64_t magic;
   int device;
-  int nSpans;
+  int nTiles;
+  int keepFrom;              // the first tile of the last kKeepBytes
   bool outputs;
-  char* table;               // device: nSpans + 1 ints, then the segments
-  const ar::Segment* segments;
+  ar::Tile* tiles;           // device
 };
 
 namespace ar {
@@ -205,42 +278,23 @@ namespace {
 
 bool listOk(const arTensorList* l) { return l != nullptr && (uintptr_t)l % 8 == 0 && l->magic == kListMagic; }
 
-// Cuts the tensors into spans: walks them in order and closes a span once its
-// cost (bytes, and kSegmentCost a segment) reaches the target, a tensor larger
-// than what is left of the span split there at a 4 KiB grain of its own bytes.
-void cutSpans(int nTensors, const void* const* src, void* const* dst, const size_t* counts,
-              const arDataType_t* dtypes, std::vector<Segment>& segments, std::vector<int>& first) {
-  double cost = 0.0;
-  for (int i = 0; i < nTensors; ++i)
-    if (counts[i] > 0) cost += (double)counts[i] * elemSize(dtypes[i]) + kSegmentCost;
-  size_t target = (size_t)(cost / kMaxSpans) + 1;
-  if (target < kSpanBytes) target = kSpanBytes;
-  constexpr size_t grain = 4096;
-  target = (target + grain - 1) / grain * grain + grain;
-  first.push_back(0);
-  size_t room = target;
+void cutTiles(int nTensors, const void* const* src, void* const* dst, const size_t* counts,
+              const arDataType_t* dtypes, std::vector<Tile>& tiles) {
+  double bytes = 0.0;
+  for (int i = 0; i < nTensors; ++i) bytes += (double)counts[i] * elemSize(dtypes[i]);
+  size_t tile = kTileMin;
+  while (tile < kTileMax && (double)tile * kTilesEach * kNormGrid < bytes) tile *= 2;
   for (int i = 0; i < nTensors; ++i) {
     const size_t esz = (size_t)elemSize(dtypes[i]);
-    size_t done = 0;
-    while (done < counts[i]) {
-      if (room < kSegmentCost + grain) {
-        first.push_back((int)segments.size());
-        room = target;
-      }
-      const size_t can = (room - kSegmentCost) / grain * grain / esz;
-      const size_t n = counts[i] - done < can ? counts[i] - done : can;
-      Segment g{};
+    for (size_t done = 0; done < counts[i]; done += tile / esz) {
+      Tile g{};
       g.src = (const char*)src[i] + done * esz;
       g.dst = dst != nullptr ? (char*)dst[i] + done * esz : nullptr;
-      g.count = (int64_t)n;
+      g.count = (int)(counts[i] - done < tile / esz ? counts[i] - done : tile / esz);
       g.dtype = dtypes[i];
-      segments.push_back(g);
-      const size_t used = n * esz + kSegmentCost;
-      room = room > used ? room - used : 0;
-      done += n;
+      tiles.push_back(g);
     }
   }
-  if ((int)segments.size() > first.back()) first.push_back((int)segments.size());
 }
 
 arResult_t createList(arTensorList_t* out, int nTensors, const void* const* src, void* const* dst,
@@ -262,9 +316,9 @@ arResult_t createList(arTensorList_t* out, int nTensors, const void* const* src,
     v.push_back(Extent{(uintptr_t)dst[i], bytes, 1, bytes, true, i});
   }
   if (dst != nullptr && outputsOverlap(v)) return arInvalidArgument;
-  std::vector<Segment> segments;
-  std::vector<int> first;
-  cutSpans(nTensors, src, dst, counts, dtypes, segments, first);
+  std::vector<Tile> tiles;
+  cutTiles(nTensors, src, dst, counts, dtypes, tiles);
+  if (tiles.size() > (size_t)1 << 30) return arInvalidArgument;
 
   int dev = 0, ndev = 0;
   if (hipGetDeviceCount(&ndev) != hipSuccess || ndev < 1) return arHipError;
@@ -272,45 +326,48 @@ arResult_t createList(arTensorList_t* out, int nTensors, const void* const* src,
   arTensorList* l = new (std::nothrow) arTensorList();
   if (l == nullptr) return arSystemError;
   l->device = dev;
-  l->nSpans = (int)first.size() - 1;
+  l->nTiles = (int)tiles.size();
   l->outputs = dst != nullptr;
-  const size_t head = (first.size() * sizeof(int) + 31) / 32 * 32;
-  std::vector<char> table;
-  try {
-    table.assign(head + segments.size() * sizeof(Segment), 0);
-  } catch (...) {
-    delete l;
-    throw;
+  l->keepFrom = l->nTiles;
+  for (size_t kept = 0; l->keepFrom > 0; --l->keepFrom) {
+    const Tile& g = tiles[(size_t)l->keepFrom - 1];
+    kept += (size_t)g.count * (size_t)elemSize(g.dtype);
+    if (kept > kKeepBytes) break;
   }
-  memcpy(table.data(), first.data(), first.size() * sizeof(int));
-  if (!segments.empty()) memcpy(table.data() + head, segments.data(), segments.size() * sizeof(Segment));
-  if (hipMalloc((void**)&l->table, table.size()) != hipSuccess) {
-    delete l;
-    return arHipError;
+  if (l->nTiles > 0) {
+    const size_t bytes = tiles.size() * sizeof(Tile);
+    if (hipMalloc((void**)&l->tiles, bytes) != hipSuccess) {
+      delete l;
+      return arHipError;
+    }
+    if (hipMemcpy(l->tiles, tiles.data(), bytes, hipMemcpyHostToDevice) != hipSuccess) {
+      (void)hipFree(l->tiles);
+      delete l;
+      return arHipError;
+    }
   }
-  if (hipMemcpy(l->table, table.data(), table.size(), hipMemcpyHostToDevice) != hipSuccess) {
-    (void)hipFree(l->table);
-    delete l;
-    return arHipError;
-  }
-  l->segments = (const Segment*)(l->table + head);
   l->magic = kListMagic;
   *out = l;
   return arSuccess;
 }
 
+int gridOf(const arTensorList* l) { return l->nTiles < kNormGrid ? l->nTiles : kNormGrid; }
+
 size_t listWorkspace(const arTensorList* l) {
-  return ((size_t)(l->nSpans > 0 ? l->nSpans : 1) * sizeof(double) + 15) / 16 * 16;
+  return ((size_t)(l->nTiles > 0 ? gridOf(l) : 1) * sizeof(double) + 15) / 16 * 16;
 }
 
 template <int KIND>
 hipError_t launchNorm(const NormArgs& a, bool clip, hipStream_t st) {
-  if (a.nSpans > 0) hipLaunchKernelGGL(normSpans<KIND>, dim3(a.nSpans), dim3(kNormBlock), 0, st, a);
-  if (!clip)
-    hipLaunchKernelGGL(normFinish<KIND>, dim3(1), dim3(kNormBlock), 0, st, a);
-  else if (a.nSpans > 0)
-    hipLaunchKernelGGL(clipSpans<KIND>, dim3(a.nSpans), dim3(kNormBlock), 0, st, a);
-  else if (a.norm != nullptr)
+  if (a.nTiles <= (clip ? kSmallClipTiles : kSmallNormTiles)) {   // an empty list too: its norm is 0
+    if (clip) hipLaunchKernelGGL((smallList<KIND, true>), dim3(1), dim3(kSmallBlock), 0, st, a);
+    else hipLaunchKernelGGL((smallList<KIND, false>), dim3(1), dim3(kSmallBlock), 0, st, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(normTiles<KIND>, dim3(a.nPartial), dim3(kNormBlock), 0, st, a);
+  if (clip)
+    hipLaunchKernelGGL(clipTiles<KIND>, dim3(a.nTiles < kClipGrid ? a.nTiles : kClipGrid), dim3(kNormBlock), 0, st, a);
+  else
     hipLaunchKernelGGL(normFinish<KIND>, dim3(1), dim3(kNormBlock), 0, st, a);
   return hipGetLastError();
 }
@@ -327,14 +384,15 @@ arResult_t runNorm(arTensorList* l, bool clip, int kind, float scale, float maxN
   if (hipGetDevice(&dev) != hipSuccess) return arHipError;
   if (dev != l->device) return arInvalidUsage;
   NormArgs a{};
-  a.segments = l->segments;
-  a.first = (const int*)l->table;
+  a.tiles = l->tiles;
   a.partial = (double*)workspace;
   a.norm = norm;
   a.scale = scale;
   a.maxNorm = maxNorm;
   a.eps = eps;
-  a.nSpans = l->nSpans;
+  a.nTiles = l->nTiles;
+  a.nPartial = gridOf(l);
+  a.keepFrom = clip ? l->keepFrom : l->nTiles;
   const hipError_t e = kind == arNorm2 ? launchNorm<arNorm2>(a, clip, st) : launchNorm<arNormMax>(a, clip, st);
   return e == hipSuccess ? arSuccess : arHipError;
 }
@@ -362,7 +420,7 @@ extern "C" arResult_t arTensorListDestroy(arTensorList_t list) {
   if (list == nullptr) return arSuccess;
   if (!ar::listOk(list)) return arInvalidArgument;
   list->magic = 0;
-  const hipError_t e = hipFree(list->table);
+  const hipError_t e = hipFree(list->tiles);
   delete list;
   return e == hipSuccess ? arSuccess : arHipError;
 }

@@ -43,6 +43,17 @@ __device__ __forceinline__ void storeVec(T* p, typename VecOf<T, V>::type v) {
   *(typename VecOf<T, V>::packed*)p = v;
 }
 
+// The same for memory that is not used again soon (non-temporal).
+template <typename T, int V>
+__device__ __forceinline__ typename VecOf<T, V>::type loadStream(const T* p) {
+  return __builtin_nontemporal_load((const typename VecOf<T, V>::packed*)p);
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void storeStream(T* p, typename VecOf<T, V>::type v) {
+  __builtin_nontemporal_store(v, (typename VecOf<T, V>::packed*)p);
+}
+
 // Sum over a wavefront; every lane receives it.  A butterfly: each of the 64
 // lanes adds the same pairs, so the order is fixed.
 __device__ __forceinline__ float waveSum(float v) {

@@ -295,3 +295,21 @@ def test_a_training_step(B):
         torch.cuda.synchronize()
     check_norm(norm, norm_of(host, "2") / n)
     check_clip(outs, host, norm_of(host, "2") / n, 1.0 / n, 1.0)
+
+
+@pytest.mark.parametrize("tiles", [15, 16, 17, 63, 64, 65, 511, 512, 513, 4100])
+@pytest.mark.parametrize("kind", ["2", "max"])
+def test_around_the_launch_rules(B, tiles, kind):
+    """Lists on both sides of the sizes where the number of launches and of workgroups changes."""
+    host, devs = grads([1024] * (tiles - 1) + [1000], [torch.float32], tiles)
+    want = norm_of(host, kind)
+    outs = [torch.full_like(t, float("nan")) for t in devs]
+    norm = torch.full((1,), float("nan"), device="cuda")
+    with B.TensorList(devs, outs) as lst:
+        B.arGradNorm(lst, norm, kind=kind)
+        check_norm(norm, want)
+        norm.fill_(float("nan"))
+        B.arGradClip(lst, norm, 0.5 * want, kind=kind)
+        torch.cuda.synchronize()
+    check_norm(norm, want)
+    check_clip(outs, host, want, 1.0, 0.5 * want)
