@@ -38,7 +38,7 @@ constexpr int kTilesEach = 8;
 // 128 MiB bf16 norm and clip 513 us with 16 a CU, 532 with 8, 550 with 4.
 constexpr int kClipGrid = 16 * kOpsCUs;
 // What the norm reads last it reads through the caches, and the second pass
-// begins there: 453 MB fp16 220-235 us against 262 all non-temporal, 246 all
+// begins there: 474 MB fp16 220-235 us against 262 all non-temporal, 246 all
 // cached; 128, 192, 256 and 384 MB kept 239, 234, 235, 240.
 constexpr size_t kKeepBytes = (size_t)224 << 20;
 // Lists of few tiles run in one workgroup and one launch.  Called back to back

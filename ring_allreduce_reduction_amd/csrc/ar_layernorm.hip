@@ -30,6 +30,7 @@ struct LnArgs {
   float* mean[kLnRanks];
   float* rstd[kLnRanks];
   int64_t rowStart[kLnRanks + 1]; // rank r has rows [rowStart[r], rowStart[r + 1]) of the launch
+  int blockStart[kLnRanks + 1];   // and workgroups [blockStart[r], blockStart[r + 1]), where they are shared out
   int64_t xStride, yStride, dyStride;
   int cols;
   int nranks;
@@ -63,11 +64,29 @@ __device__ __forceinline__ int rankOfRow(const LnArgs& a, int64_t row) {
   return r;
 }
 
-template <int DT, int WT>
-__global__ void __launch_bounds__(kLnBlock) layerNormRows(const LnArgs a) {
+// Calls f(first element, vector of V) for a thread's whole vectors of a row of n
+// elements, then g(element) for its share of the few behind them.
+template <int V, int BLOCK, typename F, typename G>
+__device__ __forceinline__ void forRow(int n, F f, G g) {
+  const int whole = n / V * V;
+#pragma unroll 4
+  for (int c = threadIdx.x * V; c < whole; c += BLOCK * V) f(c);
+  const int c = whole + (int)threadIdx.x;
+  if (c < n) g(c);
+}
+
+// Rows too wide for registers, and rows of less than one vector: a workgroup
+// per row, which is read three times (from the caches after the first).  2
+// ranks of 1000 rows of 40000 bf16: 87 us with 1024 threads and 8 workgroups a
+// CU, 94 with 2, 106 with 512 threads, 117 with 256.
+template <int DT, int WT, int BLOCK>
+__global__ void __launch_bounds__(BLOCK) layerNormRows(const LnArgs a) {
   typedef typename Elem<DT>::type T;
   typedef typename Elem<WT>::type W;
-  __shared__ float lds[kLnBlock / 64];
+  constexpr int V = kVec<DT>;
+  typedef typename VecOf<T, V>::type Vec;
+  typedef typename VecOf<W, V>::type WVec;
+  __shared__ float lds[BLOCK / kWave];
   const int64_t rows = a.rowStart[a.nranks];
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const int r = rankOfRow(a, row);
@@ -77,21 +96,179 @@ __global__ void __launch_bounds__(kLnBlock) layerNormRows(const LnArgs a) {
     const W* gamma = (const W*)a.gamma[r];
     const W* beta = (const W*)a.beta[r];
     float s = 0.0f;
-    for (int c = threadIdx.x; c < a.cols; c += kLnBlock) s += (float)x[c];
+    forRow<V, BLOCK>(a.cols,
+                     [&](int c) {
+                       const Vec v = loadVec<T, V>(x + c);
+#pragma unroll
+                       for (int e = 0; e < V; ++e) s += (float)v[e];
+                     },
+                     [&](int c) { s += (float)x[c]; });
     const float mean = blockSum(s, lds) / (float)a.cols;
     float q = 0.0f;
-    for (int c = threadIdx.x; c < a.cols; c += kLnBlock) {
-      const float d = (float)x[c] - mean;
-      q = fmaf(d, d, q);
-    }
+    forRow<V, BLOCK>(a.cols,
+                     [&](int c) {
+                       const Vec v = loadVec<T, V>(x + c);
+#pragma unroll
+                       for (int e = 0; e < V; ++e) q = fmaf((float)v[e] - mean, (float)v[e] - mean, q);
+                     },
+                     [&](int c) { q = fmaf((float)x[c] - mean, (float)x[c] - mean, q); });
     const float rstd = 1.0f / sqrtf(blockSum(q, lds) / (float)a.cols + a.eps);
-    for (int c = threadIdx.x; c < a.cols; c += kLnBlock) {
-      const float h = ((float)x[c] - mean) * rstd;
-      y[c] = (T)fmaf(h, gamma ? (float)gamma[c] : 1.0f, beta ? (float)beta[c] : 0.0f);
-    }
+    forRow<V, BLOCK>(a.cols,
+                     [&](int c) {
+                       const Vec v = loadVec<T, V>(x + c);
+                       const WVec g = gamma ? loadVec<W, V>(gamma + c) : (WVec)(W)1.0f;
+                       const WVec b = beta ? loadVec<W, V>(beta + c) : (WVec)(W)0.0f;
+                       FloatVec<V> o;
+#pragma unroll
+                       for (int e = 0; e < V; ++e) o[e] = fmaf(((float)v[e] - mean) * rstd, (float)g[e], (float)b[e]);
+                       storeStream<T, V>(y + c, __builtin_convertvector(o, Vec));
+                     },
+                     [&](int c) {
+                       y[c] = (T)fmaf(((float)x[c] - mean) * rstd, gamma ? (float)gamma[c] : 1.0f,
+                                      beta ? (float)beta[c] : 0.0f);
+                     });
     if (threadIdx.x == 0 && a.mean[r] != nullptr) {
       a.mean[r][i] = mean;
       a.rstd[r][i] = rstd;
+    }
+  }
+}
+
+// A group of THREADS threads (part of a wavefront, one, or a workgroup) owns whole
+// rows and keeps them in registers: thread t holds vectors t, t + THREADS, ...
+// of a row, NP of them, so memory is read once and written once.  All but the
+// last of a thread's vectors lie inside the row.  The last is moved back to
+// end with the row where it would pass it, so that every load is one whole
+// vector without a branch: `skip` of its elements then belong to another
+// thread (all V where the vector lies wholly past the end).  They count in no
+// sum; what they store is what their owner stores.
+template <int THREADS, int NP, int V>
+struct RowPieces {
+  int last;    // first element of the last vector
+  int skip;    // its elements that are another thread's
+  __device__ __forceinline__ RowPieces(int t, int cols) {
+    const int at = ((NP - 1) * THREADS + t) * V;
+    last = at > cols - V ? cols - V : at;
+    skip = at - last < V ? at - last : V;
+  }
+  __device__ __forceinline__ int offset(int p, int t) const { return p < NP - 1 ? (p * THREADS + t) * V : last; }
+  __device__ __forceinline__ bool owns(int p, int e) const { return p < NP - 1 || e >= skip; }
+  template <typename T, bool STREAM>
+  __device__ __forceinline__ void load(typename VecOf<T, V>::type (&v)[NP], const T* row, int t) const {
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+      v[p] = STREAM ? loadStream<T, V>(row + offset(p, t)) : loadVec<T, V>(row + offset(p, t));
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(int p, T* row, int t, typename VecOf<T, V>::type v) const {
+    if (p < NP - 1 || skip < V) storeStream<T, V>(row + offset(p, t), v);
+  }
+};
+
+// The workgroups of a launch are shared out among its ranks by their rows, so
+// a workgroup meets one rank's weights only and loads them once.  The groups of
+// a rank take its rows in turn: together they sweep it as one moving window.
+__device__ __forceinline__ int rankOfBlock(const LnArgs& a) {
+  int r = 0;
+  while ((int)blockIdx.x >= a.blockStart[r + 1]) ++r;
+  return r;
+}
+
+// Sum over a group's threads.  A workgroup's uses LDS buffers in turn: by the
+// time one is written again every wavefront has passed the barrier after it
+// was read.
+template <int THREADS>
+__device__ __forceinline__ float groupSum(float v, float (&lds)[2][16], int& turn) {
+  v = laneSum<(THREADS < kWave ? THREADS : kWave)>(v);
+  if (THREADS <= kWave) return v;
+  if (threadIdx.x % kWave == 0) lds[turn][threadIdx.x / kWave] = v;
+  __syncthreads();
+  float s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < THREADS / kWave; ++w) s += lds[turn][w];
+  turn ^= 1;
+  return s;
+}
+
+// DEPTH rows are in registers at once: while one is reduced the loads of the
+// others are in flight.  Bound by memory.  8 ranks of 4096 rows, 16-bit: 8192
+// columns 190 us (5.7 TB/s; a bare copy of as much runs at 6.2), 4096 99 us,
+// 2048 51 us; 200000 rows of 256 42 us, 2 ranks of 1000 rows of 32768 52 us.
+// With the launch's rows taken in turn by all groups instead of each rank's by
+// its own, 1024 columns took 67 us instead of 51 (every group met every rank's
+// weights); with a run of rows per group instead of turns 8192 took 208.
+template <int DT, int WT, int THREADS, int NP, int DEPTH>
+__global__ void __launch_bounds__(THREADS < kLnBlock ? kLnBlock : THREADS) layerNormInRegisters(const LnArgs a) {
+  typedef typename Elem<DT>::type T;
+  typedef typename Elem<WT>::type W;
+  constexpr int V = kVec<DT>, GROUPS = THREADS < kLnBlock ? kLnBlock / THREADS : 1;
+  typedef typename VecOf<T, V>::type Vec;
+  typedef typename VecOf<W, V>::type WVec;
+  __shared__ float lds[2][16];
+  int turn = 0;
+  const int t = threadIdx.x % THREADS;
+  int sub = GROUPS > 1 ? (int)threadIdx.x / THREADS : 0;
+  if (THREADS == kWave) sub = __builtin_amdgcn_readfirstlane(sub);
+  const int r = rankOfBlock(a);
+  const int64_t rows = a.rowStart[r + 1] - a.rowStart[r];
+  const int64_t step = (int64_t)(a.blockStart[r + 1] - a.blockStart[r]) * GROUPS;
+  int64_t row = (int64_t)((int)blockIdx.x - a.blockStart[r]) * GROUPS + sub;
+  if (row >= rows) return;
+  const RowPieces<THREADS, NP, V> pieces(t, a.cols);
+  const T* xs = (const T*)a.x[r];
+  Vec x[DEPTH][NP];
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d)
+    if (row + d * step < rows) pieces.template load<T, true>(x[d], xs + (row + d * step) * a.xStride, t);
+  WVec g[NP], b[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    g[p] = (WVec)(W)1.0f;
+    b[p] = (WVec)(W)0.0f;
+  }
+  if (a.gamma[r] != nullptr) pieces.template load<W, false>(g, (const W*)a.gamma[r], t);
+  if (a.beta[r] != nullptr) pieces.template load<W, false>(b, (const W*)a.beta[r], t);
+  const float inv = 1.0f / (float)a.cols;
+  while (true) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      float s = 0.0f;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        float u = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) u += pieces.owns(p, e) ? (float)x[d][p][e] : 0.0f;
+        s += u;
+      }
+      const float mean = groupSum<THREADS>(s, lds, turn) * inv;
+      float q = 0.0f;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        float u = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float c = pieces.owns(p, e) ? (float)x[d][p][e] - mean : 0.0f;
+          u = fmaf(c, c, u);
+        }
+        q += u;
+      }
+      const float rstd = 1.0f / sqrtf(groupSum<THREADS>(q, lds, turn) * inv + a.eps);
+      T* y = (T*)a.y[r] + row * a.yStride;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        FloatVec<V> o;
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          o[e] = fmaf(((float)x[d][p][e] - mean) * rstd, (float)g[p][e], (float)b[p][e]);
+        pieces.template store<T>(p, y, t, __builtin_convertvector(o, Vec));
+      }
+      if (t == 0 && a.mean[r] != nullptr) {
+        a.mean[r][row] = mean;
+        a.rstd[r][row] = rstd;
+      }
+      if (row + DEPTH * step < rows) pieces.template load<T, true>(x[d], xs + (row + DEPTH * step) * a.xStride, t);
+      row += step;
+      if (row >= rows) return;
     }
   }
 }
@@ -225,10 +402,69 @@ hipError_t byTypes(int dtype, int wtype, A... args) {
 
 int rowGrid(int64_t rows) { return (int)(rows < 8 * kOpsCUs ? rows : 8 * kOpsCUs); }
 
+// Shares at most about `most` workgroups of `groups` rows at a time out among
+// the ranks by their rows (one at least for a rank with rows); returns the grid.
+int shareBlocks(LnArgs* a, int groups, int most) {
+  const int64_t rows = a->rowStart[a->nranks];
+  int ranks = 0;
+  for (int r = 0; r < a->nranks; ++r) ranks += a->rowStart[r + 1] > a->rowStart[r];
+  const double share = most > ranks ? (double)(most - ranks) / (double)rows : 0.0;
+  a->blockStart[0] = 0;
+  for (int r = 0; r < a->nranks; ++r) {
+    const int64_t n = a->rowStart[r + 1] - a->rowStart[r];
+    const int64_t full = (n + groups - 1) / groups;
+    const int64_t mine = n == 0 ? 0 : (int64_t)((double)n * share) + 1;
+    a->blockStart[r + 1] = a->blockStart[r] + (int)(mine < full ? mine : full);
+  }
+  return a->blockStart[a->nranks];
+}
+
+template <int DT, int WT, int THREADS, int NP, int DEPTH>
+void launchForward(LnArgs a, hipStream_t st) {
+  constexpr int BLOCK = THREADS < kLnBlock ? kLnBlock : THREADS;
+  static const int resident = [] {
+    int n = 0;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, layerNormInRegisters<DT, WT, THREADS, NP, DEPTH>, BLOCK, 0) !=
+        hipSuccess || n < 1)
+      n = 1;
+    return n;
+  }();
+  const int grid = shareBlocks(&a, BLOCK / THREADS, resident * kOpsCUs);
+  hipLaunchKernelGGL((layerNormInRegisters<DT, WT, THREADS, NP, DEPTH>), dim3(grid), dim3(BLOCK), 0, st, a);
+}
+
+template <int DT, int WT, int BLOCK>
+void launchRows(const LnArgs& a, hipStream_t st) {
+  const int64_t rows = a.rowStart[a.nranks];
+  const int most = (BLOCK < 128 ? 32 : 8) * kOpsCUs;
+  hipLaunchKernelGGL((layerNormRows<DT, WT, BLOCK>), dim3((unsigned)(rows < most ? rows : most)), dim3(BLOCK), 0, st, a);
+}
+
 template <int DT, int WT>
 struct Forward {
   static hipError_t run(const LnArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL((layerNormRows<DT, WT>), dim3(rowGrid(a.rowStart[a.nranks])), dim3(kLnBlock), 0, st, a);
+    const int vecs = (a.cols + kVec<DT> - 1) / kVec<DT>;
+    // Groups as small as hold the row in four vectors a thread: a wavefront
+    // needs no barrier, and parts of one keep narrow rows from leaving lanes
+    // idle (128 columns 41 us, 100 with a wavefront a row).  512 x 2 measured
+    // 190 at 8192 columns, 256 x 4 193-197, 1024 x 1 237; 256 x 3 50 at 5001,
+    // 512 x 2 58; 512 x 4 97 at 16384, 1024 x 2 101.  Two rows in flight, four
+    // where a row is one vector a thread; from 1024 x 3 the registers hold one.
+    if (a.cols < kVec<DT>) launchRows<DT, WT, 64>(a, st);
+    else if (vecs <= 16) launchForward<DT, WT, 16, 1, 4>(a, st);
+    else if (vecs <= 32) launchForward<DT, WT, 32, 1, 4>(a, st);
+    else if (vecs <= 64) launchForward<DT, WT, 64, 1, 4>(a, st);
+    else if (vecs <= 128) launchForward<DT, WT, 64, 2, 2>(a, st);
+    else if (vecs <= 192) launchForward<DT, WT, 64, 3, 2>(a, st);
+    else if (vecs <= 256) launchForward<DT, WT, 64, 4, 2>(a, st);
+    else if (vecs <= 512) launchForward<DT, WT, 256, 2, 2>(a, st);
+    else if (vecs <= 768) launchForward<DT, WT, 256, 3, 2>(a, st);
+    else if (vecs <= 1024) launchForward<DT, WT, 512, 2, 2>(a, st);
+    else if (vecs <= 1536) launchForward<DT, WT, 512, 3, 2>(a, st);
+    else if (vecs <= 2048) launchForward<DT, WT, 512, 4, 2>(a, st);
+    else if (vecs <= 3072) launchForward<DT, WT, 1024, 3, 1>(a, st);
+    else if (vecs <= 4096) launchForward<DT, WT, 1024, 4, 1>(a, st);
+    else launchRows<DT, WT, 1024>(a, st);
     return hipGetLastError();
   }
 };

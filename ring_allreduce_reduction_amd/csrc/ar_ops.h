@@ -54,12 +54,35 @@ __device__ __forceinline__ void storeStream(T* p, typename VecOf<T, V>::type v) 
   __builtin_nontemporal_store(v, (typename VecOf<T, V>::packed*)p);
 }
 
-// Sum over a wavefront; every lane receives it.  A butterfly: each of the 64
-// lanes adds the same pairs, so the order is fixed.
-__device__ __forceinline__ float waveSum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+template <int CTRL>
+__device__ __forceinline__ float addDpp(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over a wavefront or its halves or quarters of 16 or 32 lanes; every lane
+// of the part receives it.  Lanes swap inside rows of 16 (quads, then the half
+// row and row mirrored: the other half's sum is the same in each of its lanes
+// by then), then the rows' sums are swapped or read across.  The order is
+// fixed and the same for every lane.
+template <int LANES>
+__device__ __forceinline__ float laneSum(float v) {
+  static_assert(LANES == 16 || LANES == 32 || LANES == 64, "parts of a wavefront");
+  v = addDpp<0xb1>(v);    // quad_perm 1,0,3,2
+  v = addDpp<0x4e>(v);    // quad_perm 2,3,0,1
+  v = addDpp<0x141>(v);   // row_half_mirror
+  v = addDpp<0x140>(v);   // row_mirror
+  const int b = __builtin_bit_cast(int, v);
+  if (LANES == 32) return v + __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(b, 0x401f));   // lane ^ 16
+  if (LANES == 64) {
+    const float r0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0));
+    const float r1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16));
+    const float r2 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32));
+    const float r3 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 48));
+    return (r0 + r1) + (r2 + r3);
+  }
   return v;
 }
+
+__device__ __forceinline__ float waveSum(float v) { return laneSum<64>(v); }
 
 }  // namespace ar
