@@ -35,14 +35,16 @@ struct LnArgs {
   int cols;
   int nranks;
   float eps;
-  float* partial;                 // backward: this launch's first row of partial sums
+  float* partial;                 // backward: this launch's first row of partial sums, or null
+  int partialCols;                // cols up to a multiple of 4
 };
 
 // The weights' gradients of every rank receive the same sums.
 struct LnSumArgs {
   void* dgamma[AR_MAX_RANKS];
   void* dbeta[AR_MAX_RANKS];
-  const float* partial;           // nPartial rows of [dgamma sums, dbeta sums], 2 * cols floats each
+  const float* partial;           // nPartial rows of [dgamma sums, dbeta sums], partialCols floats each
+  int partialCols;
   int nPartial;
   int nranks;
   int cols;
@@ -142,26 +144,35 @@ __global__ void __launch_bounds__(BLOCK) layerNormRows(const LnArgs a) {
 // vector without a branch: `skip` of its elements then belong to another
 // thread (all V where the vector lies wholly past the end).  They count in no
 // sum; what they store is what their owner stores.
-template <int THREADS, int NP, int V>
+template <int NP, int V>
 struct RowPieces {
-  int last;    // first element of the last vector
-  int skip;    // its elements that are another thread's
-  __device__ __forceinline__ RowPieces(int t, int cols) {
-    const int at = ((NP - 1) * THREADS + t) * V;
-    last = at > cols - V ? cols - V : at;
-    skip = at - last < V ? at - last : V;
+  uint32_t first;    // first element of the first vector
+  uint32_t stride;   // elements from a vector to the next
+  uint32_t last;     // first element of the last vector
+  int skip;          // its elements that are another thread's
+  __device__ __forceinline__ RowPieces(int t, int threads, int cols)
+      : first((uint32_t)(t * V)), stride((uint32_t)(threads * V)) {
+    const int at = ((NP - 1) * threads + t) * V;
+    last = (uint32_t)(at > cols - V ? cols - V : at);
+    skip = at - (int)last < V ? at - (int)last : V;
   }
-  __device__ __forceinline__ int offset(int p, int t) const { return p < NP - 1 ? (p * THREADS + t) * V : last; }
+  __device__ __forceinline__ uint32_t offset(int p) const { return p < NP - 1 ? first + (uint32_t)p * stride : last; }
   __device__ __forceinline__ bool owns(int p, int e) const { return p < NP - 1 || e >= skip; }
+  // A row starts at the same address for every thread, the offset inside it
+  // fits 32 bits: one scalar base and one register of offset per access.
+  template <typename T>
+  __device__ __forceinline__ T* at(int p, T* row) const {
+    return (T*)((char*)row + (uint32_t)(offset(p) * (uint32_t)sizeof(T)));
+  }
   template <typename T, bool STREAM>
-  __device__ __forceinline__ void load(typename VecOf<T, V>::type (&v)[NP], const T* row, int t) const {
+  __device__ __forceinline__ void load(typename VecOf<T, V>::type (&v)[NP], const T* row) const {
 #pragma unroll
     for (int p = 0; p < NP; ++p)
-      v[p] = STREAM ? loadStream<T, V>(row + offset(p, t)) : loadVec<T, V>(row + offset(p, t));
+      v[p] = STREAM ? loadStream<T, V>(at(p, const_cast<T*>(row))) : loadVec<T, V>(at(p, const_cast<T*>(row)));
   }
   template <typename T>
-  __device__ __forceinline__ void store(int p, T* row, int t, typename VecOf<T, V>::type v) const {
-    if (p < NP - 1 || skip < V) storeStream<T, V>(row + offset(p, t), v);
+  __device__ __forceinline__ void store(int p, T* row, typename VecOf<T, V>::type v) const {
+    if (p < NP - 1 || skip < V) storeStream<T, V>(at(p, row), v);
   }
 };
 
@@ -174,20 +185,49 @@ __device__ __forceinline__ int rankOfBlock(const LnArgs& a) {
   return r;
 }
 
-// Sum over a group's threads.  A workgroup's uses LDS buffers in turn: by the
-// time one is written again every wavefront has passed the barrier after it
-// was read.
+// Sums over a group's threads.  A workgroup's wavefronts leave theirs in LDS and
+// every row of 16 lanes reads the 16 slots and adds them across its lanes (slots
+// of wavefronts that the workgroup does not have hold zeros, see clearSlots).
+// Two LDS buffers in turn: by the time one is written again every wavefront has
+// passed the barrier after it was read.
+struct SumSlots {
+  float v[2][2][16];   // buffer, sum, wavefront
+};
+
+// Called by every thread before the first sum; that sum's barrier publishes it.
+__device__ __forceinline__ void clearSlots(SumSlots& lds) {
+  if (threadIdx.x < 64 && (int)(threadIdx.x % 16) >= (int)blockDim.x / kWave)
+    (&lds.v[0][0][0])[threadIdx.x] = 0.0f;
+}
+
 template <int THREADS>
-__device__ __forceinline__ float groupSum(float v, float (&lds)[2][16], int& turn) {
-  v = laneSum<(THREADS < kWave ? THREADS : kWave)>(v);
-  if (THREADS <= kWave) return v;
-  if (threadIdx.x % kWave == 0) lds[turn][threadIdx.x / kWave] = v;
+__device__ __forceinline__ float groupSum(float v, SumSlots& lds, int& turn) {
+  if (THREADS <= kWave) return laneSum<(THREADS < kWave ? THREADS : kWave)>(v);
+  v = waveSumLast(v);
+  if (threadIdx.x % kWave == kWave - 1) lds.v[turn][0][threadIdx.x / kWave] = v;
   __syncthreads();
-  float s = 0.0f;
-#pragma unroll
-  for (int w = 0; w < THREADS / kWave; ++w) s += lds[turn][w];
+  v = rowSum(lds.v[turn][0][threadIdx.x % 16]);
   turn ^= 1;
-  return s;
+  return v;
+}
+
+template <int THREADS>
+__device__ __forceinline__ void groupSum2(float& v, float& u, SumSlots& lds, int& turn) {
+  if (THREADS <= kWave) {
+    v = laneSum<(THREADS < kWave ? THREADS : kWave)>(v);
+    u = laneSum<(THREADS < kWave ? THREADS : kWave)>(u);
+    return;
+  }
+  v = waveSumLast(v);
+  u = waveSumLast(u);
+  if (threadIdx.x % kWave == kWave - 1) {
+    lds.v[turn][0][threadIdx.x / kWave] = v;
+    lds.v[turn][1][threadIdx.x / kWave] = u;
+  }
+  __syncthreads();
+  v = rowSum(lds.v[turn][0][threadIdx.x % 16]);
+  u = rowSum(lds.v[turn][1][threadIdx.x % 16]);
+  turn ^= 1;
 }
 
 // DEPTH rows are in registers at once: while one is reduced the loads of the
@@ -204,8 +244,9 @@ __global__ void __launch_bounds__(THREADS < kLnBlock ? kLnBlock : THREADS) layer
   constexpr int V = kVec<DT>, GROUPS = THREADS < kLnBlock ? kLnBlock / THREADS : 1;
   typedef typename VecOf<T, V>::type Vec;
   typedef typename VecOf<W, V>::type WVec;
-  __shared__ float lds[2][16];
+  __shared__ SumSlots lds;
   int turn = 0;
+  if (THREADS > kWave) clearSlots(lds);
   const int t = threadIdx.x % THREADS;
   int sub = GROUPS > 1 ? (int)threadIdx.x / THREADS : 0;
   if (THREADS == kWave) sub = __builtin_amdgcn_readfirstlane(sub);
@@ -214,20 +255,20 @@ __global__ void __launch_bounds__(THREADS < kLnBlock ? kLnBlock : THREADS) layer
   const int64_t step = (int64_t)(a.blockStart[r + 1] - a.blockStart[r]) * GROUPS;
   int64_t row = (int64_t)((int)blockIdx.x - a.blockStart[r]) * GROUPS + sub;
   if (row >= rows) return;
-  const RowPieces<THREADS, NP, V> pieces(t, a.cols);
+  const RowPieces<NP, V> pieces(t, THREADS, a.cols);
   const T* xs = (const T*)a.x[r];
   Vec x[DEPTH][NP];
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d)
-    if (row + d * step < rows) pieces.template load<T, true>(x[d], xs + (row + d * step) * a.xStride, t);
+    if (row + d * step < rows) pieces.template load<T, true>(x[d], xs + (row + d * step) * a.xStride);
   WVec g[NP], b[NP];
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
     g[p] = (WVec)(W)1.0f;
     b[p] = (WVec)(W)0.0f;
   }
-  if (a.gamma[r] != nullptr) pieces.template load<W, false>(g, (const W*)a.gamma[r], t);
-  if (a.beta[r] != nullptr) pieces.template load<W, false>(b, (const W*)a.beta[r], t);
+  if (a.gamma[r] != nullptr) pieces.template load<W, false>(g, (const W*)a.gamma[r]);
+  if (a.beta[r] != nullptr) pieces.template load<W, false>(b, (const W*)a.beta[r]);
   const float inv = 1.0f / (float)a.cols;
   while (true) {
 #pragma unroll
@@ -260,24 +301,194 @@ __global__ void __launch_bounds__(THREADS < kLnBlock ? kLnBlock : THREADS) layer
 #pragma unroll
         for (int e = 0; e < V; ++e)
           o[e] = fmaf(((float)x[d][p][e] - mean) * rstd, (float)g[p][e], (float)b[p][e]);
-        pieces.template store<T>(p, y, t, __builtin_convertvector(o, Vec));
+        pieces.template store<T>(p, y, __builtin_convertvector(o, Vec));
       }
       if (t == 0 && a.mean[r] != nullptr) {
         a.mean[r][row] = mean;
         a.rstd[r][row] = rstd;
       }
-      if (row + DEPTH * step < rows) pieces.template load<T, true>(x[d], xs + (row + DEPTH * step) * a.xStride, t);
+      if (row + DEPTH * step < rows) pieces.template load<T, true>(x[d], xs + (row + DEPTH * step) * a.xStride);
       row += step;
       if (row >= rows) return;
     }
   }
 }
 
-template <int DT, int WT>
-__global__ void __launch_bounds__(kLnBlock) layerNormBackwardRows(const LnArgs a) {
+// Stores the elements of a vector of sums that its thread owns; whole ones start
+// at a multiple of 16 bytes of `row`, which is as aligned itself.
+template <int V, typename Pieces>
+__device__ __forceinline__ void storeOwned(const Pieces& pieces, int p, float* row, FloatVec<V> v) {
+  float* to = row + pieces.offset(p);
+  if (pieces.owns(p, 0)) {
+#pragma unroll
+    for (int e = 0; e < V; e += 4) *(FloatVec<4>*)(to + e) = FloatVec<4>{v[e], v[e + 1], v[e + 2], v[e + 3]};
+  } else {
+#pragma unroll
+    for (int e = 1; e < V; ++e)
+      if (pieces.owns(p, e)) to[e] = v[e];
+  }
+}
+
+// The bits of a vector that its thread owns, to be and-ed with a vector.
+template <int DT>
+struct OwnBits {
+  typedef uint32_t words __attribute__((ext_vector_type(4)));
+  typedef typename VecOf<typename Elem<DT>::type, kVec<DT>>::type Vec;
+  words bits;
+  __device__ __forceinline__ explicit OwnBits(int skip) {
+    constexpr int PER = kVec<DT> / 4;   // elements of a word: 1 or 2
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      bits[w] = PER == 1 ? (w >= skip ? 0xffffffffu : 0u)
+                         : (2 * w >= skip ? 0xffffu : 0u) | (2 * w + 1 >= skip ? 0xffff0000u : 0u);
+  }
+  __device__ __forceinline__ Vec of(Vec v) const { return __builtin_bit_cast(Vec, __builtin_bit_cast(words, v) & bits); }
+};
+
+// The backward pass with a row's x and dy in registers.  With d = x - m:
+//   s = sum dy g,  u = sum dy d g,  dx = (r dy) g - d (r^3 u / C) - r s / C,
+//   dg += (dy d) r,  db += dy.
+// A thread meets the same columns in every row, so it adds their weights'
+// gradients up in registers too; a workgroup's groups are joined through LDS at
+// the end, and each workgroup leaves one row of partial sums.  x - m is formed
+// as it stands, not as x r - m r: a row with a large offset loses nothing.
+// Bound by memory at 8192 columns (8 ranks of 4096 rows, bf16: 286-290 us, 5.6
+// TB/s, with the 8 us of the sums' kernel); a row costs a wavefront about 200
+// instructions at 8 values a thread, which shows where rows are short: 2048
+// columns 85 us for 403 MB, 128 columns 64 us for 310 MB.
+template <int DT, int WT, int THREADS, int NP, int DEPTH, int WAVES>
+__global__ void __launch_bounds__(THREADS < kLnBlock ? kLnBlock : THREADS) __attribute__((amdgpu_waves_per_eu(WAVES)))
+layerNormBackwardInRegisters(const LnArgs a) {
   typedef typename Elem<DT>::type T;
   typedef typename Elem<WT>::type W;
-  __shared__ float lds[kLnBlock / 64];
+  constexpr int V = kVec<DT>, GROUPS = THREADS < kLnBlock ? kLnBlock / THREADS : 1;
+  typedef typename VecOf<T, V>::type Vec;
+  typedef typename VecOf<W, V>::type WVec;
+  __shared__ SumSlots lds;
+  __shared__ __align__(16) float joined[GROUPS > 1 ? GROUPS * 2 * THREADS * NP * V : 1];
+  int turn = 0;
+  const int threads = GROUPS > 1 ? THREADS : (int)blockDim.x;
+  const int t = GROUPS > 1 ? (int)threadIdx.x % THREADS : (int)threadIdx.x;
+  int sub = GROUPS > 1 ? (int)threadIdx.x / THREADS : 0;
+  if (THREADS == kWave) sub = __builtin_amdgcn_readfirstlane(sub);
+  if (THREADS > kWave) clearSlots(lds);
+  const int r = rankOfBlock(a);
+  const int64_t rows = a.rowStart[r + 1] - a.rowStart[r];
+  const int64_t step = (int64_t)(a.blockStart[r + 1] - a.blockStart[r]) * GROUPS;
+  int64_t row = (int64_t)((int)blockIdx.x - a.blockStart[r]) * GROUPS + sub;
+  const RowPieces<NP, V> pieces(t, threads, a.cols);
+  const OwnBits<DT> own(pieces.skip);
+  const T* xs = (const T*)a.x[r];
+  const T* dys = (const T*)a.dy[r];
+  T* dxs = (T*)a.y[r];
+  const float* means = a.mean[r];
+  const float* rstds = a.rstd[r];
+  Vec x[DEPTH][NP], dy[DEPTH][NP];
+  float mean[DEPTH], rstd[DEPTH];
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) {
+    const int64_t at = row + d * step;
+    if (at < rows) {
+      pieces.template load<T, true>(x[d], xs + at * a.xStride);
+      pieces.template load<T, true>(dy[d], dys + at * a.dyStride);
+      mean[d] = means[at];
+      rstd[d] = rstds[at];
+    }
+  }
+  WVec g[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) g[p] = (WVec)(W)1.0f;
+  if (a.gamma[r] != nullptr) pieces.template load<W, false>(g, (const W*)a.gamma[r]);
+  FloatVec<V> dg[NP], db[NP];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    dg[p] = (FloatVec<V>)0.0f;
+    db[p] = (FloatVec<V>)0.0f;
+  }
+  const float inv = 1.0f / (float)a.cols;
+  while (row < rows) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      float s = 0.0f, u = 0.0f;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) {
+        const Vec mine = p < NP - 1 ? dy[d][p] : own.of(dy[d][p]);
+        float sp = 0.0f, up = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float o = (float)mine[e];
+          const float od = o * ((float)x[d][p][e] - mean[d]);
+          sp = fmaf(o, (float)g[p][e], sp);
+          up = fmaf(od, (float)g[p][e], up);
+          dg[p][e] = fmaf(od, rstd[d], dg[p][e]);
+          db[p][e] += o;
+        }
+        s += sp;
+        u += up;
+      }
+      if (dxs != nullptr) {
+        groupSum2<THREADS>(s, u, lds, turn);
+        const float k1 = -rstd[d] * (s * inv), k2 = -(rstd[d] * rstd[d]) * (rstd[d] * (u * inv));
+        T* dx = dxs + row * a.yStride;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          FloatVec<V> o;
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            o[e] = fmaf((float)dy[d][p][e] * rstd[d], (float)g[p][e], fmaf((float)x[d][p][e] - mean[d], k2, k1));
+          pieces.template store<T>(p, dx, __builtin_convertvector(o, Vec));
+        }
+      }
+      const int64_t at = row + DEPTH * step;
+      if (at < rows) {
+        pieces.template load<T, true>(x[d], xs + at * a.xStride);
+        pieces.template load<T, true>(dy[d], dys + at * a.dyStride);
+        mean[d] = means[at];
+        rstd[d] = rstds[at];
+      }
+      row += step;
+      if (row >= rows) break;
+    }
+  }
+  if (a.partial == nullptr) return;
+  float* sums = a.partial + (size_t)blockIdx.x * 2 * a.partialCols;
+  if (GROUPS == 1) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      storeOwned<V>(pieces, p, sums, dg[p]);
+      storeOwned<V>(pieces, p, sums + a.partialCols, db[p]);
+    }
+    return;
+  }
+  constexpr int WIDTH = THREADS * NP * V;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    storeOwned<V>(pieces, p, joined + sub * 2 * WIDTH, dg[p]);
+    storeOwned<V>(pieces, p, joined + (sub * 2 + 1) * WIDTH, db[p]);
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.cols; c += kLnBlock) {
+    float u = 0.0f, v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < GROUPS; ++k) {
+      u += joined[k * 2 * WIDTH + c];
+      v += joined[(k * 2 + 1) * WIDTH + c];
+    }
+    sums[c] = u;
+    sums[a.partialCols + c] = v;
+  }
+}
+
+// Rows too wide for registers, or narrower than a vector: a workgroup per row,
+// read twice.
+template <int DT, int WT, int BLOCK>
+__global__ void __launch_bounds__(BLOCK) layerNormBackwardRows(const LnArgs a) {
+  typedef typename Elem<DT>::type T;
+  typedef typename Elem<WT>::type W;
+  constexpr int V = kVec<DT>;
+  typedef typename VecOf<T, V>::type Vec;
+  typedef typename VecOf<W, V>::type WVec;
+  __shared__ float lds[BLOCK / kWave];
   const int64_t rows = a.rowStart[a.nranks];
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const int r = rankOfRow(a, row);
@@ -287,66 +498,148 @@ __global__ void __launch_bounds__(kLnBlock) layerNormBackwardRows(const LnArgs a
     T* dx = (T*)a.y[r] + i * a.yStride;
     const W* gamma = (const W*)a.gamma[r];
     const float mean = a.mean[r][i], rstd = a.rstd[r][i];
-    float s = 0.0f, t = 0.0f;
-    for (int c = threadIdx.x; c < a.cols; c += kLnBlock) {
-      const float q = (float)dy[c] * (gamma ? (float)gamma[c] : 1.0f);
-      s += q;
-      t = fmaf(q, ((float)x[c] - mean) * rstd, t);
-    }
+    float s = 0.0f, u = 0.0f;
+    forRow<V, BLOCK>(a.cols,
+                     [&](int c) {
+                       const Vec v = loadVec<T, V>(x + c), o = loadVec<T, V>(dy + c);
+                       const WVec g = gamma ? loadVec<W, V>(gamma + c) : (WVec)(W)1.0f;
+#pragma unroll
+                       for (int e = 0; e < V; ++e) {
+                         const float q = (float)o[e] * (float)g[e];
+                         s += q;
+                         u = fmaf(q, ((float)v[e] - mean) * rstd, u);
+                       }
+                     },
+                     [&](int c) {
+                       const float q = (float)dy[c] * (gamma ? (float)gamma[c] : 1.0f);
+                       s += q;
+                       u = fmaf(q, ((float)x[c] - mean) * rstd, u);
+                     });
     s = blockSum(s, lds) / (float)a.cols;
-    t = blockSum(t, lds) / (float)a.cols;
-    for (int c = threadIdx.x; c < a.cols; c += kLnBlock) {
-      const float q = (float)dy[c] * (gamma ? (float)gamma[c] : 1.0f);
-      const float h = ((float)x[c] - mean) * rstd;
-      dx[c] = (T)(rstd * (q - s - h * t));
-    }
+    u = blockSum(u, lds) / (float)a.cols;
+    forRow<V, BLOCK>(a.cols,
+                     [&](int c) {
+                       const Vec v = loadVec<T, V>(x + c), o = loadVec<T, V>(dy + c);
+                       const WVec g = gamma ? loadVec<W, V>(gamma + c) : (WVec)(W)1.0f;
+                       FloatVec<V> d;
+#pragma unroll
+                       for (int e = 0; e < V; ++e)
+                         d[e] = rstd * fmaf(-(((float)v[e] - mean) * rstd), u, fmaf((float)o[e], (float)g[e], -s));
+                       storeVec<T, V>(dx + c, __builtin_convertvector(d, Vec));
+                     },
+                     [&](int c) {
+                       dx[c] = (T)(rstd * fmaf(-(((float)x[c] - mean) * rstd), u,
+                                               fmaf((float)dy[c], gamma ? (float)gamma[c] : 1.0f, -s)));
+                     });
   }
 }
 
-// Block (column group, slice of the rows): one thread per column adds its
-// slice's rows in order.
-template <int DT>
+// The weights' sums of such rows: a wavefront per vector of columns and slice of
+// the rows, four rows at a time; ONE takes single columns (rows of less than a
+// vector and the columns behind the last whole one).
+template <int DT, bool ONE>
 __global__ void __launch_bounds__(kLnBlock) layerNormWeightSums(const LnArgs a) {
   typedef typename Elem<DT>::type T;
-  const int c = (int)blockIdx.x * kLnBlock + (int)threadIdx.x;
-  if (c >= a.cols) return;
+  constexpr int V = ONE ? 1 : kVec<DT>;
+  typedef typename VecOf<T, V>::type Vec;
+  const int first = ONE ? a.cols / kVec<DT> * kVec<DT> : 0;
+  const int c = first + ((int)blockIdx.x * kLnBlock + (int)threadIdx.x) * V;
+  if (c + V > a.cols) return;
   const int64_t rows = a.rowStart[a.nranks];
   const int64_t lo = rows * blockIdx.y / gridDim.y, hi = rows * (blockIdx.y + 1) / gridDim.y;
-  float dg = 0.0f, db = 0.0f;
-  int r = 0;
-  for (int64_t row = lo; row < hi; ++row) {
-    while (row >= a.rowStart[r + 1]) ++r;
-    const int64_t i = row - a.rowStart[r];
-    const float d = (float)((const T*)a.dy[r])[i * a.dyStride + c];
-    const float h = ((float)((const T*)a.x[r])[i * a.xStride + c] - a.mean[r][i]) * a.rstd[r][i];
-    dg = fmaf(d, h, dg);
-    db += d;
+  FloatVec<V> dg = (FloatVec<V>)0.0f, db = (FloatVec<V>)0.0f;
+  for (int r = 0; r < a.nranks; ++r) {
+    const int64_t from = (lo > a.rowStart[r] ? lo : a.rowStart[r]) - a.rowStart[r];
+    const int64_t to = (hi < a.rowStart[r + 1] ? hi : a.rowStart[r + 1]) - a.rowStart[r];
+    const T* x = (const T*)a.x[r] + c;
+    const T* dy = (const T*)a.dy[r] + c;
+#pragma unroll 4
+    for (int64_t i = from; i < to; ++i) {
+      const Vec v = loadStream<T, V>(x + i * a.xStride), o = loadStream<T, V>(dy + i * a.dyStride);
+      const float mean = a.mean[r][i], rstd = a.rstd[r][i];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        dg[e] = fmaf((float)o[e], ((float)v[e] - mean) * rstd, dg[e]);
+        db[e] += (float)o[e];
+      }
+    }
   }
-  float* p = a.partial + (size_t)blockIdx.y * 2 * a.cols;
-  p[c] = dg;
-  p[a.cols + c] = db;
+  float* p = a.partial + (size_t)blockIdx.y * 2 * a.partialCols + c;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    p[e] = dg[e];
+    p[a.partialCols + e] = db[e];
+  }
 }
+
+// The partial sums of all workgroups and launches, 64 columns a workgroup: its
+// 64 slices of 16 threads take every 64th row, then the slices are joined in
+// order.  blockIdx.y: dgamma or dbeta.
+constexpr int kSumBlock = 1024, kSumCols = 64, kSlices = kSumBlock / (kSumCols / 4);
 
 template <int WT>
-__global__ void __launch_bounds__(kLnBlock) layerNormWeightGrads(const LnSumArgs a) {
+__global__ void __launch_bounds__(kSumBlock) layerNormWeightGrads(const LnSumArgs a) {
   typedef typename Elem<WT>::type W;
-  const int c = (int)blockIdx.x * kLnBlock + (int)threadIdx.x;
-  if (c >= a.cols) return;
-  float dg = 0.0f, db = 0.0f;
-  for (int p = 0; p < a.nPartial; ++p) {
-    dg += a.partial[(size_t)p * 2 * a.cols + c];
-    db += a.partial[(size_t)p * 2 * a.cols + a.cols + c];
+  __shared__ float lds[kSlices][kSumCols];
+  void* const* out = blockIdx.y == 0 ? a.dgamma : a.dbeta;
+  if (out[0] == nullptr) return;
+  const int lane = threadIdx.x % (kSumCols / 4), slice = threadIdx.x / (kSumCols / 4);
+  const int c = (int)blockIdx.x * kSumCols + lane * 4;
+  FloatVec<4> sum = (FloatVec<4>)0.0f;
+  if (c < a.cols) {
+    const float* p = a.partial + (size_t)blockIdx.y * a.partialCols + c;
+#pragma unroll 4
+    for (int k = slice; k < a.nPartial; k += kSlices) sum += *(const FloatVec<4>*)(p + (size_t)k * 2 * a.partialCols);
   }
-  for (int r = 0; r < a.nranks; ++r) {
-    if (a.dgamma[r] != nullptr) ((W*)a.dgamma[r])[c] = (W)dg;
-    if (a.dbeta[r] != nullptr) ((W*)a.dbeta[r])[c] = (W)db;
-  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) lds[slice][lane * 4 + e] = sum[e];
+  __syncthreads();
+  const int col = (int)blockIdx.x * kSumCols + (int)threadIdx.x;
+  if (threadIdx.x >= kSumCols || col >= a.cols) return;
+  float all = 0.0f;
+#pragma unroll 8
+  for (int k = 0; k < kSlices; ++k) all += lds[k][threadIdx.x];
+  for (int r = 0; r < a.nranks; ++r) ((W*)out[r])[col] = (W)all;
 }
 
-// Rows of partial sums a launch of `rows` rows writes.
-int partialRows(int64_t rows) {
-  const int64_t n = (rows + 15) / 16;
-  return (int)(n < 1 ? 1 : n > kOpsCUs ? kOpsCUs : n);
+// How a backward launch is cut: `threads` threads hold a row, `pieces` vectors
+// each (0 threads: the kernels for rows that registers do not hold), and at
+// most `most` workgroups.
+struct BackwardCut {
+  int threads, pieces;
+  int groups;   // of a workgroup
+  int most;
+};
+
+BackwardCut backwardCut(int cols, int esz) {
+  const int V = 16 / esz, vecs = (cols + V - 1) / V;
+  if (cols < V || vecs > (esz == 4 ? 4096 : 2048)) {
+    // 2 ranks of 1000 rows of 32768: the sums' kernels 59 us with 64 slices of
+    // the rows, 92 with 256
+    const int wide = (vecs + kLnBlock - 1) / kLnBlock;   // workgroups across the columns
+    return {0, 0, 1, wide < 64 ? 4 * kOpsCUs / wide : 16};
+  }
+  // One vector a thread as long as a workgroup reaches: 8192 columns 16-bit
+  // 286-290 us with 1024 x 1 and three rows in flight, 292-297 with 512 x 2
+  // (two rows; 160 registers a thread), 315 with one row in flight; 4096
+  // columns 155 with 512 x 1, 163 with 256 x 2.  About 12 wavefronts a CU: each
+  // workgroup costs a row of partial sums to write and read (2048 columns 85
+  // us, 88 with 20 wavefronts; 8192 columns fill a CU with one workgroup).
+  if (vecs <= 16) return {16, 1, 16, 4 * kOpsCUs};
+  if (vecs <= 32) return {32, 1, 8, 4 * kOpsCUs};
+  if (vecs <= 64) return {64, 1, 4, 4 * kOpsCUs};
+  if (vecs <= 128) return {64, 2, 4, 4 * kOpsCUs};
+  const int pieces = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : vecs <= 3072 ? 3 : 4;
+  const int waves = ((vecs + pieces - 1) / pieces + kWave - 1) / kWave;
+  return {waves * kWave, pieces, 1, (waves <= 12 ? 12 / waves : 1) * kOpsCUs};
+}
+
+// Rows of partial sums that a launch of `rows` rows of all its ranks leaves at
+// most: its workgroups.  Few rows take few workgroups, each of which costs a
+// row of partial sums to write and read.
+int partialRows(int64_t rows, const BackwardCut& k) {
+  const int64_t most = (rows + k.groups - 1) / k.groups;
+  return (int)(most < 1 ? 1 : most > k.most ? k.most : most);
 }
 
 struct Shape {
@@ -402,8 +695,9 @@ hipError_t byTypes(int dtype, int wtype, A... args) {
 
 int rowGrid(int64_t rows) { return (int)(rows < 8 * kOpsCUs ? rows : 8 * kOpsCUs); }
 
-// Shares at most about `most` workgroups of `groups` rows at a time out among
-// the ranks by their rows (one at least for a rank with rows); returns the grid.
+// Shares `most` workgroups of `groups` rows at a time out among the ranks by
+// their rows, at least one to a rank with rows (so more than `most` only where
+// there are more such ranks); returns the grid.
 int shareBlocks(LnArgs* a, int groups, int most) {
   const int64_t rows = a->rowStart[a->nranks];
   int ranks = 0;
@@ -419,8 +713,15 @@ int shareBlocks(LnArgs* a, int groups, int most) {
   return a->blockStart[a->nranks];
 }
 
+// What RowPieces assumes: all of a thread's vectors but the last lie inside the
+// row, and the last ones reach its end.
+bool rowFits(int cols, int V, int threads, int pieces) {
+  return cols >= V && cols >= (pieces - 1) * threads * V && cols <= pieces * threads * V;
+}
+
 template <int DT, int WT, int THREADS, int NP, int DEPTH>
-void launchForward(LnArgs a, hipStream_t st) {
+hipError_t launchForward(LnArgs a, hipStream_t st) {
+  if (!rowFits(a.cols, kVec<DT>, THREADS, NP)) return hipErrorInvalidValue;
   constexpr int BLOCK = THREADS < kLnBlock ? kLnBlock : THREADS;
   static const int resident = [] {
     int n = 0;
@@ -431,13 +732,15 @@ void launchForward(LnArgs a, hipStream_t st) {
   }();
   const int grid = shareBlocks(&a, BLOCK / THREADS, resident * kOpsCUs);
   hipLaunchKernelGGL((layerNormInRegisters<DT, WT, THREADS, NP, DEPTH>), dim3(grid), dim3(BLOCK), 0, st, a);
+  return hipGetLastError();
 }
 
 template <int DT, int WT, int BLOCK>
-void launchRows(const LnArgs& a, hipStream_t st) {
+hipError_t launchRows(const LnArgs& a, hipStream_t st) {
   const int64_t rows = a.rowStart[a.nranks];
   const int most = (BLOCK < 128 ? 32 : 8) * kOpsCUs;
   hipLaunchKernelGGL((layerNormRows<DT, WT, BLOCK>), dim3((unsigned)(rows < most ? rows : most)), dim3(BLOCK), 0, st, a);
+  return hipGetLastError();
 }
 
 template <int DT, int WT>
@@ -450,43 +753,84 @@ struct Forward {
     // 190 at 8192 columns, 256 x 4 193-197, 1024 x 1 237; 256 x 3 50 at 5001,
     // 512 x 2 58; 512 x 4 97 at 16384, 1024 x 2 101.  Two rows in flight, four
     // where a row is one vector a thread; from 1024 x 3 the registers hold one.
-    if (a.cols < kVec<DT>) launchRows<DT, WT, 64>(a, st);
-    else if (vecs <= 16) launchForward<DT, WT, 16, 1, 4>(a, st);
-    else if (vecs <= 32) launchForward<DT, WT, 32, 1, 4>(a, st);
-    else if (vecs <= 64) launchForward<DT, WT, 64, 1, 4>(a, st);
-    else if (vecs <= 128) launchForward<DT, WT, 64, 2, 2>(a, st);
-    else if (vecs <= 192) launchForward<DT, WT, 64, 3, 2>(a, st);
-    else if (vecs <= 256) launchForward<DT, WT, 64, 4, 2>(a, st);
-    else if (vecs <= 512) launchForward<DT, WT, 256, 2, 2>(a, st);
-    else if (vecs <= 768) launchForward<DT, WT, 256, 3, 2>(a, st);
-    else if (vecs <= 1024) launchForward<DT, WT, 512, 2, 2>(a, st);
-    else if (vecs <= 1536) launchForward<DT, WT, 512, 3, 2>(a, st);
-    else if (vecs <= 2048) launchForward<DT, WT, 512, 4, 2>(a, st);
-    else if (vecs <= 3072) launchForward<DT, WT, 1024, 3, 1>(a, st);
-    else if (vecs <= 4096) launchForward<DT, WT, 1024, 4, 1>(a, st);
-    else launchRows<DT, WT, 1024>(a, st);
-    return hipGetLastError();
+    if (a.cols < kVec<DT>) return launchRows<DT, WT, 64>(a, st);
+    if (vecs <= 16) return launchForward<DT, WT, 16, 1, 4>(a, st);
+    if (vecs <= 32) return launchForward<DT, WT, 32, 1, 4>(a, st);
+    if (vecs <= 64) return launchForward<DT, WT, 64, 1, 4>(a, st);
+    if (vecs <= 128) return launchForward<DT, WT, 64, 2, 2>(a, st);
+    if (vecs <= 192) return launchForward<DT, WT, 64, 3, 2>(a, st);
+    if (vecs <= 256) return launchForward<DT, WT, 64, 4, 2>(a, st);
+    if (vecs <= 512) return launchForward<DT, WT, 256, 2, 2>(a, st);
+    if (vecs <= 768) return launchForward<DT, WT, 256, 3, 2>(a, st);
+    if (vecs <= 1024) return launchForward<DT, WT, 512, 2, 2>(a, st);
+    if (vecs <= 1536) return launchForward<DT, WT, 512, 3, 2>(a, st);
+    if (vecs <= 2048) return launchForward<DT, WT, 512, 4, 2>(a, st);
+    if (vecs <= 3072) return launchForward<DT, WT, 1024, 3, 1>(a, st);
+    if (vecs <= 4096) return launchForward<DT, WT, 1024, 4, 1>(a, st);
+    return launchRows<DT, WT, 1024>(a, st);
   }
 };
 
+template <int DT, int WT, int THREADS, int NP, int DEPTH, int WAVES>
+int launchBackward(LnArgs a, const BackwardCut& k, hipStream_t st) {
+  if (!rowFits(a.cols, kVec<DT>, k.threads, k.pieces) || k.threads > THREADS || k.pieces != NP) return -1;
+  const int grid = shareBlocks(&a, k.groups, partialRows(a.rowStart[a.nranks], k));
+  hipLaunchKernelGGL((layerNormBackwardInRegisters<DT, WT, THREADS, NP, DEPTH, WAVES>), dim3(grid),
+                     dim3(THREADS < kLnBlock ? kLnBlock : k.threads), 0, st, a);
+  return grid;
+}
+
+// Runs the backward pass of a launch with rows; *partials receives the rows of
+// partial sums it leaves.
 template <int DT, int WT>
 struct Backward {
-  static hipError_t run(const LnArgs& a, bool dx, hipStream_t st) {
+  static hipError_t run(const LnArgs& a, int* partials, hipStream_t st) {
+    constexpr int V = kVec<DT>;
+    const BackwardCut k = backwardCut(a.cols, 16 / V);
     const int64_t rows = a.rowStart[a.nranks];
-    // the weights' sums first: dx may be written over x or dy
-    if (a.partial != nullptr)
-      hipLaunchKernelGGL((layerNormWeightSums<DT>), dim3((a.cols + kLnBlock - 1) / kLnBlock, partialRows(rows)),
-                         dim3(kLnBlock), 0, st, a);
-    if (dx && rows > 0)
-      hipLaunchKernelGGL((layerNormBackwardRows<DT, WT>), dim3(rowGrid(rows)), dim3(kLnBlock), 0, st, a);
-    return hipGetLastError();
+    if (k.threads == 16) *partials = launchBackward<DT, WT, 16, 1, 2, 1>(a, k, st);
+    else if (k.threads == 32) *partials = launchBackward<DT, WT, 32, 1, 2, 1>(a, k, st);
+    else if (k.threads == 64 && k.pieces == 1) *partials = launchBackward<DT, WT, 64, 1, 2, 1>(a, k, st);
+    else if (k.threads == 64) *partials = launchBackward<DT, WT, 64, 2, 2, 3>(a, k, st);
+    else if (k.pieces == 1) *partials = k.threads <= 256   ? launchBackward<DT, WT, 256, 1, 3, 3>(a, k, st)
+                                      : k.threads <= 512 ? launchBackward<DT, WT, 512, 1, 3, 3>(a, k, st)
+                                                         : launchBackward<DT, WT, 1024, 1, 3, 4>(a, k, st);
+    else if (k.pieces == 2) *partials = launchBackward<DT, WT, 1024, 2, 1, 4>(a, k, st);
+    else if (k.pieces >= 3) {
+      if constexpr (V == 4) *partials = k.pieces == 3 ? launchBackward<DT, WT, 1024, 3, 1, 4>(a, k, st)
+                                                      : launchBackward<DT, WT, 1024, 4, 1, 4>(a, k, st);
+    } else {
+      // the weights' sums first: dx may be written over x or dy
+      if (a.partial != nullptr) {
+        *partials = partialRows(rows, k);
+        if (a.cols >= V)
+          hipLaunchKernelGGL((layerNormWeightSums<DT, false>), dim3((a.cols / V + kLnBlock - 1) / kLnBlock, *partials),
+                             dim3(kLnBlock), 0, st, a);
+        if (a.cols % V != 0)
+          hipLaunchKernelGGL((layerNormWeightSums<DT, true>), dim3(1, *partials), dim3(kLnBlock), 0, st, a);
+      }
+      if (a.y[firstRank(a)] != nullptr) {
+        const int block = a.cols < V ? 64 : 1024;
+        const int most = (a.cols < V ? 32 : 8) * kOpsCUs;
+        const dim3 grid((unsigned)(rows < most ? rows : most));
+        if (a.cols < V) hipLaunchKernelGGL((layerNormBackwardRows<DT, WT, 64>), grid, dim3(block), 0, st, a);
+        else hipLaunchKernelGGL((layerNormBackwardRows<DT, WT, 1024>), grid, dim3(block), 0, st, a);
+      }
+    }
+    const hipError_t err = hipGetLastError();
+    return *partials < 0 ? hipErrorInvalidValue : err;
+  }
+  static int firstRank(const LnArgs& a) {
+    int r = 0;
+    while (a.rowStart[r + 1] == 0) ++r;
+    return r;
   }
 };
 
 template <int DT, int WT>
 struct WeightGrads {
   static hipError_t run(const LnSumArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL((layerNormWeightGrads<WT>), dim3((a.cols + kLnBlock - 1) / kLnBlock), dim3(kLnBlock), 0, st,
+    hipLaunchKernelGGL((layerNormWeightGrads<WT>), dim3((a.cols + kSumCols - 1) / kSumCols, 2), dim3(kSumBlock), 0, st,
                        a);
     return hipGetLastError();
   }
@@ -549,9 +893,19 @@ arResult_t forward(const void* const* x, const void* const* gamma, const void* c
 arResult_t workspaceBytes(const size_t* rows, int nranks, size_t cols, size_t* bytes) {
   Shape s;
   if (bytes == nullptr || !shapeOk(rows, nranks, cols, &s)) return arInvalidArgument;
-  size_t n = 0;
-  for (int l = 0; l < s.launches; ++l) n += (size_t)partialRows(rowsOfLaunch(rows, nranks, l * kLnRanks));
-  *bytes = n * 2 * cols * sizeof(float);
+  // the element type is not known here: the larger of both cuts
+  size_t most = 0;
+  for (int esz = 2; esz <= 4; esz += 2) {
+    const BackwardCut k = backwardCut((int)cols, esz);
+    size_t n = 0;
+    for (int l = 0; l < s.launches; ++l) {
+      const int64_t launchRows = rowsOfLaunch(rows, nranks, l * kLnRanks);
+      const int blocks = launchRows > 0 ? partialRows(launchRows, k) : 0;
+      n += (size_t)(blocks > 0 && blocks < kLnRanks ? kLnRanks : blocks);   // one at least for each rank with rows
+    }
+    most = n > most ? n : most;
+  }
+  *bytes = (most > 0 ? most : 1) * 2 * ((cols + 3) / 4 * 4) * sizeof(float);
   return arSuccess;
 }
 
@@ -598,7 +952,7 @@ arResult_t backward(const void* const* dy, const void* const* x, const void* con
     LnArgs a{};
     fillRows(&a, rows, nranks, first);
     const int64_t n = a.rowStart[a.nranks];
-    if (n == 0 && !weights) continue;
+    if (n == 0) continue;
     for (int r = 0; r < a.nranks; ++r) {
       if (rows[first + r] == 0) continue;
       a.x[r] = x[first + r];
@@ -612,10 +966,12 @@ arResult_t backward(const void* const* dy, const void* const* x, const void* con
     a.dyStride = (int64_t)dyStride;
     a.yStride = (int64_t)dxStride;
     a.cols = (int)cols;
-    if (weights) a.partial = (float*)workspace + (size_t)nPartial * 2 * cols;
-    nPartial += partialRows(n);
-    if (byTypes<Backward, const LnArgs&, bool, hipStream_t>(dtype, wtype, a, dx != nullptr, st) != hipSuccess)
+    a.partialCols = (int)((cols + 3) / 4 * 4);
+    if (weights) a.partial = (float*)workspace + (size_t)nPartial * 2 * a.partialCols;
+    int partials = 0;
+    if (byTypes<Backward, const LnArgs&, int*, hipStream_t>(dtype, wtype, a, &partials, st) != hipSuccess)
       return arHipError;
+    nPartial += partials;
   }
   if (!weights) return arSuccess;
   LnSumArgs g{};
@@ -625,6 +981,7 @@ arResult_t backward(const void* const* dy, const void* const* x, const void* con
   }
   g.partial = (const float*)workspace;
   g.nPartial = nPartial;
+  g.partialCols = (int)((cols + 3) / 4 * 4);
   g.nranks = nranks;
   g.cols = (int)cols;
   return byTypes<WeightGrads, const LnSumArgs&, hipStream_t>(dtype, wtype, g, st) == hipSuccess ? arSuccess

@@ -54,32 +54,43 @@ __device__ __forceinline__ void storeStream(T* p, typename VecOf<T, V>::type v) 
   __builtin_nontemporal_store(v, (typename VecOf<T, V>::packed*)p);
 }
 
-template <int CTRL>
+// v plus what lane permutation CTRL brings, in the rows of ROWS.
+template <int CTRL, int ROWS = 0xf>
 __device__ __forceinline__ float addDpp(float v) {
-  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, true));
 }
 
-// Sum over a wavefront or its halves or quarters of 16 or 32 lanes; every lane
-// of the part receives it.  Lanes swap inside rows of 16 (quads, then the half
-// row and row mirrored: the other half's sum is the same in each of its lanes
-// by then), then the rows' sums are swapped or read across.  The order is
-// fixed and the same for every lane.
-template <int LANES>
-__device__ __forceinline__ float laneSum(float v) {
-  static_assert(LANES == 16 || LANES == 32 || LANES == 64, "parts of a wavefront");
+// Sum over rows of 16 lanes; every lane receives its row's.  Lanes swap in
+// quads, then with the half row and the row mirrored: the other half's sum is
+// the same in each of its lanes by then.  The order is fixed and the same for
+// every lane.
+__device__ __forceinline__ float rowSum(float v) {
   v = addDpp<0xb1>(v);    // quad_perm 1,0,3,2
   v = addDpp<0x4e>(v);    // quad_perm 2,3,0,1
   v = addDpp<0x141>(v);   // row_half_mirror
-  v = addDpp<0x140>(v);   // row_mirror
-  const int b = __builtin_bit_cast(int, v);
-  if (LANES == 32) return v + __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(b, 0x401f));   // lane ^ 16
+  return addDpp<0x140>(v);   // row_mirror
+}
+
+// Sum over a wavefront, right in its last lane: row 0's sum is passed to row 1
+// and row 2's to row 3, then row 1's to row 3.
+__device__ __forceinline__ float waveSumLast(float v) {
+  v = rowSum(v);
+  v = addDpp<0x142, 0xa>(v);      // row_bcast 15
+  return addDpp<0x143, 0xc>(v);   // row_bcast 31
+}
+
+// Sum over a wavefront or its halves or quarters of 16 or 32 lanes; every lane
+// of the part receives it.
+template <int LANES>
+__device__ __forceinline__ float laneSum(float v) {
+  static_assert(LANES == 16 || LANES == 32 || LANES == 64, "parts of a wavefront");
   if (LANES == 64) {
-    const float r0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0));
-    const float r1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16));
-    const float r2 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32));
-    const float r3 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 48));
-    return (r0 + r1) + (r2 + r3);
+    const int all = __builtin_bit_cast(int, waveSumLast(v));
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(all, 63));
   }
+  v = rowSum(v);
+  if (LANES == 32)   // with lane ^ 16
+    v += __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(__builtin_bit_cast(int, v), 0x401f));
   return v;
 }
 
