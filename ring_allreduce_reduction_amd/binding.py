@@ -1,4 +1,5 @@
-"""ctypes binding of libar.so -- argument marshalling only.
+"""ctypes binding of libar.so -- argument marshalling only (the operators' tensor
+lists are read by a small extension module, ar_torch.cpp).
 
 Every function here has the C ABI's name (include/ar.h) and passes plain
 pointers and sizes through; all work runs in the library's HIP kernels.
@@ -6,6 +7,7 @@ PyTorch is used only for device memory and streams.  Loading fails loudly if
 the library has not been built: there is no fallback path.
 """
 import ctypes
+import importlib.util
 import os
 
 import torch  # noqa: F401  -- loads the HIP runtime the library must share
@@ -436,8 +438,30 @@ def arDestroy(comm):
 _FLOAT_DTYPES = {torch.float32: arFloat32, torch.float16: arFloat16, torch.bfloat16: arBfloat16}
 
 
+_torch_calls_module = None
+
+
+def _torch_calls():
+    """The extension module that reads the operators' tensors (ar_torch.cpp), with libar.so's entry points."""
+    global _torch_calls_module
+    if _torch_calls_module is None:
+        L = lib()
+        path = os.path.join(HERE, "_ar_torch.so")
+        if not os.path.exists(path):
+            raise ImportError("_ar_torch.so is not built (run __graft_entry__.build() or "
+                              "python ring_allreduce_reduction_amd/build.py)")
+        spec = importlib.util.spec_from_file_location("_ar_torch", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in
+                      (L.arLayerNorm, L.arLayerNormBackward, L.arLayerNormBackwardWorkspace, L.arGradNorm,
+                       L.arGradClip)])
+        _torch_calls_module = module
+    return _torch_calls_module
+
+
 def _on_device(tensors):
-    """Every tensor of a call lives on torch's current device: the kernels run there."""
+    """Every tensor of a list lives on torch's current device: the kernels run there."""
     dev = None
     for t in tensors:
         if t.device.type != "cuda":
@@ -459,73 +483,6 @@ def _workspace(nbytes, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
 
 
-def _check_workspace(workspace, nbytes):
-    if not workspace.is_contiguous() or workspace.numel() * workspace.element_size() < nbytes:
-        raise ValueError("the workspace must be contiguous and hold %d bytes" % nbytes)
-    if workspace.data_ptr() % 16:
-        raise ValueError("the workspace must be 16-byte aligned")
-
-
-def _row_views(what, tensors, n, cols, dtype, rows=None):
-    """(rows, stride) of the ranks' row buffers: each (..., cols), contiguous or 2-D with unit column stride and
-    a row stride that all ranks share."""
-    if len(tensors) != n:
-        raise ValueError("need %d %s buffers, got %d" % (n, what, len(tensors)))
-    out, stride = [], None
-    for r, t in enumerate(tensors):
-        shape = t.shape
-        if not shape or shape[-1] != cols:
-            raise ValueError("%s buffer %d has shape %s, expected rows of %d" % (what, r, tuple(shape), cols))
-        if t.dtype != dtype:
-            raise ValueError("%s buffer %d is %s, expected %s like the others" % (what, r, t.dtype, dtype))
-        k = shape[0] if len(shape) == 2 else t.numel() // cols
-        if rows is not None and k != rows[r]:
-            raise ValueError("%s buffer %d has %d rows, expected %d" % (what, r, k, rows[r]))
-        if k > 1 or not t.is_contiguous():
-            if t.is_contiguous():
-                s = cols
-            elif len(shape) == 2 and (cols == 1 or t.stride(1) == 1) and (k <= 1 or t.stride(0) >= cols):
-                s = t.stride(0) if k > 1 else None
-            else:
-                raise ValueError("%s buffer %d must have contiguous rows" % (what, r))
-            if s is not None:
-                if stride is None:
-                    stride = s
-                elif stride != s:
-                    raise ValueError("%s buffer %d has row stride %d, the others %d" % (what, r, s, stride))
-        out.append(k)
-    return out, (cols if stride is None else stride)
-
-
-def _flat_bufs(what, tensors, n, sizes, dtype):
-    if len(tensors) != n:
-        raise ValueError("need %d %s buffers, got %d" % (n, what, len(tensors)))
-    for r, t in enumerate(tensors):
-        if t.dtype != dtype:
-            raise ValueError("%s buffer %d is %s, expected %s" % (what, r, t.dtype, dtype))
-        if not t.is_contiguous() or t.numel() != sizes[r]:
-            raise ValueError("%s buffer %d must hold %d contiguous elements" % (what, r, sizes[r]))
-
-
-def _norm_types(xs, weights):
-    """The element types of rows and weights, and the shared width."""
-    if not xs:
-        raise ValueError("need at least one rank")
-    x = xs[0]
-    if x.dtype not in _FLOAT_DTYPES or x.dim() < 1:
-        raise ValueError("rows must be float32, float16 or bfloat16 tensors of at least one dimension")
-    if x.shape[-1] < 1:
-        raise ValueError("rows must have at least one column")
-    wt = x.dtype
-    for w in weights:
-        if w:
-            wt = w[0].dtype
-            break
-    if wt != x.dtype and wt != torch.float32:
-        raise ValueError("weights must be %s or float32, got %s" % (x.dtype, wt))
-    return x.dtype, wt, x.shape[-1]
-
-
 def _arr(tensors):
     return None if tensors is None else (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
 
@@ -534,26 +491,9 @@ def arLayerNorm(xs, ys, gammas=None, betas=None, means=None, rstds=None, eps=1e-
     """Layer norm of every rank's rows.  xs, ys: one tensor per rank, (..., cols), contiguous or 2-D with padded
     rows (one row stride for all ranks of a list); gammas, betas: the ranks' weights, of the rows' type or
     float32; means, rstds: float32 tensors of one element per row, for arLayerNormBackward.  ys may be xs."""
-    n = len(xs)
-    dt, wt, cols = _norm_types(xs, (gammas, betas))
-    rows, xs_stride = _row_views("input", xs, n, cols, dt)
-    _, ys_stride = _row_views("output", ys, n, cols, dt, rows)
-    if (means is None) != (rstds is None):
-        raise ValueError("give both means and rstds or neither")
-    seen = list(xs) + list(ys)
-    for what, w in (("gamma", gammas), ("beta", betas)):
-        if w is not None:
-            _flat_bufs(what, w, n, [cols] * n, wt)
-            seen += w
-    if means is not None:
-        _flat_bufs("mean", means, n, rows, torch.float32)
-        _flat_bufs("rstd", rstds, n, rows, torch.float32)
-        seen += list(means) + list(rstds)
-    _on_device(seen)
-    _check(lib().arLayerNorm(_arr(xs), _arr(gammas), _arr(betas), _arr(ys), _arr(means), _arr(rstds),
-                             (ctypes.c_size_t * n)(*rows), n, cols, xs_stride, ys_stride, float(eps),
-                             _FLOAT_DTYPES[dt], _FLOAT_DTYPES[wt], ctypes.c_void_p(_stream_handle(stream))),
-           "arLayerNorm")
+    rc = _torch_calls().layer_norm(xs, ys, gammas, betas, means, rstds, float(eps), stream)
+    if rc:
+        _check(rc, "arLayerNorm")
 
 
 def arLayerNormBackwardWorkspace(rows, cols):
@@ -569,31 +509,12 @@ def arLayerNormBackward(dys, xs, means, rstds, gammas=None, dxs=None, dgammas=No
     """The gradients of arLayerNorm from its inputs and statistics: dxs (may be dys or xs, or None), and dgammas /
     dbetas (or None), each rank's copy of the sums over all ranks' rows.  workspace: a device tensor of
     arLayerNormBackwardWorkspace bytes that no other running call uses; None allocates one."""
-    n = len(xs)
-    dt, wt, cols = _norm_types(xs, (gammas, dgammas, dbetas))
-    rows, xs_stride = _row_views("input", xs, n, cols, dt)
-    _, dys_stride = _row_views("output gradient", dys, n, cols, dt, rows)
-    dxs_stride = cols if dxs is None else _row_views("input gradient", dxs, n, cols, dt, rows)[1]
-    _flat_bufs("mean", means, n, rows, torch.float32)
-    _flat_bufs("rstd", rstds, n, rows, torch.float32)
-    seen = list(xs) + list(dys) + list(means) + list(rstds) + (list(dxs) if dxs is not None else [])
-    for what, w in (("gamma", gammas), ("gamma gradient", dgammas), ("beta gradient", dbetas)):
-        if w is not None:
-            _flat_bufs(what, w, n, [cols] * n, wt)
-            seen += w
-    _on_device(seen)
-    need, ws = 0, None
-    if dgammas is not None or dbetas is not None:
-        need = arLayerNormBackwardWorkspace(rows, cols)
-        if workspace is None:
-            workspace = _workspace(need, stream)
-        _on_device((workspace,))
-        _check_workspace(workspace, need)
-        ws = workspace.data_ptr()
-    _check(lib().arLayerNormBackward(_arr(dys), _arr(xs), _arr(gammas), _arr(means), _arr(rstds), _arr(dxs),
-                                     _arr(dgammas), _arr(dbetas), (ctypes.c_size_t * n)(*rows), n, cols, dys_stride,
-                                     xs_stride, dxs_stride, _FLOAT_DTYPES[dt], _FLOAT_DTYPES[wt], ws, need,
-                                     ctypes.c_void_p(_stream_handle(stream))), "arLayerNormBackward")
+    call = _torch_calls().layer_norm_backward
+    rc = call(dys, xs, means, rstds, gammas, dxs, dgammas, dbetas, workspace, stream)
+    if rc < 0:   # the bytes of the workspace that is missing
+        rc = call(dys, xs, means, rstds, gammas, dxs, dgammas, dbetas, _workspace(-rc, stream), stream)
+    if rc:
+        _check(rc, "arLayerNormBackward")
 
 
 def arTensorListCreate(srcs, dsts=None):
@@ -660,35 +581,28 @@ class TensorList:
             pass
 
 
-def _norm_call_args(lst, kind, norm, workspace, stream):
+def _grad_call(lst, kind, scale, maxNorm, eps, norm, workspace, stream, where):
     if not isinstance(lst, TensorList) or lst.handle is None:
         raise ValueError("need an open TensorList")
-    if norm is not None:
-        if norm.dtype != torch.float32 or norm.numel() != 1:
-            raise ValueError("norm must be a float32 tensor of one element")
-        _on_device((norm,))
     if workspace is None:
         workspace = _workspace(lst.workspace_bytes, stream)
-    else:
-        _on_device((workspace,))
-        _check_workspace(workspace, lst.workspace_bytes)
-    return (NORM_BY_NAME[kind] if isinstance(kind, str) else int(kind), None if norm is None else norm.data_ptr(),
-            workspace.data_ptr(), ctypes.c_void_p(_stream_handle(stream)))
+    rc = _torch_calls().grad_norm(lst.handle.value, lst.workspace_bytes,
+                                  NORM_BY_NAME[kind] if isinstance(kind, str) else kind, float(scale), maxNorm,
+                                  float(eps), norm, workspace, stream)
+    if rc:
+        _check(rc, where)
 
 
 def arGradNorm(lst, norm, kind=arNorm2, scale=1.0, workspace=None, stream=None):
     """norm (float32, one element) = |scale| * the norm over every element of the TensorList's tensors.
     workspace: a device tensor of lst.workspace() bytes that no other running call uses; None allocates one."""
-    k, p, w, s = _norm_call_args(lst, kind, norm, workspace, stream)
-    _check(lib().arGradNorm(lst.handle, k, float(scale), p, w, lst.workspace_bytes, s), "arGradNorm")
+    _grad_call(lst, kind, scale, None, 0.0, norm, workspace, stream, "arGradNorm")
 
 
 def arGradClip(lst, norm, maxNorm, eps=1e-6, kind=arNorm2, scale=1.0, workspace=None, stream=None):
     """The norm, and every tensor times scale * min(1, maxNorm / (norm + eps)) into the list's outputs.  norm may
     be None."""
-    k, p, w, s = _norm_call_args(lst, kind, norm, workspace, stream)
-    _check(lib().arGradClip(lst.handle, k, float(scale), float(maxNorm), float(eps), p, w, lst.workspace_bytes, s),
-           "arGradClip")
+    _grad_call(lst, kind, scale, float(maxNorm), eps, norm, workspace, stream, "arGradClip")
 
 
 class Comm:

@@ -90,8 +90,32 @@ def build(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(LIB + ".tmp", LIB)
+    build_torch_calls(verbose)
     build_probe(verbose)
     return LIB
+
+
+TORCH_CALLS = os.path.join(HERE, "_ar_torch.so")
+
+
+def build_torch_calls(verbose: bool = False) -> str:
+    """The extension module that reads torch tensors for binding.py (host code only)."""
+    import sysconfig
+    import torch
+    t = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(),
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(rocm, "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(t, "include"),
+           "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           os.path.join(CSRC, "ar_torch.cpp"), "-L" + os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
+           "-L" + ROCM_LIB, "-lamdhip64", "-Wl,-rpath," + ROCM_LIB, "-o", TORCH_CALLS + ".tmp"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(TORCH_CALLS + ".tmp", TORCH_CALLS)
+    return TORCH_CALLS
 
 
 PROBE_LIB = os.path.join(HERE, "libstream_ceiling.so")
