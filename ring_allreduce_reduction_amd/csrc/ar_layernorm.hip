@@ -50,6 +50,13 @@ struct LnSumArgs {
   int cols;
 };
 
+struct LnFewArgs {
+  LnArgs rows;
+  void* dgamma[kLnRanks];         // null pointers: not wanted
+  void* dbeta[kLnRanks];
+  int dxRows;                     // workgroups that write dx
+};
+
 __device__ __forceinline__ float blockSum(float v, float* lds) {
   v = waveSum(v);
   __syncthreads();                // lds may still be read from the sum before
@@ -479,59 +486,62 @@ layerNormBackwardInRegisters(const LnArgs a) {
   }
 }
 
-// Rows too wide for registers, or narrower than a vector: a workgroup per row,
-// read twice.
+// dx of a row, by a workgroup that reads the row twice.
 template <int DT, int WT, int BLOCK>
-__global__ void __launch_bounds__(BLOCK) layerNormBackwardRows(const LnArgs a) {
+__device__ __forceinline__ void backwardRow(const LnArgs& a, int64_t row, float* lds) {
   typedef typename Elem<DT>::type T;
   typedef typename Elem<WT>::type W;
   constexpr int V = kVec<DT>;
   typedef typename VecOf<T, V>::type Vec;
   typedef typename VecOf<W, V>::type WVec;
+  const int r = rankOfRow(a, row);
+  const int64_t i = row - a.rowStart[r];
+  const T* x = (const T*)a.x[r] + i * a.xStride;
+  const T* dy = (const T*)a.dy[r] + i * a.dyStride;
+  T* dx = (T*)a.y[r] + i * a.yStride;
+  const W* gamma = (const W*)a.gamma[r];
+  const float mean = a.mean[r][i], rstd = a.rstd[r][i];
+  float s = 0.0f, u = 0.0f;
+  forRow<V, BLOCK>(a.cols,
+                   [&](int c) {
+                     const Vec v = loadVec<T, V>(x + c), o = loadVec<T, V>(dy + c);
+                     const WVec g = gamma ? loadVec<W, V>(gamma + c) : (WVec)(W)1.0f;
+#pragma unroll
+                     for (int e = 0; e < V; ++e) {
+                       const float q = (float)o[e] * (float)g[e];
+                       s += q;
+                       u = fmaf(q, ((float)v[e] - mean) * rstd, u);
+                     }
+                   },
+                   [&](int c) {
+                     const float q = (float)dy[c] * (gamma ? (float)gamma[c] : 1.0f);
+                     s += q;
+                     u = fmaf(q, ((float)x[c] - mean) * rstd, u);
+                   });
+  s = blockSum(s, lds) / (float)a.cols;
+  u = blockSum(u, lds) / (float)a.cols;
+  forRow<V, BLOCK>(a.cols,
+                   [&](int c) {
+                     const Vec v = loadVec<T, V>(x + c), o = loadVec<T, V>(dy + c);
+                     const WVec g = gamma ? loadVec<W, V>(gamma + c) : (WVec)(W)1.0f;
+                     FloatVec<V> d;
+#pragma unroll
+                     for (int e = 0; e < V; ++e)
+                       d[e] = rstd * fmaf(-(((float)v[e] - mean) * rstd), u, fmaf((float)o[e], (float)g[e], -s));
+                     storeVec<T, V>(dx + c, __builtin_convertvector(d, Vec));
+                   },
+                   [&](int c) {
+                     dx[c] = (T)(rstd * fmaf(-(((float)x[c] - mean) * rstd), u,
+                                             fmaf((float)dy[c], gamma ? (float)gamma[c] : 1.0f, -s)));
+                   });
+}
+
+// Rows too wide for registers, or narrower than a vector.
+template <int DT, int WT, int BLOCK>
+__global__ void __launch_bounds__(BLOCK) layerNormBackwardRows(const LnArgs a) {
   __shared__ float lds[BLOCK / kWave];
   const int64_t rows = a.rowStart[a.nranks];
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int r = rankOfRow(a, row);
-    const int64_t i = row - a.rowStart[r];
-    const T* x = (const T*)a.x[r] + i * a.xStride;
-    const T* dy = (const T*)a.dy[r] + i * a.dyStride;
-    T* dx = (T*)a.y[r] + i * a.yStride;
-    const W* gamma = (const W*)a.gamma[r];
-    const float mean = a.mean[r][i], rstd = a.rstd[r][i];
-    float s = 0.0f, u = 0.0f;
-    forRow<V, BLOCK>(a.cols,
-                     [&](int c) {
-                       const Vec v = loadVec<T, V>(x + c), o = loadVec<T, V>(dy + c);
-                       const WVec g = gamma ? loadVec<W, V>(gamma + c) : (WVec)(W)1.0f;
-#pragma unroll
-                       for (int e = 0; e < V; ++e) {
-                         const float q = (float)o[e] * (float)g[e];
-                         s += q;
-                         u = fmaf(q, ((float)v[e] - mean) * rstd, u);
-                       }
-                     },
-                     [&](int c) {
-                       const float q = (float)dy[c] * (gamma ? (float)gamma[c] : 1.0f);
-                       s += q;
-                       u = fmaf(q, ((float)x[c] - mean) * rstd, u);
-                     });
-    s = blockSum(s, lds) / (float)a.cols;
-    u = blockSum(u, lds) / (float)a.cols;
-    forRow<V, BLOCK>(a.cols,
-                     [&](int c) {
-                       const Vec v = loadVec<T, V>(x + c), o = loadVec<T, V>(dy + c);
-                       const WVec g = gamma ? loadVec<W, V>(gamma + c) : (WVec)(W)1.0f;
-                       FloatVec<V> d;
-#pragma unroll
-                       for (int e = 0; e < V; ++e)
-                         d[e] = rstd * fmaf(-(((float)v[e] - mean) * rstd), u, fmaf((float)o[e], (float)g[e], -s));
-                       storeVec<T, V>(dx + c, __builtin_convertvector(d, Vec));
-                     },
-                     [&](int c) {
-                       dx[c] = (T)(rstd * fmaf(-(((float)x[c] - mean) * rstd), u,
-                                               fmaf((float)dy[c], gamma ? (float)gamma[c] : 1.0f, -s)));
-                     });
-  }
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) backwardRow<DT, WT, BLOCK>(a, row, lds);
 }
 
 // The weights' sums of such rows: a wavefront per vector of columns and slice of
@@ -569,6 +579,78 @@ __global__ void __launch_bounds__(kLnBlock) layerNormWeightSums(const LnArgs a) 
   for (int e = 0; e < V; ++e) {
     p[e] = dg[e];
     p[a.partialCols + e] = db[e];
+  }
+}
+
+// Few rows in one launch: the first workgroups take a row each and write dx,
+// the others take 8 vectors of columns and add all rows up (32 slices of them,
+// joined through LDS).  Everything is read twice, from the caches, but no
+// partial sums leave a workgroup.  dx must not be written over x or dy.  256
+// rows of 768 to 8192 columns bf16 4.3-7.1 us, 6.9-15.3 in two launches; 512
+// rows 5.3-10.5 and 6.2-16.9; 1024 rows of 256 columns 8.4 and 6.6: no more
+// than 512 rows come here.
+constexpr int kFewRows = 512;
+constexpr int kFewLanes = 8, kFewSlices = kLnBlock / kFewLanes;
+
+template <int DT, int WT>
+__global__ void __launch_bounds__(kLnBlock) layerNormBackwardFew(const LnFewArgs w) {
+  const LnArgs& a = w.rows;
+  typedef typename Elem<DT>::type T;
+  typedef typename Elem<WT>::type W;
+  constexpr int V = kVec<DT>;
+  typedef typename VecOf<T, V>::type Vec;
+  struct RowAt {
+    const T *x, *dy;
+    const float *mean, *rstd;
+  };
+  __shared__ float sums[2][kFewSlices][kFewLanes * V];
+  __shared__ RowAt at[kFewRows];
+  if ((int)blockIdx.x < w.dxRows) {
+    backwardRow<DT, WT, kLnBlock>(a, blockIdx.x, &sums[0][0][0]);
+    return;
+  }
+  // where each row lies, so that rows of all ranks are read side by side
+  for (int r = 0; r < a.nranks; ++r) {
+    const int from = (int)a.rowStart[r], rows = (int)a.rowStart[r + 1] - from;
+    for (int i = threadIdx.x; i < rows; i += kLnBlock)
+      at[from + i] = RowAt{(const T*)a.x[r] + i * a.xStride, (const T*)a.dy[r] + i * a.dyStride, a.mean[r] + i,
+                           a.rstd[r] + i};
+  }
+  __syncthreads();
+  const int rows = (int)a.rowStart[a.nranks];
+  const int lane = threadIdx.x % kFewLanes, slice = threadIdx.x / kFewLanes;
+  const int first = ((int)blockIdx.x - w.dxRows) * kFewLanes * V;
+  // the last vector is moved back to end with the row; a column then summed
+  // twice has the same sum twice
+  const int c = first + lane * V > a.cols - V ? a.cols - V : first + lane * V;
+  FloatVec<V> dg = (FloatVec<V>)0.0f, db = (FloatVec<V>)0.0f;
+#pragma unroll 4
+  for (int i = slice; i < rows; i += kFewSlices) {
+    const RowAt p = at[i];
+    const Vec v = loadVec<T, V>(p.x + c), o = loadVec<T, V>(p.dy + c);
+    const float mean = *p.mean, rstd = *p.rstd;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      dg[e] = fmaf((float)o[e] * ((float)v[e] - mean), rstd, dg[e]);
+      db[e] += (float)o[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    sums[0][slice][lane * V + e] = dg[e];
+    sums[1][slice][lane * V + e] = db[e];
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < 2 * kFewLanes * V; k += kLnBlock) {
+    const int which = k / (kFewLanes * V), i = k % (kFewLanes * V);
+    const int from = first + i / V * V;
+    const int col = (from > a.cols - V ? a.cols - V : from) + i % V;
+    void* const* out = which == 0 ? w.dgamma : w.dbeta;
+    if (out[0] == nullptr) continue;
+    float all = 0.0f;
+#pragma unroll
+    for (int s = 0; s < kFewSlices; ++s) all += sums[which][s][i];
+    for (int r = 0; r < a.nranks; ++r) ((W*)out[r])[col] = (W)all;
   }
 }
 
@@ -828,6 +910,16 @@ struct Backward {
 };
 
 template <int DT, int WT>
+struct BackwardFew {
+  static hipError_t run(const LnFewArgs& w, hipStream_t st) {
+    constexpr int V = kVec<DT>;
+    const int across = (w.rows.cols + kFewLanes * V - 1) / (kFewLanes * V);
+    hipLaunchKernelGGL((layerNormBackwardFew<DT, WT>), dim3(w.dxRows + across), dim3(kLnBlock), 0, st, w);
+    return hipGetLastError();
+  }
+};
+
+template <int DT, int WT>
 struct WeightGrads {
   static hipError_t run(const LnSumArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((layerNormWeightGrads<WT>), dim3((a.cols + kSumCols - 1) / kSumCols, 2), dim3(kSumBlock), 0, st,
@@ -946,10 +1038,14 @@ arResult_t backward(const void* const* dy, const void* const* x, const void* con
     if (!ok) return arInvalidArgument;
   }
   if (outputsOverlap(v)) return arInvalidArgument;
+  bool inPlace = false;
+  for (int r = 0; dx != nullptr && r < nranks; ++r)
+    inPlace = inPlace || (rows[r] > 0 && (dx[r] == x[r] || dx[r] == dy[r]));
   int nPartial = 0;
   for (int l = 0; l < s.launches; ++l) {
     const int first = l * kLnRanks;
-    LnArgs a{};
+    LnFewArgs w{};
+    LnArgs& a = w.rows;
     fillRows(&a, rows, nranks, first);
     const int64_t n = a.rowStart[a.nranks];
     if (n == 0) continue;
@@ -967,6 +1063,15 @@ arResult_t backward(const void* const* dy, const void* const* x, const void* con
     a.yStride = (int64_t)dxStride;
     a.cols = (int)cols;
     a.partialCols = (int)((cols + 3) / 4 * 4);
+    if (weights && s.launches == 1 && !inPlace && n <= kFewRows && (int)cols >= 16 / esz) {
+      for (int r = 0; r < nranks; ++r) {
+        w.dgamma[r] = dgamma ? dgamma[r] : nullptr;
+        w.dbeta[r] = dbeta ? dbeta[r] : nullptr;
+      }
+      w.dxRows = dx != nullptr ? (int)n : 0;
+      return byTypes<BackwardFew, const LnFewArgs&, hipStream_t>(dtype, wtype, w, st) == hipSuccess ? arSuccess
+                                                                                                  : arHipError;
+    }
     if (weights) a.partial = (float*)workspace + (size_t)nPartial * 2 * a.partialCols;
     int partials = 0;
     if (byTypes<Backward, const LnArgs&, int*, hipStream_t>(dtype, wtype, a, &partials, st) != hipSuccess)

@@ -326,3 +326,12 @@ def test_single_rows_of_other_shapes(B):
     y = torch.empty(2, 3, 40, device="cuda")
     B.arLayerNorm([x.view(2, 3, 40).cuda()], [y])
     check_forward([x], None, None, 1e-5, [y.view(6, 40)], None, None)
+
+
+@pytest.mark.parametrize("rows", [[511], [512], [513], [500, 12], [500, 13, 0], [16] * 32, [16] * 33, [1, 0, 511, 0]], ids=str)
+@pytest.mark.parametrize("cols,dt", [(8, torch.bfloat16), (200, torch.bfloat16), (1031, torch.float32)], ids=str)
+def test_around_the_few_rows_rule(B, rows, cols, dt):
+    """Both sides of the row count where the weights' gradients change from one launch to two."""
+    xs, dys, gam, _ = inputs(rows, cols, dt, torch.float32, sum(rows) + cols)
+    check_backward(dys, xs, gam, *run_backward(B, dys, xs, gam, 1e-5))
+    check_backward(dys, xs, gam, *run_backward(B, dys, xs, gam, 1e-5, dx=False))
