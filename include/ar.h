@@ -638,6 +638,7 @@ typedef enum {
  * Squares are formed and summed in 64 bits: no value of any type overflows or
  * vanishes.  A NaN or infinity among the values gives a NaN or infinite norm.
  * An empty list has norm 0.  The device must be the list's (arInvalidUsage).
+ * norm and the workspace must not overlap each other or any listed tensor.
  */
 arResult_t arGradNorm(arTensorList_t list, arNormKind_t kind, float scale, float* norm, void* workspace,
                       size_t workspaceBytes, void* stream);

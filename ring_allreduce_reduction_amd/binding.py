@@ -435,9 +435,6 @@ def arDestroy(comm):
 
 # ---------------------------------------------------------------- operators around the AllReduce
 
-_FLOAT_DTYPES = {torch.float32: arFloat32, torch.float16: arFloat16, torch.bfloat16: arBfloat16}
-
-
 _torch_calls_module = None
 
 
@@ -454,22 +451,10 @@ def _torch_calls():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in
-                      (L.arLayerNorm, L.arLayerNormBackward, L.arLayerNormBackwardWorkspace, L.arGradNorm,
-                       L.arGradClip)])
+                      (L.arLayerNorm, L.arLayerNormBackward, L.arLayerNormBackwardWorkspace, L.arTensorListCreate,
+                       L.arGradNorm, L.arGradClip)])
         _torch_calls_module = module
     return _torch_calls_module
-
-
-def _on_device(tensors):
-    """Every tensor of a list lives on torch's current device: the kernels run there."""
-    dev = None
-    for t in tensors:
-        if t.device.type != "cuda":
-            raise ValueError("operator tensors must be device tensors, got one on %s" % t.device)
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.device.index != dev:
-            raise ValueError("a tensor is on %s, the current device is cuda:%d" % (t.device, dev))
 
 
 def _workspace(nbytes, stream):
@@ -481,10 +466,6 @@ def _workspace(nbytes, stream):
         stream = torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-
-
-def _arr(tensors):
-    return None if tensors is None else (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
 
 
 def arLayerNorm(xs, ys, gammas=None, betas=None, means=None, rstds=None, eps=1e-5, stream=None):
@@ -519,24 +500,9 @@ def arLayerNormBackward(dys, xs, means, rstds, gammas=None, dxs=None, dgammas=No
 
 def arTensorListCreate(srcs, dsts=None):
     """A list handle over contiguous device tensors; dsts: where arGradClip writes (srcs itself: in place)."""
-    n = len(srcs)
-    if dsts is not None and len(dsts) != n:
-        raise ValueError("need %d outputs, got %d" % (n, len(dsts)))
-    dtypes = []
-    for i, t in enumerate(srcs):
-        if t.dtype not in _FLOAT_DTYPES:
-            raise ValueError("tensor %d is %s" % (i, t.dtype))
-        dtypes.append(_FLOAT_DTYPES[t.dtype])
-        for what, q in (("tensor", t),) + ((("output", dsts[i]),) if dsts is not None else ()):
-            if not q.is_contiguous() or q.dtype != t.dtype or q.numel() != t.numel():
-                raise ValueError("%s %d must hold %d contiguous elements of %s" % (what, i, t.numel(), t.dtype))
-    _on_device(srcs)
-    _on_device(dsts or ())
-    h = ctypes.c_void_p()
-    _check(lib().arTensorListCreate(ctypes.byref(h), n, _arr(srcs), _arr(dsts),
-                                    (ctypes.c_size_t * n)(*[t.numel() for t in srcs]), (ctypes.c_int * n)(*dtypes)),
-           "arTensorListCreate")
-    return h
+    rc, handle = _torch_calls().tensor_list(srcs, dsts)
+    _check(rc, "arTensorListCreate")
+    return ctypes.c_void_p(handle)
 
 
 def arTensorListWorkspace(handle):

@@ -379,6 +379,8 @@ arResult_t runNorm(arTensorList* l, bool clip, int kind, float scale, float maxN
   if (clip && (!(maxNorm >= 0.0f) || !(eps >= 0.0f) || !std::isfinite(eps))) return arInvalidArgument;
   if (workspace == nullptr || (uintptr_t)workspace % 16 != 0 || workspaceBytes < listWorkspace(l))
     return arInvalidArgument;
+  const uintptr_t n = (uintptr_t)norm, w = (uintptr_t)workspace;
+  if (n + sizeof(float) > w && n < w + listWorkspace(l)) return arInvalidArgument;
   if (groupOpen() || (clip && !l->outputs)) return arInvalidUsage;
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return arHipError;

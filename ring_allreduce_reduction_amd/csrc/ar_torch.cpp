@@ -14,6 +14,8 @@
 #include <hip/hip_runtime_api.h>
 #include <stdint.h>
 
+#include <vector>
+
 #include "ar.h"
 
 namespace {
@@ -26,12 +28,15 @@ typedef arResult_t (*LayerNormBackwardFn)(const void* const*, const void* const*
                                           void* const*, const size_t*, int, size_t, size_t, size_t, size_t,
                                           arDataType_t, arDataType_t, void*, size_t, void*);
 typedef arResult_t (*WorkspaceFn)(const size_t*, int, size_t, size_t*);
+typedef arResult_t (*ListCreateFn)(arTensorList_t*, int, const void* const*, void* const*, const size_t*,
+                                   const arDataType_t*);
 typedef arResult_t (*GradNormFn)(arTensorList_t, arNormKind_t, float, float*, void*, size_t, void*);
 typedef arResult_t (*GradClipFn)(arTensorList_t, arNormKind_t, float, float, float, float*, void*, size_t, void*);
 
 LayerNormFn gLayerNorm;
 LayerNormBackwardFn gLayerNormBackward;
 WorkspaceFn gWorkspace;
+ListCreateFn gListCreate;
 GradNormFn gGradNorm;
 GradClipFn gGradClip;
 
@@ -72,6 +77,7 @@ struct Devices {
       anyHost = true;
       return;
     }
+    if (t.is_neg()) fail("a tensor is a lazy negation: call resolve_neg() first");
     const int d = t.get_device();
     if (current < 0 && hipGetDevice(&current) != hipSuccess) current = -1;
     if (d != current) other = d;
@@ -82,17 +88,17 @@ struct Devices {
   }
 };
 
-// A list or tuple of tensors, one a rank.
+// A list or tuple of tensors, one a rank unless `most` says otherwise.
 struct List {
   PyObject* fast = nullptr;
   int n = 0;
-  explicit List(PyObject* o) {
+  explicit List(PyObject* o, Py_ssize_t most = AR_MAX_RANKS) {
     fast = PySequence_Fast(o, "expected a list of tensors");
     if (fast == nullptr) throw PythonError();
     const Py_ssize_t size = PySequence_Fast_GET_SIZE(fast);
-    if (size > AR_MAX_RANKS) {
+    if (size > most) {
       Py_CLEAR(fast);
-      fail("at most %d ranks, got %zd", AR_MAX_RANKS, size);
+      fail("at most %zd tensors, got %zd", most, size);
     }
     n = (int)size;
   }
@@ -238,18 +244,19 @@ bool arguments(Py_ssize_t given, Py_ssize_t want) {
 }
 
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind takes five addresses");
+  if (n != 6) {
+    PyErr_SetString(PyExc_TypeError, "bind takes six addresses");
     return nullptr;
   }
-  void* p[5];
-  for (int i = 0; i < 5; ++i) p[i] = PyLong_AsVoidPtr(args[i]);
+  void* p[6];
+  for (int i = 0; i < 6; ++i) p[i] = PyLong_AsVoidPtr(args[i]);
   if (PyErr_Occurred()) return nullptr;
   gLayerNorm = (LayerNormFn)p[0];
   gLayerNormBackward = (LayerNormBackwardFn)p[1];
   gWorkspace = (WorkspaceFn)p[2];
-  gGradNorm = (GradNormFn)p[3];
-  gGradClip = (GradClipFn)p[4];
+  gListCreate = (ListCreateFn)p[3];
+  gGradNorm = (GradNormFn)p[4];
+  gGradClip = (GradClipFn)p[5];
   Py_RETURN_NONE;
 }
 
@@ -328,6 +335,50 @@ PyObject* layerNormBackward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// tensor_list(srcs, dsts or None) -> (result code, list address)
+PyObject* tensorList(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!arguments(n, 2)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    constexpr Py_ssize_t kMost = 1 << 20;
+    const List srcs(args[0], kMost);
+    const bool outputs = args[1] != Py_None;
+    std::vector<const void*> src((size_t)srcs.n);
+    std::vector<void*> dst(outputs ? (size_t)srcs.n + 1 : 0);   // never empty: null means no outputs
+    std::vector<size_t> counts((size_t)srcs.n);
+    std::vector<arDataType_t> types((size_t)srcs.n);
+    Devices devices;
+    for (int i = 0; i < srcs.n; ++i) {
+      const at::Tensor& t = srcs[i];
+      if (!floatType(t.scalar_type())) fail("tensor %d is %s", i, typeName(t.scalar_type()));
+      if (!t.is_contiguous())
+        fail("tensor %d must hold %lld contiguous elements of %s", i, (long long)t.numel(), typeName(t.scalar_type()));
+      devices.see(t);
+      src[(size_t)i] = t.data_ptr();
+      counts[(size_t)i] = (size_t)t.numel();
+      types[(size_t)i] = codeOf(t.scalar_type());
+    }
+    if (outputs) {
+      const List dsts(args[1], kMost);
+      if (dsts.n != srcs.n) fail("need %d outputs, got %d", srcs.n, dsts.n);
+      for (int i = 0; i < srcs.n; ++i) {
+        const at::Tensor &t = srcs[i], &o = dsts[i];
+        if (!o.is_contiguous() || o.scalar_type() != t.scalar_type() || o.numel() != t.numel())
+          fail("output %d must hold %lld contiguous elements of %s", i, (long long)t.numel(),
+               typeName(t.scalar_type()));
+        devices.see(o);
+        dst[(size_t)i] = o.data_ptr();
+      }
+    }
+    devices.check();
+    arTensorList_t list = nullptr;
+    const arResult_t r = gListCreate(&list, srcs.n, src.data(), outputs ? dst.data() : nullptr, counts.data(),
+                                     types.data());
+    PyObject* address = PyLong_FromVoidPtr(list);
+    if (address == nullptr) return nullptr;
+    return Py_BuildValue("(iN)", (int)r, address);
+  });
+}
+
 // grad_norm(list address, its workspace bytes, kind, scale, maxNorm or None, eps, norm, workspace, stream) ->
 // result code
 PyObject* gradNorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -363,6 +414,7 @@ PyObject* gradNorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
 PyMethodDef kMethods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
                           {"layer_norm", FAST(layerNorm), METH_FASTCALL, nullptr},
                           {"layer_norm_backward", FAST(layerNormBackward), METH_FASTCALL, nullptr},
+                          {"tensor_list", FAST(tensorList), METH_FASTCALL, nullptr},
                           {"grad_norm", FAST(gradNorm), METH_FASTCALL, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ar_torch", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -313,3 +313,33 @@ def test_around_the_launch_rules(B, tiles, kind):
         torch.cuda.synchronize()
     check_norm(norm, want)
     check_clip(outs, host, want, 1.0, 0.5 * want)
+
+
+def test_refusals_on_a_list(B):
+    t = torch.ones(100, device="cuda")
+    o = torch.empty_like(t)
+    norm = torch.empty(1, device="cuda")
+    with B.TensorList([t], [o]) as lst:
+        ws = torch.empty(lst.workspace(), dtype=torch.uint8, device="cuda")
+        for kw in (dict(maxNorm=-1.0), dict(maxNorm=math.nan), dict(maxNorm=1.0, eps=-1.0), dict(maxNorm=1.0, eps=math.inf),
+                   dict(maxNorm=1.0, scale=math.inf), dict(maxNorm=1.0, scale=math.nan), dict(maxNorm=1.0, kind=7)):
+            with pytest.raises(B.ArError):
+                B.arGradClip(lst, norm, workspace=ws, **kw)
+        with pytest.raises(B.ArError):
+            B.arGradNorm(lst, None)
+        with pytest.raises(B.ArError):
+            B.arGradNorm(lst, ws[:4].view(torch.float32), workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            B.arGradNorm(lst, norm, workspace=ws[:8])
+        with pytest.raises(ValueError, match="norm"):
+            B.arGradNorm(lst, torch.empty(2, device="cuda"), workspace=ws)
+        B.lib().arGroupStart()
+        with pytest.raises(B.ArError):
+            B.arGradNorm(lst, norm, workspace=ws)
+        assert B.lib().arGroupEnd() == B.arInvalidUsage
+    with pytest.raises(ValueError, match="open TensorList"):
+        B.arGradNorm(lst, norm)
+    big = torch.ones(200, device="cuda")
+    for dst in (big[50:150], big[100:]):   # over part of its own tensor, over the other one
+        with pytest.raises(B.ArError):
+            B.TensorList([big[:100], big[100:]], [dst, o[:100]])

@@ -335,3 +335,57 @@ def test_around_the_few_rows_rule(B, rows, cols, dt):
     xs, dys, gam, _ = inputs(rows, cols, dt, torch.float32, sum(rows) + cols)
     check_backward(dys, xs, gam, *run_backward(B, dys, xs, gam, 1e-5))
     check_backward(dys, xs, gam, *run_backward(B, dys, xs, gam, 1e-5, dx=False))
+
+
+def test_column_slices_of_one_buffer(B):
+    """Inputs and outputs as columns of the same rows: they interleave and do not overlap."""
+    xs, dys, gam, bet = inputs([20], 96, torch.bfloat16, torch.float32, 23)
+    wide = torch.full((20, 400), float("nan"), dtype=torch.bfloat16, device="cuda")
+    x, y, dy, dx = (wide[:, i:i + 96] for i in (0, 96, 200, 300))
+    x.copy_(xs[0])
+    dy.copy_(dys[0])
+    m, s = [torch.empty(20, device="cuda")], [torch.empty(20, device="cuda")]
+    B.arLayerNorm([x], [y], [gam[0].cuda()], [bet[0].cuda()], m, s)
+    gg, gb = [torch.empty(96, device="cuda")], [torch.empty(96, device="cuda")]
+    B.arLayerNormBackward([dy], [x], m, s, [gam[0].cuda()], [dx], gg, gb)
+    torch.cuda.synchronize()
+    check_forward(xs, gam, bet, 1e-5, [y.contiguous()], m, s)
+    check_backward(dys, xs, gam, [dx.contiguous()], gg, gb, [m[0].cpu()], [s[0].cpu()])
+    for lo, hi in ((192, 200), (296, 300), (396, 400)):
+        assert torch.isnan(wide[:, lo:hi].float()).all()
+    with pytest.raises(B.ArError):
+        B.arLayerNorm([x], [wide[:, 95:191]])
+
+
+def test_other_devices_and_lazy_negation_are_refused(B):
+    x = torch.zeros(2, 8, device="cuda")
+    with pytest.raises(ValueError, match="device tensors"):
+        B.arLayerNorm([x], [x], [torch.zeros(8)])
+    z = torch.zeros(2, 8, dtype=torch.complex64, device="cuda").conj().imag
+    assert z.is_neg()
+    with pytest.raises(ValueError):
+        B.arLayerNorm([z], [x])
+    with pytest.raises(ValueError, match="workspace"):
+        B.arLayerNormBackward([x], [x], [x[:, 0].contiguous()], [x[:, 0].contiguous()], None, None,
+                              [torch.zeros(8, device="cuda")], workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("rows,cols,wt", [(7, 300, torch.bfloat16), (700, 300, torch.bfloat16), (9, 20000, torch.float32)])
+def test_two_streams_at_once(B, rows, cols, wt):
+    """The same call on two streams side by side, each with a workspace of its own."""
+    sets = [inputs([rows], cols, torch.bfloat16, wt, 60 + i) for i in range(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    held = []
+    for xs, dys, gam, bet in sets:
+        means = [(xs[0].double()).mean(1).float()]
+        rstds = [torch.ones(rows)]
+        held.append(dict(x=[dev(xs[0])], dy=[dev(dys[0])], g=[dev(gam[0])], m=[dev(means[0])], s=[dev(rstds[0])],
+                         dx=[torch.empty_like(dev(xs[0]))], gg=[torch.empty(cols, dtype=wt, device="cuda")],
+                         gb=[torch.empty(cols, dtype=wt, device="cuda")], host=(means, rstds)))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for h, st in zip(held, streams):
+            B.arLayerNormBackward(h["dy"], h["x"], h["m"], h["s"], h["g"], h["dx"], h["gg"], h["gb"], stream=st)
+    torch.cuda.synchronize()
+    for h, (xs, dys, gam, bet) in zip(held, sets):
+        check_backward(dys, xs, gam, h["dx"], h["gg"], h["gb"], *h["host"])
