@@ -535,7 +535,7 @@ arResult_t arAllReduceNoAlloc(const void* const* sendbufs, void* const* recvbufs
 
 /*
  * arLayerNorm -- layer norm of every rank's rows in one launch (ranks beyond
- * 32 in further launches of 32):  with m the mean of a row of `cols` values
+ * 16 in further launches of 16):  with m the mean of a row of `cols` values
  * and v the mean of (x - m)^2,  rstd = 1 / sqrt(v + eps)  and
  * y = (x - m) * rstd * gamma + beta.
  *  x, y        (host arrays of nranks device pointers) rank r's rows[r] rows of
@@ -547,9 +547,9 @@ arResult_t arAllReduceNoAlloc(const void* const* sendbufs, void* const* recvbufs
  *              weights, `cols` elements of `wtype` (dtype or arFloat32).
  *  mean, rstd  (host arrays, both or neither NULL) rank r's rows[r] float
  *              statistics, for arLayerNormBackward.
- *  rows        (host, nranks) rows of each rank; a rank may have 0 (its
- *              pointers are not looked at then, those of dgamma and dbeta in
- *              arLayerNormBackward apart).
+ *  rows        (host, nranks) rows of each rank, at most 2^31-1 together; a
+ *              rank may have 0 (its pointers are not looked at then, those of
+ *              dgamma and dbeta in arLayerNormBackward apart).
  *  nranks      1..AR_MAX_RANKS.
  *  cols        1..2^30; strides at least cols.
  *  eps         finite, >= 0.

@@ -17,19 +17,21 @@
 namespace ar {
 namespace {
 
-constexpr int kLnRanks = 32;      // ranks per launch: their pointers travel in the kernel arguments
+// Ranks per launch: their pointers travel in the kernel arguments, which every
+// launch copies (1 KB; with 32 ranks' a one-row call took 0.4-1 us longer).
+constexpr int kLnRanks = 16;
 constexpr size_t kLnMaxCols = (size_t)1 << 30;
+constexpr int64_t kLnMaxRows = 0x7fffffff;   // of all ranks
 constexpr int kLnBlock = 256;
 
 struct LnArgs {
   const void* x[kLnRanks];
-  const void* dy[kLnRanks];
   const void* gamma[kLnRanks];
-  const void* beta[kLnRanks];
+  const void* other[kLnRanks];    // forward: beta, backward: dy
   void* y[kLnRanks];              // forward: y, backward: dx
   float* mean[kLnRanks];
   float* rstd[kLnRanks];
-  int64_t rowStart[kLnRanks + 1]; // rank r has rows [rowStart[r], rowStart[r + 1]) of the launch
+  int rowStart[kLnRanks + 1];     // rank r has rows [rowStart[r], rowStart[r + 1]) of the launch
   int blockStart[kLnRanks + 1];   // and workgroups [blockStart[r], blockStart[r + 1]), where they are shared out
   int64_t xStride, yStride, dyStride;
   int cols;
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(BLOCK) layerNormRows(const LnArgs a) {
     const T* x = (const T*)a.x[r] + i * a.xStride;
     T* y = (T*)a.y[r] + i * a.yStride;
     const W* gamma = (const W*)a.gamma[r];
-    const W* beta = (const W*)a.beta[r];
+    const W* beta = (const W*)a.other[r];
     float s = 0.0f;
     forRow<V, BLOCK>(a.cols,
                      [&](int c) {
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(THREADS < kLnBlock ? kLnBlock : THREADS) layer
     b[p] = (WVec)(W)0.0f;
   }
   if (a.gamma[r] != nullptr) pieces.template load<W, false>(g, (const W*)a.gamma[r]);
-  if (a.beta[r] != nullptr) pieces.template load<W, false>(b, (const W*)a.beta[r]);
+  if (a.other[r] != nullptr) pieces.template load<W, false>(b, (const W*)a.other[r]);
   const float inv = 1.0f / (float)a.cols;
   while (true) {
 #pragma unroll
@@ -386,7 +388,7 @@ layerNormBackwardInRegisters(const LnArgs a) {
   const RowPieces<NP, V> pieces(t, threads, a.cols);
   const OwnBits<DT> own(pieces.skip);
   const T* xs = (const T*)a.x[r];
-  const T* dys = (const T*)a.dy[r];
+  const T* dys = (const T*)a.other[r];
   T* dxs = (T*)a.y[r];
   const float* means = a.mean[r];
   const float* rstds = a.rstd[r];
@@ -497,7 +499,7 @@ __device__ __forceinline__ void backwardRow(const LnArgs& a, int64_t row, float*
   const int r = rankOfRow(a, row);
   const int64_t i = row - a.rowStart[r];
   const T* x = (const T*)a.x[r] + i * a.xStride;
-  const T* dy = (const T*)a.dy[r] + i * a.dyStride;
+  const T* dy = (const T*)a.other[r] + i * a.dyStride;
   T* dx = (T*)a.y[r] + i * a.yStride;
   const W* gamma = (const W*)a.gamma[r];
   const float mean = a.mean[r][i], rstd = a.rstd[r][i];
@@ -562,7 +564,7 @@ __global__ void __launch_bounds__(kLnBlock) layerNormWeightSums(const LnArgs a) 
     const int64_t from = (lo > a.rowStart[r] ? lo : a.rowStart[r]) - a.rowStart[r];
     const int64_t to = (hi < a.rowStart[r + 1] ? hi : a.rowStart[r + 1]) - a.rowStart[r];
     const T* x = (const T*)a.x[r] + c;
-    const T* dy = (const T*)a.dy[r] + c;
+    const T* dy = (const T*)a.other[r] + c;
 #pragma unroll 4
     for (int64_t i = from; i < to; ++i) {
       const Vec v = loadStream<T, V>(x + i * a.xStride), o = loadStream<T, V>(dy + i * a.dyStride);
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(kLnBlock) layerNormBackwardFew(const LnFewArgs
   for (int r = 0; r < a.nranks; ++r) {
     const int from = (int)a.rowStart[r], rows = (int)a.rowStart[r + 1] - from;
     for (int i = threadIdx.x; i < rows; i += kLnBlock)
-      at[from + i] = RowAt{(const T*)a.x[r] + i * a.xStride, (const T*)a.dy[r] + i * a.dyStride, a.mean[r] + i,
+      at[from + i] = RowAt{(const T*)a.x[r] + i * a.xStride, (const T*)a.other[r] + i * a.dyStride, a.mean[r] + i,
                            a.rstd[r] + i};
   }
   __syncthreads();
@@ -734,9 +736,10 @@ bool shapeOk(const size_t* rows, int nranks, size_t cols, Shape* s) {
   if (rows == nullptr || nranks < 1 || nranks > AR_MAX_RANKS || cols < 1 || cols > kLnMaxCols) return false;
   s->total = 0;
   for (int r = 0; r < nranks; ++r) {
-    if (rows[r] > (size_t)1 << 40) return false;
+    if (rows[r] > (size_t)kLnMaxRows) return false;
     s->total += (int64_t)rows[r];
   }
+  if (s->total > kLnMaxRows) return false;
   s->launches = (nranks + kLnRanks - 1) / kLnRanks;
   return true;
 }
@@ -931,7 +934,7 @@ struct WeightGrads {
 void fillRows(LnArgs* a, const size_t* rows, int nranks, int first) {
   a->nranks = nranks - first < kLnRanks ? nranks - first : kLnRanks;
   a->rowStart[0] = 0;
-  for (int r = 0; r < a->nranks; ++r) a->rowStart[r + 1] = a->rowStart[r] + (int64_t)rows[first + r];
+  for (int r = 0; r < a->nranks; ++r) a->rowStart[r + 1] = a->rowStart[r] + (int)rows[first + r];
 }
 
 arResult_t forward(const void* const* x, const void* const* gamma, const void* const* beta, void* const* y,
@@ -969,7 +972,7 @@ arResult_t forward(const void* const* x, const void* const* gamma, const void* c
       a.x[r] = x[first + r];
       a.y[r] = y[first + r];
       a.gamma[r] = gamma ? gamma[first + r] : nullptr;
-      a.beta[r] = beta ? beta[first + r] : nullptr;
+      a.other[r] = beta ? beta[first + r] : nullptr;
       a.mean[r] = mean ? mean[first + r] : nullptr;
       a.rstd[r] = rstd ? rstd[first + r] : nullptr;
     }
@@ -1052,7 +1055,7 @@ arResult_t backward(const void* const* dy, const void* const* x, const void* con
     for (int r = 0; r < a.nranks; ++r) {
       if (rows[first + r] == 0) continue;
       a.x[r] = x[first + r];
-      a.dy[r] = dy[first + r];
+      a.other[r] = dy[first + r];
       a.y[r] = dx ? dx[first + r] : nullptr;
       a.gamma[r] = gamma ? gamma[first + r] : nullptr;
       a.mean[r] = const_cast<float*>(mean[first + r]);

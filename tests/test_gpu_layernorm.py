@@ -145,9 +145,9 @@ def test_padded_rows_and_odd_addresses(B, cols, dt):
         check_backward(dys, xs, gam, *run_backward(B, dys, xs, gam, 1e-5, pad, offset))
 
 
-@pytest.mark.parametrize("n", [2, 32, 33, 72, 128])
+@pytest.mark.parametrize("n", [2, 16, 17, 32, 33, 72, 128])
 def test_many_ranks(B, n):
-    """Past 32 ranks the rows take several launches; ranks without rows still receive the weights' gradient."""
+    """Past 16 ranks the rows take several launches; ranks without rows still receive the weights' gradient."""
     rows = [(3 * r + 2) % 5 for r in range(n)]
     xs, dys, gam, bet = inputs(rows, 130, torch.float32, torch.float32, n)
     check_forward(xs, gam, bet, 1e-5, *run_forward(B, xs, gam, bet, 1e-5))
@@ -328,7 +328,7 @@ def test_single_rows_of_other_shapes(B):
     check_forward([x], None, None, 1e-5, [y.view(6, 40)], None, None)
 
 
-@pytest.mark.parametrize("rows", [[511], [512], [513], [500, 12], [500, 13, 0], [16] * 32, [16] * 33, [1, 0, 511, 0]], ids=str)
+@pytest.mark.parametrize("rows", [[511], [512], [513], [500, 12], [500, 13, 0], [32] * 16, [16] * 32, [16] * 33, [1, 0, 511, 0]], ids=str)
 @pytest.mark.parametrize("cols,dt", [(8, torch.bfloat16), (200, torch.bfloat16), (1031, torch.float32)], ids=str)
 def test_around_the_few_rows_rule(B, rows, cols, dt):
     """Both sides of the row count where the weights' gradients change from one launch to two."""

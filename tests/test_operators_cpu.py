@@ -49,7 +49,7 @@ def test_forward_refusals(B):
            dict(dtype=B.arUint64), dict(dtype=9), dict(wtype=B.arBfloat16), dict(dtype=B.arFloat16, wtype=B.arBfloat16),
            dict(x=None), dict(y=None), dict(x=P(0)), dict(y=P(0)), dict(x=P(BASE + 2)), dict(mean=P(3 * BASE)),
            dict(rstd=P(3 * BASE)), dict(gamma=P(0)), dict(beta=P(BASE + 1)), dict(mean=P(3 * BASE), rstd=P(0)),
-           dict(rows=N((1 << 40) + 1)), dict(rows=N(1 << 40), xs=1 << 32, ys=1 << 32)]
+           dict(rows=N(1 << 31)), dict(rows=N(1 << 30, 1 << 30), nranks=2, x=P(BASE, BASE), y=P(2 * BASE, 3 * BASE)), dict(rows=N(1 << 40), xs=1 << 32, ys=1 << 32)]
     for kw in bad:
         assert forward(B, **kw) == B.arInvalidArgument, kw
     # nothing to do
