@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(BLOCK) layerNormBackwardRows(const LnArgs a) {
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) backwardRow<DT, WT, BLOCK>(a, row, lds);
 }
 
-// The weights' sums of such rows: a wavefront per vector of columns and slice of
+// The weights' sums of such rows: a thread per vector of columns and slice of
 // the rows, four rows at a time; ONE takes single columns (rows of less than a
 // vector and the columns behind the last whole one).
 template <int DT, bool ONE>
@@ -613,13 +613,13 @@ __global__ void __launch_bounds__(kLnBlock) layerNormBackwardFew(const LnFewArgs
   }
   // where each row lies, so that rows of all ranks are read side by side
   for (int r = 0; r < a.nranks; ++r) {
-    const int from = (int)a.rowStart[r], rows = (int)a.rowStart[r + 1] - from;
+    const int from = a.rowStart[r], rows = a.rowStart[r + 1] - from;
     for (int i = threadIdx.x; i < rows; i += kLnBlock)
       at[from + i] = RowAt{(const T*)a.x[r] + i * a.xStride, (const T*)a.other[r] + i * a.dyStride, a.mean[r] + i,
                            a.rstd[r] + i};
   }
   __syncthreads();
-  const int rows = (int)a.rowStart[a.nranks];
+  const int rows = a.rowStart[a.nranks];
   const int lane = threadIdx.x % kFewLanes, slice = threadIdx.x / kFewLanes;
   const int first = ((int)blockIdx.x - w.dxRows) * kFewLanes * V;
   // the last vector is moved back to end with the row; a column then summed
@@ -777,8 +777,6 @@ hipError_t byTypes(int dtype, int wtype, A... args) {
   if (dtype == arFloat16) return F<arFloat16, arFloat16>::run(args...);
   return F<arBfloat16, arBfloat16>::run(args...);
 }
-
-int rowGrid(int64_t rows) { return (int)(rows < 8 * kOpsCUs ? rows : 8 * kOpsCUs); }
 
 // Shares `most` workgroups of `groups` rows at a time out among the ranks by
 // their rows, at least one to a rank with rows (so more than `most` only where

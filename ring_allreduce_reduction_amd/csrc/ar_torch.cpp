@@ -93,6 +93,7 @@ struct List {
   PyObject* fast = nullptr;
   int n = 0;
   explicit List(PyObject* o, Py_ssize_t most = AR_MAX_RANKS) {
+    if (THPVariable_Check(o)) fail("expected a list of tensors, got one tensor");   // it would be read row by row
     fast = PySequence_Fast(o, "expected a list of tensors");
     if (fast == nullptr) throw PythonError();
     const Py_ssize_t size = PySequence_Fast_GET_SIZE(fast);

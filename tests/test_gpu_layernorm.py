@@ -389,3 +389,14 @@ def test_two_streams_at_once(B, rows, cols, wt):
     torch.cuda.synchronize()
     for h, (xs, dys, gam, bet) in zip(held, sets):
         check_backward(dys, xs, gam, h["dx"], h["gg"], h["gb"], *h["host"])
+
+
+def test_streams_given_as_handles(B):
+    """A stream object, its raw handle, the default stream as 0, and none: torch's current stream."""
+    xs, dys, gam, bet = inputs([700, 9], 600, torch.float32, torch.float32, 71)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0, None):
+        check_forward(xs, gam, bet, 1e-5, *run_forward(B, xs, gam, bet, 1e-5, stream=stream))
+        check_backward(dys, xs, gam, *run_backward(B, dys, xs, gam, 1e-5, stream=stream))
+    with torch.cuda.stream(side):
+        check_backward(dys, xs, gam, *run_backward(B, dys, xs, gam, 1e-5))

@@ -144,6 +144,15 @@ def test_binding_refusals(B):
     x, w = torch.zeros(4, 8), torch.zeros(8)
     with pytest.raises(ValueError, match="at least one rank"):
         B.arLayerNorm([], [])
+    for args in ((x, [x]), ([x], x), ([x], [x], x)):
+        with pytest.raises(ValueError, match="got one tensor"):
+            B.arLayerNorm(*args)
+    with pytest.raises(TypeError, match="list of tensors"):
+        B.arLayerNorm(5, [x])
+    with pytest.raises(ValueError, match="expected a tensor"):
+        B.arLayerNorm([5], [x])
+    with pytest.raises(ValueError, match="at most 128"):
+        B.arLayerNorm([x] * 129, [x] * 129)
     with pytest.raises(ValueError, match="float32, float16 or bfloat16"):
         B.arLayerNorm([x.double()], [x.double()])
     with pytest.raises(ValueError, match="at least one column"):
