@@ -241,11 +241,12 @@ __device__ __forceinline__ void groupSum2(float& v, float& u, SumSlots& lds, int
 
 // DEPTH rows are in registers at once: while one is reduced the loads of the
 // others are in flight.  Bound by memory.  8 ranks of 4096 rows, 16-bit: 8192
-// columns 190 us (5.7 TB/s; a bare copy of as much runs at 6.2), 4096 99 us,
-// 2048 51 us; 200000 rows of 256 42 us, 2 ranks of 1000 rows of 32768 52 us.
+// columns 180 us (6.0 TB/s; a bare copy of as much runs at 6.2), 4096 95 us,
+// 2048 49 us; 200000 rows of 256 40 us, 2 ranks of 1000 rows of 32768 52 us.
 // With the launch's rows taken in turn by all groups instead of each rank's by
 // its own, 1024 columns took 67 us instead of 51 (every group met every rank's
-// weights); with a run of rows per group instead of turns 8192 took 208.
+// weights); with a run of rows per group instead of turns 8192 took 208
+// instead of 194 (both with the grid the GPU holds at once).
 template <int DT, int WT, int THREADS, int NP, int DEPTH>
 __global__ void __launch_bounds__(THREADS < kLnBlock ? kLnBlock : THREADS) layerNormInRegisters(const LnArgs a) {
   typedef typename Elem<DT>::type T;
@@ -364,7 +365,7 @@ struct OwnBits {
 // Bound by memory at 8192 columns (8 ranks of 4096 rows, bf16: 286-290 us, 5.6
 // TB/s, with the 8 us of the sums' kernel); a row costs a wavefront about 200
 // instructions at 8 values a thread, which shows where rows are short: 2048
-// columns 85 us for 403 MB, 128 columns 64 us for 310 MB.
+// columns 85 us for 403 MB, 128 columns 60 us for 310 MB.
 template <int DT, int WT, int THREADS, int NP, int DEPTH, int WAVES>
 __global__ void __launch_bounds__(THREADS < kLnBlock ? kLnBlock : THREADS) __attribute__((amdgpu_waves_per_eu(WAVES)))
 layerNormBackwardInRegisters(const LnArgs a) {
@@ -709,9 +710,12 @@ BackwardCut backwardCut(int cols, int esz) {
   // columns 155 with 512 x 1, 163 with 256 x 2.  About 12 wavefronts a CU: each
   // workgroup costs a row of partial sums to write and read (2048 columns 85
   // us, 88 with 20 wavefronts; 8192 columns fill a CU with one workgroup).
-  if (vecs <= 16) return {16, 1, 16, 4 * kOpsCUs};
-  if (vecs <= 32) return {32, 1, 8, 4 * kOpsCUs};
-  if (vecs <= 64) return {64, 1, 4, 4 * kOpsCUs};
+  // Narrow rows, one vector a thread: 256 columns 57 us with 2 workgroups of
+  // four wavefronts a CU, 73 with 1, 60 with 3, 63 with 4; two vectors: 1024
+  // columns 79 with 4 (three rows in flight; 81 with two), 85 with 3.
+  if (vecs <= 16) return {16, 1, 16, 2 * kOpsCUs};
+  if (vecs <= 32) return {32, 1, 8, 2 * kOpsCUs};
+  if (vecs <= 64) return {64, 1, 4, 2 * kOpsCUs};
   if (vecs <= 128) return {64, 2, 4, 4 * kOpsCUs};
   const int pieces = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : vecs <= 3072 ? 3 : 4;
   const int waves = ((vecs + pieces - 1) / pieces + kWave - 1) / kWave;
@@ -813,7 +817,19 @@ hipError_t launchForward(LnArgs a, hipStream_t st) {
       n = 1;
     return n;
   }();
-  const int grid = shareBlocks(&a, BLOCK / THREADS, resident * kOpsCUs);
+  // Many rows take several rounds of workgroups: they start in order and each
+  // as another ends, which keeps the window over memory closer than a lasting
+  // grid whose workgroups drift apart does (8 ranks x 4096 rows of 8192
+  // columns 194 us in one round, 189, 187, 180, 182 in 2, 4, 8, 16).  Each
+  // loads the weights again, so it gets 4 rows at least, 16 where a row is
+  // wider than 1024 vectors (16384 columns 98 us in one round, 97, 101, 106 in
+  // 2, 4, 8); rows that do not start at 16 bytes gain nothing (12000 of 5001
+  // columns 50 us, 55 in 2).
+  const int64_t each = a.rowStart[a.nranks] / ((int64_t)resident * kOpsCUs * (BLOCK / THREADS)) /
+                       (THREADS * NP > 1024 ? 16 : 4);
+  const bool aligned16 = (a.xStride | a.yStride) % kVec<DT> == 0;
+  const int rounds = !aligned16 || each < 1 ? 1 : each > 8 ? 8 : (int)each;
+  const int grid = shareBlocks(&a, BLOCK / THREADS, resident * kOpsCUs * rounds);
   hipLaunchKernelGGL((layerNormInRegisters<DT, WT, THREADS, NP, DEPTH>), dim3(grid), dim3(BLOCK), 0, st, a);
   return hipGetLastError();
 }
@@ -874,7 +890,7 @@ struct Backward {
     if (k.threads == 16) *partials = launchBackward<DT, WT, 16, 1, 2, 1>(a, k, st);
     else if (k.threads == 32) *partials = launchBackward<DT, WT, 32, 1, 2, 1>(a, k, st);
     else if (k.threads == 64 && k.pieces == 1) *partials = launchBackward<DT, WT, 64, 1, 2, 1>(a, k, st);
-    else if (k.threads == 64) *partials = launchBackward<DT, WT, 64, 2, 2, 3>(a, k, st);
+    else if (k.threads == 64) *partials = launchBackward<DT, WT, 64, 2, 3, 2>(a, k, st);
     else if (k.pieces == 1) *partials = k.threads <= 256   ? launchBackward<DT, WT, 256, 1, 3, 3>(a, k, st)
                                       : k.threads <= 512 ? launchBackward<DT, WT, 512, 1, 3, 3>(a, k, st)
                                                          : launchBackward<DT, WT, 1024, 1, 3, 4>(a, k, st);

@@ -400,3 +400,25 @@ def test_streams_given_as_handles(B):
         check_backward(dys, xs, gam, *run_backward(B, dys, xs, gam, 1e-5, stream=stream))
     with torch.cuda.stream(side):
         check_backward(dys, xs, gam, *run_backward(B, dys, xs, gam, 1e-5))
+
+
+@pytest.mark.parametrize("rows,cols,dt", [([40000], 64, torch.bfloat16), ([30000, 12345], 264, torch.bfloat16),
+                                          ([20011], 1032, torch.float32), ([7000, 3, 6500], 2056, torch.float16),
+                                          ([9001], 4104, torch.bfloat16)], ids=str)
+def test_several_rounds_of_workgroups(B, rows, cols, dt):
+    """Row counts past what the GPU holds at once, with a part round at the end: every row of every rank, checked on
+    the device against a 64-bit form (bounds as elsewhere)."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    xs = [torch.randn(k, cols, generator=g, device="cuda").to(dt) for k in rows]
+    gam = [torch.randn(cols, generator=g, device="cuda") for _ in rows]
+    bet = [torch.randn(cols, generator=g, device="cuda") for _ in rows]
+    ys = [torch.full_like(x, float("nan")) for x in xs]
+    m, s = [torch.full((k,), float("nan"), device="cuda") for k in rows], [torch.full((k,), float("nan"), device="cuda") for k in rows]
+    B.arLayerNorm(xs, ys, gam, bet, m, s)
+    for r, x in enumerate(xs):
+        for i in range(0, len(x), 4096):
+            part = slice(i, i + 4096)
+            want = ou.ln_forward(x[part].cpu(), gam[r].cpu(), bet[r].cpu(), 1e-5)
+            ou.within(ys[r][part], want[0], want[3], dt, "y of rank %d from row %d" % (r, i))
+            ou.within(m[r][part], want[1], want[4], torch.float32, "mean")
+            ou.within(s[r][part], want[2], want[5], torch.float32, "rstd")
