@@ -612,7 +612,7 @@ typedef struct arTensorList* arTensorList_t;
  * where they are while the list is used.  Allocates device memory (32 bytes a
  * tile) and copies to it synchronously: not for capture.
  * Errors: arInvalidArgument (bad pointers, counts, types; outputs that
- * overlap), arHipError, arSystemError.
+ * overlap; more than 2^25 tiles), arHipError, arSystemError.
  */
 arResult_t arTensorListCreate(arTensorList_t* list, int nTensors, const void* const* src, void* const* dst,
                               const size_t* counts, const arDataType_t* dtypes);

@@ -34,6 +34,7 @@ constexpr size_t kTileMax = 32 * 1024;
 // every workgroup still has at least eight or the list is all in flight at once.
 constexpr size_t kTileMin = 4096;
 constexpr int kTilesEach = 8;
+constexpr size_t kMostTiles = (size_t)1 << 25;   // 1 TiB of large tensors, 1 GiB of tiles
 // The second pass writes as much as it reads and likes more workgroups: 8 x
 // 128 MiB bf16 norm and clip 513 us with 16 a CU, 532 with 8, 550 with 4.
 constexpr int kClipGrid = 16 * kOpsCUs;
@@ -110,9 +111,9 @@ __device__ __forceinline__ double blockJoin(double v, double* lds) {
   return s;
 }
 
-// GROUP threads (a workgroup or a wavefront) add a tile: UN 16-byte loads a thread in flight; element e of
-// every vector adds to sum e % 4, so that four chains of additions run side
-// by side.
+// GROUP threads (a workgroup or a wavefront) add a tile: UN 16-byte loads a
+// thread in flight; element e of every vector adds to sum e % 4, so that four
+// chains of additions run side by side.
 template <int KIND, int DT, bool KEEP, int GROUP>
 __device__ __forceinline__ void addTile(typename Running<KIND>::type (&acc)[4], const Tile& g) {
   typedef typename Elem<DT>::type T;
@@ -278,12 +279,17 @@ namespace {
 
 bool listOk(const arTensorList* l) { return l != nullptr && (uintptr_t)l % 8 == 0 && l->magic == kListMagic; }
 
-void cutTiles(int nTensors, const void* const* src, void* const* dst, const size_t* counts,
+// False where the list would need more than kMostTiles.
+bool cutTiles(int nTensors, const void* const* src, void* const* dst, const size_t* counts,
               const arDataType_t* dtypes, std::vector<Tile>& tiles) {
   double bytes = 0.0;
   for (int i = 0; i < nTensors; ++i) bytes += (double)counts[i] * elemSize(dtypes[i]);
   size_t tile = kTileMin;
   while (tile < kTileMax && (double)tile * kTilesEach * kNormGrid < bytes) tile *= 2;
+  size_t need = 0;
+  for (int i = 0; i < nTensors; ++i) need += (counts[i] * (size_t)elemSize(dtypes[i]) + tile - 1) / tile;
+  if (need > kMostTiles) return false;
+  tiles.reserve(need);
   for (int i = 0; i < nTensors; ++i) {
     const size_t esz = (size_t)elemSize(dtypes[i]);
     for (size_t done = 0; done < counts[i]; done += tile / esz) {
@@ -295,6 +301,7 @@ void cutTiles(int nTensors, const void* const* src, void* const* dst, const size
       tiles.push_back(g);
     }
   }
+  return true;
 }
 
 arResult_t createList(arTensorList_t* out, int nTensors, const void* const* src, void* const* dst,
@@ -317,8 +324,7 @@ arResult_t createList(arTensorList_t* out, int nTensors, const void* const* src,
   }
   if (dst != nullptr && outputsOverlap(v)) return arInvalidArgument;
   std::vector<Tile> tiles;
-  cutTiles(nTensors, src, dst, counts, dtypes, tiles);
-  if (tiles.size() > (size_t)1 << 30) return arInvalidArgument;
+  if (!cutTiles(nTensors, src, dst, counts, dtypes, tiles)) return arInvalidArgument;
 
   int dev = 0, ndev = 0;
   if (hipGetDeviceCount(&ndev) != hipSuccess || ndev < 1) return arHipError;

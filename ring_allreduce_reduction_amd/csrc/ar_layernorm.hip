@@ -585,6 +585,19 @@ __global__ void __launch_bounds__(kLnBlock) layerNormWeightSums(const LnArgs a) 
   }
 }
 
+// The sum of N slices' values in eight chains, joined in pairs: an eighth of the
+// roundings of one chain.
+template <int N, typename F>
+__device__ __forceinline__ float joinSlices(F value) {
+  static_assert(N % 8 == 0, "eight chains");
+  float c[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) c[k] = value(k);
+#pragma unroll
+  for (int k = 8; k < N; ++k) c[k % 8] += value(k);
+  return ((c[0] + c[1]) + (c[2] + c[3])) + ((c[4] + c[5]) + (c[6] + c[7]));
+}
+
 // Few rows in one launch: the first workgroups take a row each and write dx,
 // the others take 8 vectors of columns and add all rows up (32 slices of them,
 // joined through LDS).  Everything is read twice, from the caches, but no
@@ -650,9 +663,7 @@ __global__ void __launch_bounds__(kLnBlock) layerNormBackwardFew(const LnFewArgs
     const int col = (from > a.cols - V ? a.cols - V : from) + i % V;
     void* const* out = which == 0 ? w.dgamma : w.dbeta;
     if (out[0] == nullptr) continue;
-    float all = 0.0f;
-#pragma unroll
-    for (int s = 0; s < kFewSlices; ++s) all += sums[which][s][i];
+    const float all = joinSlices<kFewSlices>([&](int s) { return sums[which][s][i]; });
     for (int r = 0; r < a.nranks; ++r) ((W*)out[r])[col] = (W)all;
   }
 }
@@ -681,9 +692,7 @@ __global__ void __launch_bounds__(kSumBlock) layerNormWeightGrads(const LnSumArg
   __syncthreads();
   const int col = (int)blockIdx.x * kSumCols + (int)threadIdx.x;
   if (threadIdx.x >= kSumCols || col >= a.cols) return;
-  float all = 0.0f;
-#pragma unroll 8
-  for (int k = 0; k < kSlices; ++k) all += lds[k][threadIdx.x];
+  const float all = joinSlices<kSlices>([&](int k) { return lds[k][threadIdx.x]; });
   for (int r = 0; r < a.nranks; ++r) ((W*)out[r])[col] = (W)all;
 }
 

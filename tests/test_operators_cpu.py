@@ -107,6 +107,7 @@ def test_list_refusals(B):
     bad = [dict(out=False), dict(n=-1), dict(n=(1 << 20) + 1), dict(src=None), dict(counts=None), dict(dtypes=None),
            dict(src=(0, BASE)), dict(src=(BASE + 2, 2 * BASE)), dict(dst=(0, BASE)), dict(dst=(3 * BASE + 1, 4 * BASE)),
            dict(dtypes=(0, 1)), dict(dtypes=(1, 4)), dict(counts=((1 << 40) + 1, 1)),
+           dict(counts=(1 << 40, 1)), dict(counts=(1 << 38, 1)),   # more tiles than a list may have
            # outputs over each other, another tensor, part of their own, the same tensor twice in place
            dict(dst=(3 * BASE, 3 * BASE + 16)), dict(dst=(2 * BASE, 3 * BASE)), dict(dst=(BASE + 4, 2 * BASE)),
            dict(src=(BASE, BASE), dst=(BASE, BASE))]
