@@ -39,6 +39,7 @@ struct LnArgs {
   float eps;
   float* partial;                 // backward: this launch's first row of partial sums, or null
   int partialCols;                // cols up to a multiple of 4
+  float* rowSums;                 // backward, rows that registers do not hold: two sums a row, or null
 };
 
 // The weights' gradients of every rank receive the same sums.
@@ -489,8 +490,9 @@ layerNormBackwardInRegisters(const LnArgs a) {
   }
 }
 
-// dx of a row, by a workgroup that reads the row twice.
-template <int DT, int WT, int BLOCK>
+// A workgroup's row: its sums s / C and u / C, and dx from them, for which the
+// row is read again, or (SUMS) the sums alone to rowSums.
+template <int DT, int WT, int BLOCK, bool SUMS>
 __device__ __forceinline__ void backwardRow(const LnArgs& a, int64_t row, float* lds) {
   typedef typename Elem<DT>::type T;
   typedef typename Elem<WT>::type W;
@@ -523,6 +525,13 @@ __device__ __forceinline__ void backwardRow(const LnArgs& a, int64_t row, float*
                    });
   s = blockSum(s, lds) / (float)a.cols;
   u = blockSum(u, lds) / (float)a.cols;
+  if (SUMS) {
+    if (threadIdx.x == 0) {
+      a.rowSums[2 * row] = s;
+      a.rowSums[2 * row + 1] = u;
+    }
+    return;
+  }
   forRow<V, BLOCK>(a.cols,
                    [&](int c) {
                      const Vec v = loadVec<T, V>(x + c), o = loadVec<T, V>(dy + c);
@@ -540,20 +549,25 @@ __device__ __forceinline__ void backwardRow(const LnArgs& a, int64_t row, float*
 }
 
 // Rows too wide for registers, or narrower than a vector.
-template <int DT, int WT, int BLOCK>
+template <int DT, int WT, int BLOCK, bool SUMS>
 __global__ void __launch_bounds__(BLOCK) layerNormBackwardRows(const LnArgs a) {
   __shared__ float lds[BLOCK / kWave];
   const int64_t rows = a.rowStart[a.nranks];
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) backwardRow<DT, WT, BLOCK>(a, row, lds);
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) backwardRow<DT, WT, BLOCK, SUMS>(a, row, lds);
 }
 
-// The weights' sums of such rows: a thread per vector of columns and slice of
-// the rows, four rows at a time; ONE takes single columns (rows of less than a
-// vector and the columns behind the last whole one).
-template <int DT, bool ONE>
-__global__ void __launch_bounds__(kLnBlock) layerNormWeightSums(const LnArgs a) {
+// The weights' sums of such rows, and dx where the rows' sums are given (so x and
+// dy are read twice in all: 2 ranks of 1000 rows of 40000 bf16 173 us; 210 with
+// dx from the rows' kernel and a third reading here): a thread
+// per vector of columns and slice of the rows, four rows at a time; ONE takes
+// single columns (rows of less than a vector and the columns behind the last
+// whole one).  dx may be written over x or dy: an element is read here by the
+// thread that writes it and by no other.
+template <int DT, int WT, bool ONE>
+__global__ void __launch_bounds__(kLnBlock) layerNormBackwardColumns(const LnArgs a) {
   typedef typename Elem<DT>::type T;
-  constexpr int V = ONE ? 1 : kVec<DT>;
+  typedef typename Elem<WT>::type W;
+  constexpr int V = ONE ? 1 : kVec<DT>, UN = 4;
   typedef typename VecOf<T, V>::type Vec;
   const int first = ONE ? a.cols / kVec<DT> * kVec<DT> : 0;
   const int c = first + ((int)blockIdx.x * kLnBlock + (int)threadIdx.x) * V;
@@ -564,16 +578,40 @@ __global__ void __launch_bounds__(kLnBlock) layerNormWeightSums(const LnArgs a) 
   for (int r = 0; r < a.nranks; ++r) {
     const int64_t from = (lo > a.rowStart[r] ? lo : a.rowStart[r]) - a.rowStart[r];
     const int64_t to = (hi < a.rowStart[r + 1] ? hi : a.rowStart[r + 1]) - a.rowStart[r];
+    if (from >= to) continue;
     const T* x = (const T*)a.x[r] + c;
     const T* dy = (const T*)a.other[r] + c;
-#pragma unroll 4
-    for (int64_t i = from; i < to; ++i) {
-      const Vec v = loadStream<T, V>(x + i * a.xStride), o = loadStream<T, V>(dy + i * a.dyStride);
-      const float mean = a.mean[r][i], rstd = a.rstd[r][i];
+    T* dx = (T*)a.y[r] + c;
+    FloatVec<V> g = (FloatVec<V>)1.0f;
+    if (a.gamma[r] != nullptr)
+      g = __builtin_convertvector((loadVec<W, V>((const W*)a.gamma[r] + c)), FloatVec<V>);
+    for (int64_t i = from; i < to; i += UN) {
+      Vec v[UN], o[UN];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        dg[e] = fmaf((float)o[e], ((float)v[e] - mean) * rstd, dg[e]);
-        db[e] += (float)o[e];
+      for (int k = 0; k < UN; ++k)
+        if (i + k < to) {
+          v[k] = loadStream<T, V>(x + (i + k) * a.xStride);
+          o[k] = loadStream<T, V>(dy + (i + k) * a.dyStride);
+        }
+#pragma unroll
+      for (int k = 0; k < UN; ++k) {
+        if (i + k >= to) break;
+        const float mean = a.mean[r][i + k], rstd = a.rstd[r][i + k];
+        float s = 0.0f, u = 0.0f;
+        if (a.rowSums != nullptr) {
+          s = a.rowSums[2 * (a.rowStart[r] + i + k)];
+          u = a.rowSums[2 * (a.rowStart[r] + i + k) + 1];
+        }
+        FloatVec<V> d;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float h = ((float)v[k][e] - mean) * rstd;
+          dg[e] = fmaf((float)o[k][e], h, dg[e]);
+          db[e] += (float)o[k][e];
+          d[e] = rstd * fmaf(-h, u, fmaf((float)o[k][e], g[e], -s));
+        }
+        if (a.rowSums != nullptr)
+          storeStream<T, V>(dx + (i + k) * a.yStride, __builtin_convertvector(d, Vec));
       }
     }
   }
@@ -622,7 +660,7 @@ __global__ void __launch_bounds__(kLnBlock) layerNormBackwardFew(const LnFewArgs
   __shared__ float sums[2][kFewSlices][kFewLanes * V];
   __shared__ RowAt at[kFewRows];
   if ((int)blockIdx.x < w.dxRows) {
-    backwardRow<DT, WT, kLnBlock>(a, blockIdx.x, &sums[0][0][0]);
+    backwardRow<DT, WT, kLnBlock, false>(a, blockIdx.x, &sums[0][0][0]);
     return;
   }
   // where each row lies, so that rows of all ranks are read side by side
@@ -708,8 +746,8 @@ struct BackwardCut {
 BackwardCut backwardCut(int cols, int esz) {
   const int V = 16 / esz, vecs = (cols + V - 1) / V;
   if (cols < V || vecs > (esz == 4 ? 4096 : 2048)) {
-    // 2 ranks of 1000 rows of 32768: the sums' kernels 59 us with 64 slices of
-    // the rows, 92 with 256
+    // the weights' sums alone of 2 ranks of 1000 rows of 32768: 59 us with 64
+    // slices of the rows, 92 with 256
     const int wide = (vecs + kLnBlock - 1) / kLnBlock;   // workgroups across the columns
     return {0, 0, 1, wide < 64 ? 4 * kOpsCUs / wide : 16};
   }
@@ -912,30 +950,27 @@ struct Backward {
       if constexpr (V == 4) *partials = k.pieces == 3 ? launchBackward<DT, WT, 1024, 3, 1, 4>(a, k, st)
                                                       : launchBackward<DT, WT, 1024, 4, 1, 4>(a, k, st);
     } else {
-      // the weights' sums first: dx may be written over x or dy
-      if (a.partial != nullptr) {
+      const int block = a.cols < V ? 64 : 1024;
+      const int most = (a.cols < V ? 32 : 8) * kOpsCUs;
+      const dim3 grid((unsigned)(rows < most ? rows : most));
+      if (a.partial == nullptr) {   // dx alone
+        if (a.cols < V) hipLaunchKernelGGL((layerNormBackwardRows<DT, WT, 64, false>), grid, dim3(block), 0, st, a);
+        else hipLaunchKernelGGL((layerNormBackwardRows<DT, WT, 1024, false>), grid, dim3(block), 0, st, a);
+      } else {
+        if (a.rowSums != nullptr) {
+          if (a.cols < V) hipLaunchKernelGGL((layerNormBackwardRows<DT, WT, 64, true>), grid, dim3(block), 0, st, a);
+          else hipLaunchKernelGGL((layerNormBackwardRows<DT, WT, 1024, true>), grid, dim3(block), 0, st, a);
+        }
         *partials = partialRows(rows, k);
         if (a.cols >= V)
-          hipLaunchKernelGGL((layerNormWeightSums<DT, false>), dim3((a.cols / V + kLnBlock - 1) / kLnBlock, *partials),
-                             dim3(kLnBlock), 0, st, a);
+          hipLaunchKernelGGL((layerNormBackwardColumns<DT, WT, false>),
+                             dim3((a.cols / V + kLnBlock - 1) / kLnBlock, *partials), dim3(kLnBlock), 0, st, a);
         if (a.cols % V != 0)
-          hipLaunchKernelGGL((layerNormWeightSums<DT, true>), dim3(1, *partials), dim3(kLnBlock), 0, st, a);
-      }
-      if (a.y[firstRank(a)] != nullptr) {
-        const int block = a.cols < V ? 64 : 1024;
-        const int most = (a.cols < V ? 32 : 8) * kOpsCUs;
-        const dim3 grid((unsigned)(rows < most ? rows : most));
-        if (a.cols < V) hipLaunchKernelGGL((layerNormBackwardRows<DT, WT, 64>), grid, dim3(block), 0, st, a);
-        else hipLaunchKernelGGL((layerNormBackwardRows<DT, WT, 1024>), grid, dim3(block), 0, st, a);
+          hipLaunchKernelGGL((layerNormBackwardColumns<DT, WT, true>), dim3(1, *partials), dim3(kLnBlock), 0, st, a);
       }
     }
     const hipError_t err = hipGetLastError();
     return *partials < 0 ? hipErrorInvalidValue : err;
-  }
-  static int firstRank(const LnArgs& a) {
-    int r = 0;
-    while (a.rowStart[r + 1] == 0) ++r;
-    return r;
   }
 };
 
@@ -1012,6 +1047,18 @@ arResult_t forward(const void* const* x, const void* const* gamma, const void* c
   return arSuccess;
 }
 
+// The workspace's end: two sums for each row of the largest launch, for widths
+// that are not held in registers with some element type.
+size_t rowSumsBytes(const size_t* rows, int nranks, int launches, int cols) {
+  if (backwardCut(cols, 2).threads != 0 && backwardCut(cols, 4).threads != 0) return 0;
+  int64_t most = 0;
+  for (int l = 0; l < launches; ++l) {
+    const int64_t n = rowsOfLaunch(rows, nranks, l * kLnRanks);
+    most = n > most ? n : most;
+  }
+  return ((size_t)most * 2 * sizeof(float) + 15) / 16 * 16;
+}
+
 arResult_t workspaceBytes(const size_t* rows, int nranks, size_t cols, size_t* bytes) {
   Shape s;
   if (bytes == nullptr || !shapeOk(rows, nranks, cols, &s)) return arInvalidArgument;
@@ -1027,7 +1074,8 @@ arResult_t workspaceBytes(const size_t* rows, int nranks, size_t cols, size_t* b
     }
     most = n > most ? n : most;
   }
-  *bytes = (most > 0 ? most : 1) * 2 * ((cols + 3) / 4 * 4) * sizeof(float);
+  *bytes = (most > 0 ? most : 1) * 2 * ((cols + 3) / 4 * 4) * sizeof(float) +
+           rowSumsBytes(rows, nranks, s.launches, (int)cols);
   return arSuccess;
 }
 
@@ -1102,7 +1150,12 @@ arResult_t backward(const void* const* dy, const void* const* x, const void* con
       return byTypes<BackwardFew, const LnFewArgs&, hipStream_t>(dtype, wtype, w, st) == hipSuccess ? arSuccess
                                                                                                   : arHipError;
     }
-    if (weights) a.partial = (float*)workspace + (size_t)nPartial * 2 * a.partialCols;
+    if (weights) {
+      a.partial = (float*)workspace + (size_t)nPartial * 2 * a.partialCols;
+      // launches follow each other on the stream and share the rows' sums at the workspace's end
+      if (dx != nullptr && backwardCut((int)cols, esz).threads == 0)
+        a.rowSums = (float*)((char*)workspace + need - rowSumsBytes(rows, nranks, s.launches, (int)cols));
+    }
     int partials = 0;
     if (byTypes<Backward, const LnArgs&, int*, hipStream_t>(dtype, wtype, a, &partials, st) != hipSuccess)
       return arHipError;

@@ -422,3 +422,14 @@ def test_several_rounds_of_workgroups(B, rows, cols, dt):
             ou.within(ys[r][part], want[0], want[3], dt, "y of rank %d from row %d" % (r, i))
             ou.within(m[r][part], want[1], want[4], torch.float32, "mean")
             ou.within(s[r][part], want[2], want[5], torch.float32, "rstd")
+
+
+@pytest.mark.parametrize("rows", [[520, 0, 30], [40] * 18], ids=["3 ranks", "18 ranks"])
+@pytest.mark.parametrize("cols,dt", [(5, torch.bfloat16), (16388, torch.bfloat16), (16391, torch.float32)], ids=str)
+def test_rows_that_registers_do_not_hold(B, rows, cols, dt):
+    """More than 512 rows of such widths, in one launch of ranks and in two, beside x and dy and over them."""
+    xs, dys, gam, _ = inputs(rows, cols, dt, torch.float32, 90 + cols)
+    for into in (None, "dy", "x"):
+        check_backward(dys, xs, gam, *run_backward(B, dys, xs, gam, 1e-5, pad=3, into=into))
+    check_backward(dys, xs, gam, *run_backward(B, dys, xs, gam, 1e-5, dx=False))
+    check_backward(dys, xs, gam, *run_backward(B, dys, xs, gam, 1e-5, dg=False, db=False))
