@@ -673,36 +673,39 @@ __global__ void __launch_bounds__(kLnBlock) layerNormBackwardFew(const LnFewArgs
   __syncthreads();
   const int rows = a.rowStart[a.nranks];
   const int lane = threadIdx.x % kFewLanes, slice = threadIdx.x / kFewLanes;
-  const int first = ((int)blockIdx.x - w.dxRows) * kFewLanes * V;
-  // the last vector is moved back to end with the row; a column then summed
-  // twice has the same sum twice
-  const int c = first + lane * V > a.cols - V ? a.cols - V : first + lane * V;
-  FloatVec<V> dg = (FloatVec<V>)0.0f, db = (FloatVec<V>)0.0f;
+  const int step = ((int)gridDim.x - w.dxRows) * kFewLanes * V;
+  for (int first = ((int)blockIdx.x - w.dxRows) * kFewLanes * V; first < a.cols; first += step) {
+    // the last vector is moved back to end with the row; a column then summed
+    // twice has the same sum twice
+    const int c = first + lane * V > a.cols - V ? a.cols - V : first + lane * V;
+    FloatVec<V> dg = (FloatVec<V>)0.0f, db = (FloatVec<V>)0.0f;
 #pragma unroll 4
-  for (int i = slice; i < rows; i += kFewSlices) {
-    const RowAt p = at[i];
-    const Vec v = loadVec<T, V>(p.x + c), o = loadVec<T, V>(p.dy + c);
-    const float mean = *p.mean, rstd = *p.rstd;
+    for (int i = slice; i < rows; i += kFewSlices) {
+      const RowAt p = at[i];
+      const Vec v = loadVec<T, V>(p.x + c), o = loadVec<T, V>(p.dy + c);
+      const float mean = *p.mean, rstd = *p.rstd;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        dg[e] = fmaf((float)o[e] * ((float)v[e] - mean), rstd, dg[e]);
+        db[e] += (float)o[e];
+      }
+    }
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      dg[e] = fmaf((float)o[e] * ((float)v[e] - mean), rstd, dg[e]);
-      db[e] += (float)o[e];
+      sums[0][slice][lane * V + e] = dg[e];
+      sums[1][slice][lane * V + e] = db[e];
     }
-  }
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    sums[0][slice][lane * V + e] = dg[e];
-    sums[1][slice][lane * V + e] = db[e];
-  }
-  __syncthreads();
-  for (int k = threadIdx.x; k < 2 * kFewLanes * V; k += kLnBlock) {
-    const int which = k / (kFewLanes * V), i = k % (kFewLanes * V);
-    const int from = first + i / V * V;
-    const int col = (from > a.cols - V ? a.cols - V : from) + i % V;
-    void* const* out = which == 0 ? w.dgamma : w.dbeta;
-    if (out[0] == nullptr) continue;
-    const float all = joinSlices<kFewSlices>([&](int s) { return sums[which][s][i]; });
-    for (int r = 0; r < a.nranks; ++r) ((W*)out[r])[col] = (W)all;
+    __syncthreads();
+    for (int k = threadIdx.x; k < 2 * kFewLanes * V; k += kLnBlock) {
+      const int which = k / (kFewLanes * V), i = k % (kFewLanes * V);
+      const int from = first + i / V * V;
+      const int col = (from > a.cols - V ? a.cols - V : from) + i % V;
+      void* const* out = which == 0 ? w.dgamma : w.dbeta;
+      if (out[0] == nullptr) continue;
+      const float all = joinSlices<kFewSlices>([&](int s) { return sums[which][s][i]; });
+      for (int r = 0; r < a.nranks; ++r) ((W*)out[r])[col] = (W)all;
+    }
+    __syncthreads();   // before the next columns' sums
   }
 }
 
@@ -718,20 +721,32 @@ __global__ void __launch_bounds__(kSumBlock) layerNormWeightGrads(const LnSumArg
   void* const* out = blockIdx.y == 0 ? a.dgamma : a.dbeta;
   if (out[0] == nullptr) return;
   const int lane = threadIdx.x % (kSumCols / 4), slice = threadIdx.x / (kSumCols / 4);
-  const int c = (int)blockIdx.x * kSumCols + lane * 4;
-  FloatVec<4> sum = (FloatVec<4>)0.0f;
-  if (c < a.cols) {
-    const float* p = a.partial + (size_t)blockIdx.y * a.partialCols + c;
+  for (int first = (int)blockIdx.x * kSumCols; first < a.cols; first += (int)gridDim.x * kSumCols) {
+    const int c = first + lane * 4;
+    FloatVec<4> sum = (FloatVec<4>)0.0f;
+    if (c < a.cols) {
+      const float* p = a.partial + (size_t)blockIdx.y * a.partialCols + c;
 #pragma unroll 4
-    for (int k = slice; k < a.nPartial; k += kSlices) sum += *(const FloatVec<4>*)(p + (size_t)k * 2 * a.partialCols);
-  }
+      for (int k = slice; k < a.nPartial; k += kSlices) sum += *(const FloatVec<4>*)(p + (size_t)k * 2 * a.partialCols);
+    }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) lds[slice][lane * 4 + e] = sum[e];
-  __syncthreads();
-  const int col = (int)blockIdx.x * kSumCols + (int)threadIdx.x;
-  if (threadIdx.x >= kSumCols || col >= a.cols) return;
-  const float all = joinSlices<kSlices>([&](int k) { return lds[k][threadIdx.x]; });
-  for (int r = 0; r < a.nranks; ++r) ((W*)out[r])[col] = (W)all;
+    for (int e = 0; e < 4; ++e) lds[slice][lane * 4 + e] = sum[e];
+    __syncthreads();
+    const int col = first + (int)threadIdx.x;
+    if (threadIdx.x < kSumCols && col < a.cols) {
+      const float all = joinSlices<kSlices>([&](int k) { return lds[k][threadIdx.x]; });
+      for (int r = 0; r < a.nranks; ++r) ((W*)out[r])[col] = (W)all;
+    }
+    __syncthreads();   // before the next columns' sums
+  }
+}
+
+// A launch holds fewer than 2^32 threads along its grid: `blocks` workgroups
+// of `block` threads, as many as fit into half of that.  The kernels of the
+// weights' gradients step through the columns that are left over.
+unsigned gridOf(int64_t blocks, int block) {
+  const int64_t most = ((int64_t)1 << 31) / block;
+  return (unsigned)(blocks < most ? blocks : most);
 }
 
 // How a backward launch is cut: `threads` threads hold a row, `pieces` vectors
@@ -978,8 +993,8 @@ template <int DT, int WT>
 struct BackwardFew {
   static hipError_t run(const LnFewArgs& w, hipStream_t st) {
     constexpr int V = kVec<DT>;
-    const int across = (w.rows.cols + kFewLanes * V - 1) / (kFewLanes * V);
-    hipLaunchKernelGGL((layerNormBackwardFew<DT, WT>), dim3(w.dxRows + across), dim3(kLnBlock), 0, st, w);
+    const unsigned across = gridOf((w.rows.cols + kFewLanes * V - 1) / (kFewLanes * V), kLnBlock);
+    hipLaunchKernelGGL((layerNormBackwardFew<DT, WT>), dim3((unsigned)w.dxRows + across), dim3(kLnBlock), 0, st, w);
     return hipGetLastError();
   }
 };
@@ -987,8 +1002,8 @@ struct BackwardFew {
 template <int DT, int WT>
 struct WeightGrads {
   static hipError_t run(const LnSumArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL((layerNormWeightGrads<WT>), dim3((a.cols + kSumCols - 1) / kSumCols, 2), dim3(kSumBlock), 0, st,
-                       a);
+    const unsigned across = gridOf((a.cols + kSumCols - 1) / kSumCols, kSumBlock);
+    hipLaunchKernelGGL((layerNormWeightGrads<WT>), dim3(across, 2), dim3(kSumBlock), 0, st, a);
     return hipGetLastError();
   }
 };
