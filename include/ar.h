@@ -553,6 +553,9 @@ arResult_t arAllReduceNoAlloc(const void* const* sendbufs, void* const* recvbufs
  *  nranks      1..AR_MAX_RANKS.
  *  cols        1..2^30; strides at least cols.
  *  eps         finite, >= 0.
+ * The statistics are 32-bit: a row whose sum passes 3.4e38 has an infinite
+ * mean, one whose squared deviations add up past it rstd 0; with eps 0 the
+ * deviations must be large enough for their squares too (above 1e-19).
  * Errors: arInvalidArgument (nothing enqueued), arInvalidUsage in an open
  * group, arHipError, arSystemError.
  */

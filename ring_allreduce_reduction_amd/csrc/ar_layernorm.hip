@@ -356,9 +356,11 @@ struct OwnBits {
   __device__ __forceinline__ Vec of(Vec v) const { return __builtin_bit_cast(Vec, __builtin_bit_cast(words, v) & bits); }
 };
 
-// The backward pass with a row's x and dy in registers.  With d = x - m:
-//   s = sum dy g,  u = sum dy d g,  dx = (r dy) g - d (r^3 u / C) - r s / C,
-//   dg += (dy d) r,  db += dy.
+// The backward pass with a row's x and dy in registers.  With h = (x - m) r:
+//   s = sum dy g,  u = sum dy g h,  dx = r (dy g - s / C - h u / C),
+//   dg += dy h,  db += dy.
+// h comes first: it is a number of ordinary size whatever the rows' spread,
+// where dy (x - m) and r r may pass the ends of a float.
 // A thread meets the same columns in every row, so it adds their weights'
 // gradients up in registers too; a workgroup's groups are joined through LDS at
 // the end, and each workgroup leaves one row of partial sums.  x - m is formed
@@ -421,17 +423,18 @@ layerNormBackwardInRegisters(const LnArgs a) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
       float s = 0.0f, u = 0.0f;
+      FloatVec<V> h[NP];
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         const Vec mine = p < NP - 1 ? dy[d][p] : own.of(dy[d][p]);
         float sp = 0.0f, up = 0.0f;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float o = (float)mine[e];
-          const float od = o * ((float)x[d][p][e] - mean[d]);
-          sp = fmaf(o, (float)g[p][e], sp);
-          up = fmaf(od, (float)g[p][e], up);
-          dg[p][e] = fmaf(od, rstd[d], dg[p][e]);
+          const float o = (float)mine[e], q = o * (float)g[p][e];
+          h[p][e] = ((float)x[d][p][e] - mean[d]) * rstd[d];
+          sp += q;
+          up = fmaf(q, h[p][e], up);
+          dg[p][e] = fmaf(o, h[p][e], dg[p][e]);
           db[p][e] += o;
         }
         s += sp;
@@ -439,14 +442,15 @@ layerNormBackwardInRegisters(const LnArgs a) {
       }
       if (dxs != nullptr) {
         groupSum2<THREADS>(s, u, lds, turn);
-        const float k1 = -rstd[d] * (s * inv), k2 = -(rstd[d] * rstd[d]) * (rstd[d] * (u * inv));
+        s *= inv;
+        u *= inv;
         T* dx = dxs + row * a.yStride;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           FloatVec<V> o;
 #pragma unroll
           for (int e = 0; e < V; ++e)
-            o[e] = fmaf((float)dy[d][p][e] * rstd[d], (float)g[p][e], fmaf((float)x[d][p][e] - mean[d], k2, k1));
+            o[e] = rstd[d] * fmaf(-h[p][e], u, fmaf((float)dy[d][p][e], (float)g[p][e], -s));
           pieces.template store<T>(p, dx, __builtin_convertvector(o, Vec));
         }
       }
@@ -686,7 +690,7 @@ __global__ void __launch_bounds__(kLnBlock) layerNormBackwardFew(const LnFewArgs
       const float mean = *p.mean, rstd = *p.rstd;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        dg[e] = fmaf((float)o[e] * ((float)v[e] - mean), rstd, dg[e]);
+        dg[e] = fmaf((float)o[e], ((float)v[e] - mean) * rstd, dg[e]);
         db[e] += (float)o[e];
       }
     }
