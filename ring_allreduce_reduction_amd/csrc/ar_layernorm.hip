@@ -3,8 +3,9 @@
 //
 // Forward, a row of C values:  m = sum x / C,  v = sum (x - m)^2 / C,
 // r = 1 / sqrt(v + eps),  y = (x - m) r g + b.  The variance is taken about
-// the mean (not as the mean square less the squared mean): a row with a large
-// offset loses nothing.
+// the mean (not as the mean square less the squared mean): a large offset costs
+// what rounding the sum and the mean to 32 bits costs, and no more.  Rows of one
+// value whose sums are exact come out as b.
 // Backward, h = (x - m) r, q = dy g:  dx = r (q - sum q / C - h sum(q h) / C),
 // dg = sum over rows of dy h,  db = sum over rows of dy.
 #include <new>
@@ -146,6 +147,11 @@ __global__ void __launch_bounds__(BLOCK) layerNormRows(const LnArgs a) {
   }
 }
 
+// v, the same in every lane, in a scalar register.
+__device__ __forceinline__ float uniform(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
+}
+
 // A group of THREADS threads (part of a wavefront, one, or a workgroup) owns whole
 // rows and keeps them in registers: thread t holds vectors t, t + THREADS, ...
 // of a row, NP of them, so memory is read once and written once.  All but the
@@ -280,7 +286,10 @@ __global__ void __launch_bounds__(THREADS < kLnBlock ? kLnBlock : THREADS) layer
   }
   if (a.gamma[r] != nullptr) pieces.template load<W, false>(g, (const W*)a.gamma[r]);
   if (a.other[r] != nullptr) pieces.template load<W, false>(b, (const W*)a.other[r]);
-  const float inv = 1.0f / (float)a.cols;
+  // These and the mean in scalar registers: with one vector register more the
+  // 512 x 2 layout holds 5 wavefronts a SIMD instead of 6 (8192 columns 189 us
+  // instead of 181).
+  const float cols = uniform((float)a.cols), inv = uniform(1.0f / cols);
   while (true) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
@@ -292,7 +301,8 @@ __global__ void __launch_bounds__(THREADS < kLnBlock ? kLnBlock : THREADS) layer
         for (int e = 0; e < V; ++e) u += pieces.owns(p, e) ? (float)x[d][p][e] : 0.0f;
         s += u;
       }
-      const float mean = groupSum<THREADS>(s, lds, turn) * inv;
+      const float quotient = groupSum<THREADS>(s, lds, turn) / cols;   // not s times 1 / cols: rounded once
+      const float mean = THREADS < kWave ? quotient : uniform(quotient);
       float q = 0.0f;
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
@@ -364,7 +374,7 @@ struct OwnBits {
 // A thread meets the same columns in every row, so it adds their weights'
 // gradients up in registers too; a workgroup's groups are joined through LDS at
 // the end, and each workgroup leaves one row of partial sums.  x - m is formed
-// as it stands, not as x r - m r: a row with a large offset loses nothing.
+// as it stands, not as x r - m r, which would cancel where the offset is large.
 // Bound by memory at 8192 columns (8 ranks of 4096 rows, bf16: 286-290 us, 5.6
 // TB/s, with the 8 us of the sums' kernel); a row costs a wavefront about 200
 // instructions at 8 values a thread, which shows where rows are short: 2048

@@ -1,0 +1,42 @@
+"""Layer norm forward: rows whose mean has to come out to the last bit."""
+import op_util as ou
+import pytest
+import test_gpu_layernorm as ln
+import torch
+
+pytestmark = pytest.mark.gpu
+
+# one width of each layout (16 x 1 up to 1024 x 4 vectors), where the product of the exact sum with a rounded
+# 1 / cols misses the mean of some of VALUES; less than a vector; past registers
+COLS = {torch.float32: [3, 61, 121, 237, 503, 751, 953, 2023, 2973, 4071, 6133, 8165, 12237, 16339, 16999],
+        torch.bfloat16: [7, 61, 237, 503, 953, 1531, 2023, 4071, 6133, 8165, 12237, 16339, 24557, 32747, 33383]}
+VALUES = [1.0, 5.0, 1000.0, -3.0, 0.0]
+
+
+@pytest.fixture(scope="module")
+def B():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from ring_allreduce_reduction_amd import binding
+    binding.lib()
+    return binding
+
+
+@pytest.fixture(autouse=True)
+def _named(request):
+    import gpu_util
+    gpu_util.note(request.node.name)
+
+
+@pytest.mark.parametrize("dt,cols", [(t, c) for t in COLS for c in COLS[t]], ids=str)
+def test_rows_of_one_value(B, dt, cols):
+    """Every partial sum is a value of at most 7 bits times a number up to 33383, which 24 bits hold: the mean is the
+    value, the variance 0, y beta."""
+    x = torch.tensor(VALUES).to(dt)[:, None].expand(len(VALUES), cols).contiguous()
+    g = torch.Generator().manual_seed(cols)
+    gam, bet = [ou.rows_of(g, (cols,), torch.float32, 0.3, 1.0)], [ou.rows_of(g, (cols,), torch.float32)]
+    ys, m, s = ln.run_forward(B, [x], gam, bet, 1e-5)
+    assert torch.equal(m[0].cpu(), torch.tensor(VALUES))
+    assert torch.equal(ys[0].cpu(), bet[0].to(dt).expand(len(VALUES), cols))
+    ou.within(s[0], torch.full((len(VALUES),), 1e-5, dtype=torch.float64).rsqrt(), 1e-5 ** -0.5 * 4 * ou.U,
+              torch.float32, "rstd")
