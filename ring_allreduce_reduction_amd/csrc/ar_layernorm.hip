@@ -91,7 +91,9 @@ __device__ __forceinline__ void forRow(int n, F f, G g) {
 // Rows too wide for registers, and rows of less than one vector: a workgroup
 // per row, which is read three times (from the caches after the first).  2
 // ranks of 1000 rows of 40000 bf16: 87 us with 1024 threads and 8 workgroups a
-// CU, 94 with 2, 106 with 512 threads, 117 with 256.
+// CU, 94 with 2, 106 with 512 threads, 117 with 256.  A thread adds its vectors'
+// sums up in 64 bits: a row of 2^20 columns is 1024 values a thread, whose
+// roundings to 32 bits moved the mean of a row of 1000.1 by 0.01.
 template <int DT, int WT, int BLOCK>
 __global__ void __launch_bounds__(BLOCK) layerNormRows(const LnArgs a) {
   typedef typename Elem<DT>::type T;
@@ -108,24 +110,28 @@ __global__ void __launch_bounds__(BLOCK) layerNormRows(const LnArgs a) {
     T* y = (T*)a.y[r] + i * a.yStride;
     const W* gamma = (const W*)a.gamma[r];
     const W* beta = (const W*)a.other[r];
-    float s = 0.0f;
+    double s = 0.0;
     forRow<V, BLOCK>(a.cols,
                      [&](int c) {
                        const Vec v = loadVec<T, V>(x + c);
+                       float u = 0.0f;
 #pragma unroll
-                       for (int e = 0; e < V; ++e) s += (float)v[e];
+                       for (int e = 0; e < V; ++e) u += (float)v[e];
+                       s += u;
                      },
                      [&](int c) { s += (float)x[c]; });
-    const float mean = blockSum(s, lds) / (float)a.cols;
-    float q = 0.0f;
+    const float mean = blockSum((float)s, lds) / (float)a.cols;
+    double q = 0.0;
     forRow<V, BLOCK>(a.cols,
                      [&](int c) {
                        const Vec v = loadVec<T, V>(x + c);
+                       float u = 0.0f;
 #pragma unroll
-                       for (int e = 0; e < V; ++e) q = fmaf((float)v[e] - mean, (float)v[e] - mean, q);
+                       for (int e = 0; e < V; ++e) u = fmaf((float)v[e] - mean, (float)v[e] - mean, u);
+                       q += u;
                      },
-                     [&](int c) { q = fmaf((float)x[c] - mean, (float)x[c] - mean, q); });
-    const float rstd = 1.0f / sqrtf(blockSum(q, lds) / (float)a.cols + a.eps);
+                     [&](int c) { q += ((float)x[c] - mean) * ((float)x[c] - mean); });
+    const float rstd = 1.0f / sqrtf(blockSum((float)q, lds) / (float)a.cols + a.eps);
     forRow<V, BLOCK>(a.cols,
                      [&](int c) {
                        const Vec v = loadVec<T, V>(x + c);
@@ -520,25 +526,28 @@ __device__ __forceinline__ void backwardRow(const LnArgs& a, int64_t row, float*
   T* dx = (T*)a.y[r] + i * a.yStride;
   const W* gamma = (const W*)a.gamma[r];
   const float mean = a.mean[r][i], rstd = a.rstd[r][i];
-  float s = 0.0f, u = 0.0f;
+  double sums = 0.0, along = 0.0;   // as the forward pass
   forRow<V, BLOCK>(a.cols,
                    [&](int c) {
                      const Vec v = loadVec<T, V>(x + c), o = loadVec<T, V>(dy + c);
                      const WVec g = gamma ? loadVec<W, V>(gamma + c) : (WVec)(W)1.0f;
+                     float s = 0.0f, u = 0.0f;
 #pragma unroll
                      for (int e = 0; e < V; ++e) {
                        const float q = (float)o[e] * (float)g[e];
                        s += q;
                        u = fmaf(q, ((float)v[e] - mean) * rstd, u);
                      }
+                     sums += s;
+                     along += u;
                    },
                    [&](int c) {
                      const float q = (float)dy[c] * (gamma ? (float)gamma[c] : 1.0f);
-                     s += q;
-                     u = fmaf(q, ((float)x[c] - mean) * rstd, u);
+                     sums += q;
+                     along += q * (((float)x[c] - mean) * rstd);
                    });
-  s = blockSum(s, lds) / (float)a.cols;
-  u = blockSum(u, lds) / (float)a.cols;
+  const float s = blockSum((float)sums, lds) / (float)a.cols;
+  const float u = blockSum((float)along, lds) / (float)a.cols;
   if (SUMS) {
     if (threadIdx.x == 0) {
       a.rowSums[2 * row] = s;

@@ -1,6 +1,7 @@
 """The operators around the AllReduce at the ends of the ranges their documentation gives."""
 import op_util as ou
 import pytest
+import test_gpu_layernorm as ln
 import torch
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +47,31 @@ def test_backward_of_the_widest_rows(B, cols, inplace):
     assert torch.equal(gg, dy[0] * keep[0])
     for got, a, b in zip(dx[0].split(1 << 26), dy[0].split(1 << 26), keep[0].split(1 << 26)):
         assert (got.double() - (a.double() - s - b.double() * t)).abs().max().item() <= 6 * 10 * ou.U
+
+
+@pytest.mark.parametrize("rows", [4, 520], ids=["few rows", "many rows"])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=str)
+def test_sums_of_wide_rows(B, dt, rows, monkeypatch):
+    """Rows of 2^22 columns (of 2^16 where there are many), of one value and not: a thread's thousands of additions
+    cost no more than few.  A vector's own up to 8 additions, then one, 6 steps inside a wavefront and 16 to join
+    them: 40 covers the chain, whatever the row's width."""
+    cols = (1 << 22) + 3 if rows == 4 else (1 << 16) + 3
+    monkeypatch.setattr(ou, "chain", lambda n: 40)
+    g = torch.Generator().manual_seed(rows)
+    x = ou.rows_of(g, (4, cols), dt, 1.0, 1000.0)
+    x[0], x[2] = 1000.1, 0.1
+    dy = ou.rows_of(g, (4, cols), dt)
+    dy[0], dy[1] = 0.1, 0.3
+    ys, m, s = ln.run_forward(B, [x], None, None, 1e-5)
+    ln.check_forward([x], None, None, 1e-5, ys, m, s)
+    rest = rows - 4      # rows like the second add to the count, not to the checking
+    out = torch.empty(rows, cols, dtype=dt, device="cuda")
+    X = torch.cat([x, x[1:2].expand(rest, cols)]).cuda()
+    D = torch.cat([dy, dy[1:2].expand(rest, cols)]).cuda()
+    means = x.double().mean(1).float()
+    rstds = torch.full((4,), 0.5)
+    M, R = (torch.cat([t, t[1:2].expand(rest)]).cuda() for t in (means, rstds))
+    B.arLayerNormBackward([D], [X], [M], [R], None, [out], [torch.empty(cols, dtype=dt, device="cuda")])
+    want, bound, _, _ = ou.ln_backward(dy, x, means, rstds, None)
+    ou.within(out[:4], want, bound, dt, "dx")
+    assert all(torch.equal(out[i], out[1]) for i in range(4, rows))
