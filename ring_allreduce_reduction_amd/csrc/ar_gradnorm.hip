@@ -343,11 +343,13 @@ arResult_t createList(arTensorList_t* out, int nTensors, const void* const* src,
   if (l->nTiles > 0) {
     const size_t bytes = tiles.size() * sizeof(Tile);
     if (hipMalloc((void**)&l->tiles, bytes) != hipSuccess) {
+      (void)hipGetLastError();   // reported here; not left for the thread's next launch to find
       delete l;
       return arHipError;
     }
     if (hipMemcpy(l->tiles, tiles.data(), bytes, hipMemcpyHostToDevice) != hipSuccess) {
       (void)hipFree(l->tiles);
+      (void)hipGetLastError();
       delete l;
       return arHipError;
     }
@@ -366,16 +368,12 @@ size_t listWorkspace(const arTensorList* l) {
 template <int KIND>
 hipError_t launchNorm(const NormArgs& a, bool clip, hipStream_t st) {
   if (a.nTiles <= (clip ? kSmallClipTiles : kSmallNormTiles)) {   // an empty list too: its norm is 0
-    if (clip) hipLaunchKernelGGL((smallList<KIND, true>), dim3(1), dim3(kSmallBlock), 0, st, a);
-    else hipLaunchKernelGGL((smallList<KIND, false>), dim3(1), dim3(kSmallBlock), 0, st, a);
-    return hipGetLastError();
+    return launchKernel(clip ? smallList<KIND, true> : smallList<KIND, false>, dim3(1), dim3(kSmallBlock), a, st);
   }
-  hipLaunchKernelGGL(normTiles<KIND>, dim3(a.nPartial), dim3(kNormBlock), 0, st, a);
-  if (clip)
-    hipLaunchKernelGGL(clipTiles<KIND>, dim3(a.nTiles < kClipGrid ? a.nTiles : kClipGrid), dim3(kNormBlock), 0, st, a);
-  else
-    hipLaunchKernelGGL(normFinish<KIND>, dim3(1), dim3(kNormBlock), 0, st, a);
-  return hipGetLastError();
+  const hipError_t e = launchKernel(normTiles<KIND>, dim3(a.nPartial), dim3(kNormBlock), a, st);
+  if (e != hipSuccess) return e;
+  if (!clip) return launchKernel(normFinish<KIND>, dim3(1), dim3(kNormBlock), a, st);
+  return launchKernel(clipTiles<KIND>, dim3(a.nTiles < kClipGrid ? a.nTiles : kClipGrid), dim3(kNormBlock), a, st);
 }
 
 arResult_t runNorm(arTensorList* l, bool clip, int kind, float scale, float maxNorm, float eps, float* norm,

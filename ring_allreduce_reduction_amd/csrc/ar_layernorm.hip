@@ -919,16 +919,14 @@ hipError_t launchForward(LnArgs a, hipStream_t st) {
   const bool aligned16 = (a.xStride | a.yStride) % kVec<DT> == 0;
   const int rounds = !aligned16 || each < 1 ? 1 : each > 8 ? 8 : (int)each;
   const int grid = shareBlocks(&a, BLOCK / THREADS, resident * kOpsCUs * rounds);
-  hipLaunchKernelGGL((layerNormInRegisters<DT, WT, THREADS, NP, DEPTH>), dim3(grid), dim3(BLOCK), 0, st, a);
-  return hipGetLastError();
+  return launchKernel(layerNormInRegisters<DT, WT, THREADS, NP, DEPTH>, dim3(grid), dim3(BLOCK), a, st);
 }
 
 template <int DT, int WT, int BLOCK>
 hipError_t launchRows(const LnArgs& a, hipStream_t st) {
   const int64_t rows = a.rowStart[a.nranks];
   const int most = (BLOCK < 128 ? 32 : 8) * kOpsCUs;
-  hipLaunchKernelGGL((layerNormRows<DT, WT, BLOCK>), dim3((unsigned)(rows < most ? rows : most)), dim3(BLOCK), 0, st, a);
-  return hipGetLastError();
+  return launchKernel(layerNormRows<DT, WT, BLOCK>, dim3((unsigned)(rows < most ? rows : most)), dim3(BLOCK), a, st);
 }
 
 template <int DT, int WT>
@@ -960,12 +958,37 @@ struct Forward {
 };
 
 template <int DT, int WT, int THREADS, int NP, int DEPTH, int WAVES>
-int launchBackward(LnArgs a, const BackwardCut& k, hipStream_t st) {
-  if (!rowFits(a.cols, kVec<DT>, k.threads, k.pieces) || k.threads > THREADS || k.pieces != NP) return -1;
-  const int grid = shareBlocks(&a, k.groups, partialRows(a.rowStart[a.nranks], k));
-  hipLaunchKernelGGL((layerNormBackwardInRegisters<DT, WT, THREADS, NP, DEPTH, WAVES>), dim3(grid),
-                     dim3(THREADS < kLnBlock ? kLnBlock : k.threads), 0, st, a);
-  return grid;
+hipError_t launchBackward(LnArgs a, const BackwardCut& k, int* partials, hipStream_t st) {
+  if (!rowFits(a.cols, kVec<DT>, k.threads, k.pieces) || k.threads > THREADS || k.pieces != NP)
+    return hipErrorInvalidValue;
+  *partials = shareBlocks(&a, k.groups, partialRows(a.rowStart[a.nranks], k));
+  return launchKernel(layerNormBackwardInRegisters<DT, WT, THREADS, NP, DEPTH, WAVES>, dim3(*partials),
+                      dim3(THREADS < kLnBlock ? kLnBlock : k.threads), a, st);
+}
+
+// Rows that registers do not hold: dx alone, or the rows' sums and then the
+// columns with dx, or the columns alone.
+template <int DT, int WT>
+hipError_t launchBackwardWide(const LnArgs& a, const BackwardCut& k, int* partials, hipStream_t st) {
+  constexpr int V = kVec<DT>;
+  const bool narrow = a.cols < V;
+  const int64_t rows = a.rowStart[a.nranks];
+  const int most = (narrow ? 32 : 8) * kOpsCUs;
+  const dim3 grid((unsigned)(rows < most ? rows : most)), block(narrow ? 64 : 1024);
+  if (a.partial == nullptr)
+    return launchKernel(narrow ? layerNormBackwardRows<DT, WT, 64, false> : layerNormBackwardRows<DT, WT, 1024, false>,
+                        grid, block, a, st);
+  hipError_t e = hipSuccess;
+  if (a.rowSums != nullptr)
+    e = launchKernel(narrow ? layerNormBackwardRows<DT, WT, 64, true> : layerNormBackwardRows<DT, WT, 1024, true>,
+                     grid, block, a, st);
+  *partials = partialRows(rows, k);
+  if (e == hipSuccess && !narrow)
+    e = launchKernel(layerNormBackwardColumns<DT, WT, false>, dim3((a.cols / V + kLnBlock - 1) / kLnBlock, *partials),
+                     dim3(kLnBlock), a, st);
+  if (e == hipSuccess && a.cols % V != 0)
+    e = launchKernel(layerNormBackwardColumns<DT, WT, true>, dim3(1, *partials), dim3(kLnBlock), a, st);
+  return e;
 }
 
 // Runs the backward pass of a launch with rows; *partials receives the rows of
@@ -975,40 +998,20 @@ struct Backward {
   static hipError_t run(const LnArgs& a, int* partials, hipStream_t st) {
     constexpr int V = kVec<DT>;
     const BackwardCut k = backwardCut(a.cols, 16 / V);
-    const int64_t rows = a.rowStart[a.nranks];
-    if (k.threads == 16) *partials = launchBackward<DT, WT, 16, 1, 2, 1>(a, k, st);
-    else if (k.threads == 32) *partials = launchBackward<DT, WT, 32, 1, 2, 1>(a, k, st);
-    else if (k.threads == 64 && k.pieces == 1) *partials = launchBackward<DT, WT, 64, 1, 2, 1>(a, k, st);
-    else if (k.threads == 64) *partials = launchBackward<DT, WT, 64, 2, 3, 2>(a, k, st);
-    else if (k.pieces == 1) *partials = k.threads <= 256   ? launchBackward<DT, WT, 256, 1, 3, 3>(a, k, st)
-                                      : k.threads <= 512 ? launchBackward<DT, WT, 512, 1, 3, 3>(a, k, st)
-                                                         : launchBackward<DT, WT, 1024, 1, 3, 4>(a, k, st);
-    else if (k.pieces == 2) *partials = launchBackward<DT, WT, 1024, 2, 1, 4>(a, k, st);
-    else if (k.pieces >= 3) {
-      if constexpr (V == 4) *partials = k.pieces == 3 ? launchBackward<DT, WT, 1024, 3, 1, 4>(a, k, st)
-                                                      : launchBackward<DT, WT, 1024, 4, 1, 4>(a, k, st);
-    } else {
-      const int block = a.cols < V ? 64 : 1024;
-      const int most = (a.cols < V ? 32 : 8) * kOpsCUs;
-      const dim3 grid((unsigned)(rows < most ? rows : most));
-      if (a.partial == nullptr) {   // dx alone
-        if (a.cols < V) hipLaunchKernelGGL((layerNormBackwardRows<DT, WT, 64, false>), grid, dim3(block), 0, st, a);
-        else hipLaunchKernelGGL((layerNormBackwardRows<DT, WT, 1024, false>), grid, dim3(block), 0, st, a);
-      } else {
-        if (a.rowSums != nullptr) {
-          if (a.cols < V) hipLaunchKernelGGL((layerNormBackwardRows<DT, WT, 64, true>), grid, dim3(block), 0, st, a);
-          else hipLaunchKernelGGL((layerNormBackwardRows<DT, WT, 1024, true>), grid, dim3(block), 0, st, a);
-        }
-        *partials = partialRows(rows, k);
-        if (a.cols >= V)
-          hipLaunchKernelGGL((layerNormBackwardColumns<DT, WT, false>),
-                             dim3((a.cols / V + kLnBlock - 1) / kLnBlock, *partials), dim3(kLnBlock), 0, st, a);
-        if (a.cols % V != 0)
-          hipLaunchKernelGGL((layerNormBackwardColumns<DT, WT, true>), dim3(1, *partials), dim3(kLnBlock), 0, st, a);
-      }
+    if (k.threads == 0) return launchBackwardWide<DT, WT>(a, k, partials, st);
+    if (k.threads == 16) return launchBackward<DT, WT, 16, 1, 2, 1>(a, k, partials, st);
+    if (k.threads == 32) return launchBackward<DT, WT, 32, 1, 2, 1>(a, k, partials, st);
+    if (k.threads == 64 && k.pieces == 1) return launchBackward<DT, WT, 64, 1, 2, 1>(a, k, partials, st);
+    if (k.threads == 64) return launchBackward<DT, WT, 64, 2, 3, 2>(a, k, partials, st);
+    if (k.pieces == 1 && k.threads <= 256) return launchBackward<DT, WT, 256, 1, 3, 3>(a, k, partials, st);
+    if (k.pieces == 1 && k.threads <= 512) return launchBackward<DT, WT, 512, 1, 3, 3>(a, k, partials, st);
+    if (k.pieces == 1) return launchBackward<DT, WT, 1024, 1, 3, 4>(a, k, partials, st);
+    if (k.pieces == 2) return launchBackward<DT, WT, 1024, 2, 1, 4>(a, k, partials, st);
+    if constexpr (V == 4) {
+      if (k.pieces == 3) return launchBackward<DT, WT, 1024, 3, 1, 4>(a, k, partials, st);
+      return launchBackward<DT, WT, 1024, 4, 1, 4>(a, k, partials, st);
     }
-    const hipError_t err = hipGetLastError();
-    return *partials < 0 ? hipErrorInvalidValue : err;
+    return hipErrorInvalidValue;
   }
 };
 
@@ -1017,8 +1020,7 @@ struct BackwardFew {
   static hipError_t run(const LnFewArgs& w, hipStream_t st) {
     constexpr int V = kVec<DT>;
     const unsigned across = gridOf((w.rows.cols + kFewLanes * V - 1) / (kFewLanes * V), kLnBlock);
-    hipLaunchKernelGGL((layerNormBackwardFew<DT, WT>), dim3((unsigned)w.dxRows + across), dim3(kLnBlock), 0, st, w);
-    return hipGetLastError();
+    return launchKernel(layerNormBackwardFew<DT, WT>, dim3((unsigned)w.dxRows + across), dim3(kLnBlock), w, st);
   }
 };
 
@@ -1026,8 +1028,7 @@ template <int DT, int WT>
 struct WeightGrads {
   static hipError_t run(const LnSumArgs& a, hipStream_t st) {
     const unsigned across = gridOf((a.cols + kSumCols - 1) / kSumCols, kSumBlock);
-    hipLaunchKernelGGL((layerNormWeightGrads<WT>), dim3(across, 2), dim3(kSumBlock), 0, st, a);
-    return hipGetLastError();
+    return launchKernel(layerNormWeightGrads<WT>, dim3(across, 2), dim3(kSumBlock), a, st);
   }
 };
 

@@ -12,6 +12,17 @@ namespace ar {
 
 constexpr int kOpsCUs = 256;   // compute units of an MI355X; grids are sized to it
 
+// Launches a kernel of one argument and returns that launch's own result:
+// hipGetLastError would also report what an earlier call of the thread, the
+// library's or not, has left there.  A failure is not left for the next to find.
+template <typename A>
+hipError_t launchKernel(void (*kernel)(A), dim3 grid, dim3 block, const A& args, hipStream_t st) {
+  void* list[] = {const_cast<A*>(&args)};
+  const hipError_t e = hipLaunchKernel((const void*)kernel, grid, block, list, 0, st);
+  if (e != hipSuccess) (void)hipGetLastError();
+  return e;
+}
+
 template <int DT> struct Elem;
 template <> struct Elem<arFloat32> { typedef float type; };
 template <> struct Elem<arFloat16> { typedef _Float16 type; };

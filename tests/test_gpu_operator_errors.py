@@ -1,0 +1,73 @@
+"""Results of the operators around the AllReduce are their own: errors of other calls are not theirs, and their
+failures leave nothing behind."""
+import ctypes
+
+import pytest
+import test_gpu_gradnorm as gn
+import test_gpu_layernorm as ln
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from ring_allreduce_reduction_amd import binding
+    binding.lib()
+    return binding
+
+
+@pytest.fixture(autouse=True)
+def _named(request):
+    import gpu_util
+    gpu_util.note(request.node.name)
+
+
+@pytest.fixture(scope="module")
+def hip(B):
+    return ctypes.CDLL("libamdhip64.so.7")   # the runtime torch has loaded
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 40), (600, 40), (600, 5), (600, 17000)], ids=str)
+def test_an_earlier_error_is_not_reported(B, hip, rows, cols):
+    """A HIP call of the program's own that failed (an ordinal no device has) before each operator."""
+    xs, dys, gam, bet = ln.inputs([rows], cols, torch.float32, torch.float32, cols)
+    x, dy, g, b = ([t[0].cuda()] for t in (xs, dys, gam, bet))
+    y, dx = [torch.empty_like(x[0])], [torch.empty_like(x[0])]
+    m, s = [torch.empty(rows, device="cuda")], [torch.empty(rows, device="cuda")]
+    gg, gb = [torch.empty(cols, device="cuda")], [torch.empty(cols, device="cuda")]
+    ws = torch.empty(B.arLayerNormBackwardWorkspace([rows], cols), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    try:
+        assert hip.hipSetDevice(9999) != 0
+        B.arLayerNorm(x, y, g, b, m, s)
+        assert hip.hipSetDevice(9999) != 0
+        B.arLayerNormBackward(dy, x, m, s, g, dx, gg, gb, workspace=ws)
+        assert hip.hipSetDevice(9999) != 0
+        B.arLayerNormBackward(dy, x, m, s, g, dx)
+    finally:
+        hip.hipGetLastError()
+    torch.cuda.synchronize()
+    ln.check_forward(xs, gam, bet, 1e-5, y, m, s)
+    ln.check_backward(dys, xs, gam, dx, gg, gb, [m[0].cpu()], [s[0].cpu()])
+
+
+@pytest.mark.parametrize("n", [100, 3000000])
+def test_an_earlier_error_is_not_reported_by_norms(B, hip, n):
+    host, devs = gn.grads([n], [torch.float32], n)
+    outs = [torch.empty_like(devs[0])]
+    norm = torch.empty(1, device="cuda")
+    with B.TensorList(devs, outs) as lst:
+        ws = torch.empty(lst.workspace(), dtype=torch.uint8, device="cuda")
+        try:
+            assert hip.hipSetDevice(9999) != 0
+            B.arGradNorm(lst, norm, workspace=ws)
+            assert hip.hipSetDevice(9999) != 0
+            B.arGradClip(lst, norm, 0.5, workspace=ws)
+        finally:
+            hip.hipGetLastError()
+        torch.cuda.synchronize()
+    gn.check_norm(norm, gn.norm_of(host, "2"))
+    gn.check_clip(outs, host, gn.norm_of(host, "2"), 1.0, 0.5)
