@@ -625,7 +625,9 @@ arResult_t arTensorListCreate(arTensorList_t* list, int nTensors, const void* co
 arResult_t arTensorListWorkspace(arTensorList_t list, size_t* bytes);
 
 /* arTensorListDestroy -- free the list's device memory (waits for work that
- * uses it).  Graphs that captured calls on it must not be replayed again. */
+ * uses it).  Graphs that captured calls on it must not be replayed again.
+ * Where the memory cannot be freed (arHipError, for one while a stream is being
+ * captured) the list stays as it was, to be destroyed later. */
 arResult_t arTensorListDestroy(arTensorList_t list);
 
 typedef enum {

@@ -425,10 +425,13 @@ extern "C" arResult_t arTensorListWorkspace(arTensorList_t list, size_t* bytes) 
 extern "C" arResult_t arTensorListDestroy(arTensorList_t list) {
   if (list == nullptr) return arSuccess;
   if (!ar::listOk(list)) return arInvalidArgument;
+  if (hipFree(list->tiles) != hipSuccess) {   // the list stays whole: the caller may try again
+    (void)hipGetLastError();
+    return arHipError;
+  }
   list->magic = 0;
-  const hipError_t e = hipFree(list->tiles);
   delete list;
-  return e == hipSuccess ? arSuccess : arHipError;
+  return arSuccess;
 }
 
 extern "C" arResult_t arGradNorm(arTensorList_t list, arNormKind_t kind, float scale, float* norm, void* workspace,

@@ -71,3 +71,30 @@ def test_an_earlier_error_is_not_reported_by_norms(B, hip, n):
         torch.cuda.synchronize()
     gn.check_norm(norm, gn.norm_of(host, "2"))
     gn.check_clip(outs, host, gn.norm_of(host, "2"), 1.0, 0.5)
+
+
+def test_a_list_that_cannot_be_freed_stays_whole(B, hip):
+    """While a stream is being captured memory may not be freed: the list is still there afterwards, works, and is
+    destroyed then."""
+    host, devs = gn.grads([70001, 5], [torch.float32], 3)
+    norm = torch.empty(1, device="cuda")
+    lst = B.TensorList(devs)
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert hip.hipStreamCreateWithFlags(ctypes.byref(stream), 1) == 0
+    torch.cuda.synchronize()
+    assert hip.hipStreamBeginCapture(stream, 0) == 0
+    try:
+        with pytest.raises(B.ArError):
+            lst.close()
+    finally:
+        hip.hipStreamEndCapture(stream, ctypes.byref(graph))   # the capture was invalidated
+        if graph.value:
+            hip.hipGraphDestroy(graph)
+        hip.hipGetLastError()
+    assert lst.handle is not None
+    B.arGradNorm(lst, norm)
+    gn.check_norm(norm, gn.norm_of(host, "2"))
+    lst.close()
+    assert lst.handle is None
+    lst.close()
+    assert hip.hipStreamDestroy(stream) == 0
