@@ -29,10 +29,16 @@ bool touches(const Extent& a, const Extent& b) {
 
 bool outputsOverlap(std::vector<Extent>& v) {
   std::sort(v.begin(), v.end(), [](const Extent& a, const Extent& b) { return a.begin < b.begin; });
+  // Only pairs with an output are looked at: any number of inputs may share
+  // memory (one tensor listed 2^20 times), and dense buffers then end the search
+  // at their first pair that is not in place.
+  std::vector<size_t> nextOutput(v.size() + 1, v.size());   // the first output from here on
+  for (size_t i = v.size(); i-- > 0;) nextOutput[i] = v[i].output ? i : nextOutput[i + 1];
   for (size_t i = 0; i < v.size(); ++i) {
     const uintptr_t end = endOf(v[i]);
-    for (size_t j = i + 1; j < v.size() && v[j].begin < end; ++j) {
-      if (!v[i].output && !v[j].output) continue;
+    for (size_t j = i + 1; j < v.size(); ++j) {
+      if (!v[i].output) j = nextOutput[j];
+      if (j == v.size() || v[j].begin >= end) break;
       if (v[i].pair >= 0 && v[i].pair == v[j].pair && sameMemory(v[i], v[j])) continue;
       if (touches(v[i], v[j])) return true;
     }
