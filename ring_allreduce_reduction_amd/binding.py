@@ -521,6 +521,9 @@ class TensorList:
 
     def __init__(self, srcs, dsts=None):
         self.handle = None
+        for ts in (srcs, dsts):
+            if isinstance(ts, torch.Tensor):   # it would be read row by row
+                raise ValueError("expected a list of tensors, got one tensor")
         self.tensors = (list(srcs), None if dsts is None else list(dsts))
         self.handle = arTensorListCreate(*self.tensors)
         self.workspace_bytes = arTensorListWorkspace(self.handle)

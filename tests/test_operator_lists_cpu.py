@@ -28,3 +28,14 @@ def test_one_source_listed_many_times(B):
     dst[-1] = BASE   # the last over the shared source
     assert ops.lists(B, n=n, src=src, dst=dst, counts=counts, dtypes=dtypes) == B.arInvalidArgument
     assert time.perf_counter() - t0 < 10
+
+
+def test_one_tensor_in_place_of_a_list(B):
+    """It would be cut into its rows, or its elements.  A CPU tensor stands in: the check comes before the device's."""
+    x = torch.zeros(4, 8)
+    for args in ((x,), (x[0],), (x, [x]), ([x], x), (x, x)):
+        with pytest.raises(ValueError, match="got one tensor"):
+            B.TensorList(*args)
+    for ts in ([x], (x,), iter([x])):   # any other iterable is read once
+        with pytest.raises(ValueError, match="device tensors"):
+            B.TensorList(ts)
