@@ -8,6 +8,7 @@
 // value whose sums are exact come out as b.
 // Backward, h = (x - m) r, q = dy g:  dx = r (q - sum q / C - h sum(q h) / C),
 // dg = sum over rows of dy h,  db = sum over rows of dy.
+#include <cmath>
 #include <new>
 #include <vector>
 
@@ -1045,7 +1046,7 @@ arResult_t forward(const void* const* x, const void* const* gamma, const void* c
   if (!shapeOk(rows, nranks, cols, &s) || !strideOk(xStride, cols) || !strideOk(yStride, cols))
     return arInvalidArgument;
   if (!opsFloatType(dtype) || (wtype != dtype && wtype != arFloat32)) return arInvalidArgument;
-  if (!(eps >= 0.0f) || eps > 3.4e38f) return arInvalidArgument;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return arInvalidArgument;
   if ((mean == nullptr) != (rstd == nullptr)) return arInvalidArgument;
   if (groupOpen()) return arInvalidUsage;
   if (s.total == 0) return arSuccess;
