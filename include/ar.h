@@ -520,7 +520,8 @@ arResult_t arAllReduceNoAlloc(const void* const* sendbufs, void* const* recvbufs
  * layer applies to every rank's rows, whose weights' gradient is a sum over
  * all of them; and the global norm and clipping of the reduced gradients.
  * Like arAllReduceNoAlloc these calls need no communicator: each only
- * enqueues kernels on `stream`, in which no workgroup waits for another, and
+ * enqueues kernels on `stream` (of the current device, which holds every
+ * buffer), in which no workgroup waits for another, and
  * allocates nothing, so any call may be captured into a HIP graph, the first
  * included.  Scratch memory is the caller's: `workspace` (device, 16-byte
  * aligned, at least the bytes the matching ...Workspace call reports) is

@@ -201,8 +201,18 @@ void* workspaceOf(PyObject* o, size_t need, Devices* devices) {
   return t.data_ptr();
 }
 
-// A torch stream, a raw handle, or None: torch's current stream.
-void* streamOf(PyObject* o) {
+long longAttribute(PyObject* o, const char* name) {
+  PyObject* v = PyObject_GetAttrString(o, name);
+  if (v == nullptr) throw PythonError();
+  const long n = PyLong_AsLong(v);
+  Py_DECREF(v);
+  if (PyErr_Occurred()) throw PythonError();
+  return n;
+}
+
+// A torch stream, a raw handle, or None: torch's current stream.  A stream of
+// another device than the tensors' would run the kernels there.
+void* streamOf(PyObject* o, const Devices& devices) {
   if (o == Py_None) return (void*)c10::hip::getCurrentHIPStream().stream();
   if (PyLong_Check(o)) {
     void* p = PyLong_AsVoidPtr(o);
@@ -214,6 +224,9 @@ void* streamOf(PyObject* o) {
   void* p = PyLong_AsVoidPtr(handle);
   Py_DECREF(handle);
   if (PyErr_Occurred()) throw PythonError();
+  const long d = longAttribute(o, "device_index");
+  if (devices.current >= 0 && d != devices.current)
+    fail("the stream is on cuda:%ld, the current device is cuda:%d", d, devices.current);
   return p;
 }
 
@@ -283,7 +296,7 @@ PyObject* layerNorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     c.devices.check();
     const float eps = (float)PyFloat_AsDouble(args[6]);
     if (PyErr_Occurred()) return nullptr;
-    void* stream = streamOf(args[7]);
+    void* stream = streamOf(args[7], c.devices);
     return result([&] {
       return gLayerNorm(x, args[2] != Py_None ? g : nullptr, args[3] != Py_None ? b : nullptr, y,
                         stats ? (float**)m : nullptr, stats ? (float**)s : nullptr, c.rows, c.n, (size_t)c.cols,
@@ -327,7 +340,7 @@ PyObject* layerNormBackward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
     c.devices.check();
     if (need > 0 && workspace == nullptr) return PyLong_FromLongLong(-(long long)need);
-    void* stream = streamOf(args[9]);
+    void* stream = streamOf(args[9], c.devices);
     return result([&] {
       return gLayerNormBackward(dy, x, args[4] != Py_None ? g : nullptr, (float**)m, (float**)s, hasDx ? dx : nullptr,
                                 hasDg ? dg : nullptr, hasDb ? db : nullptr, c.rows, c.n, (size_t)c.cols, dyStride,
@@ -403,7 +416,7 @@ PyObject* gradNorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
     void* workspace = workspaceOf(args[7], need, &devices);
     devices.check();
-    void* stream = streamOf(args[8]);
+    void* stream = streamOf(args[8], devices);
     return result([&] {
       return clip ? gGradClip(list, kind, scale, maxNorm, eps, norm, workspace, need, stream)
                   : gGradNorm(list, kind, scale, norm, workspace, need, stream);

@@ -98,3 +98,28 @@ def test_a_list_that_cannot_be_freed_stays_whole(B, hip):
     assert lst.handle is None
     lst.close()
     assert hip.hipStreamDestroy(stream) == 0
+
+
+class StreamElsewhere:
+    """A stream of a second device, as torch's streams look."""
+    def __init__(self, device_index):
+        self.device_index = device_index
+        self.cuda_stream = 0
+
+
+def test_a_stream_of_another_device_is_refused(B):
+    x, w = torch.ones(4, 8, device="cuda"), torch.ones(8, device="cuda")
+    y, m, s, norm = torch.empty_like(x), torch.empty(4, device="cuda"), torch.empty(4, device="cuda"), torch.empty(1, device="cuda")
+    ws = torch.empty(B.arLayerNormBackwardWorkspace([4], 8), dtype=torch.uint8, device="cuda")
+    here = torch.cuda.current_device()
+    with B.TensorList([x], [y]) as lst:
+        lws = torch.empty(lst.workspace(), dtype=torch.uint8, device="cuda")
+        calls = [lambda st: B.arLayerNorm([x], [y], [w], [w], [m], [s], stream=st),
+                 lambda st: B.arLayerNormBackward([x], [x], [m], [s], [w], [y], [torch.empty_like(w)], None, ws, stream=st),
+                 lambda st: B.arGradNorm(lst, norm, workspace=lws, stream=st),
+                 lambda st: B.arGradClip(lst, norm, 1.0, workspace=lws, stream=st)]
+        for call in calls:
+            with pytest.raises(ValueError, match="stream is on cuda:%d" % (here + 1)):
+                call(StreamElsewhere(here + 1))
+            call(StreamElsewhere(here))
+        torch.cuda.synchronize()
