@@ -12,6 +12,8 @@ import os
 
 import torch  # noqa: F401  -- loads the HIP runtime the library must share
 
+from .build import built_for
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libar.so")
 
@@ -450,6 +452,9 @@ def _torch_calls():
         spec = importlib.util.spec_from_file_location("_ar_torch", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
+        if getattr(module, "built_for", None) != built_for():
+            raise ImportError("_ar_torch.so was built for %s and this is %s: build again (__graft_entry__.build() or "
+                              "python ring_allreduce_reduction_amd/build.py)" % (getattr(module, "built_for", "another torch"), built_for()))
         module.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in
                       (L.arLayerNorm, L.arLayerNormBackward, L.arLayerNormBackwardWorkspace, L.arTensorListCreate,
                        L.arGradNorm, L.arGradClip)])

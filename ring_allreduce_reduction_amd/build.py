@@ -98,6 +98,13 @@ def build(verbose: bool = False) -> str:
 TORCH_CALLS = os.path.join(HERE, "_ar_torch.so")
 
 
+def built_for() -> str:
+    """The Python and torch the extension module belongs to: it uses their C++ layouts."""
+    import sys
+    import torch
+    return "python %d.%d, torch %s" % (sys.version_info[0], sys.version_info[1], torch.__version__)
+
+
 def build_torch_calls(verbose: bool = False) -> str:
     """The extension module that reads torch tensors for binding.py (host code only)."""
     import sysconfig
@@ -105,7 +112,7 @@ def build_torch_calls(verbose: bool = False) -> str:
     t = os.path.dirname(torch.__file__)
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
-           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(),
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(), '-DAR_BUILT_FOR="%s"' % built_for(),
            "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(rocm, "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(t, "include"),
            "-isystem", os.path.join(t, "include", "torch", "csrc", "api", "include"),

@@ -435,4 +435,10 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ar_torch", nullptr, -1, kMethods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__ar_torch(void) { return PyModule_Create(&kModule); }
+// built_for: the Python and torch whose headers this was compiled with; the
+// binding uses the module with no other.
+PyMODINIT_FUNC PyInit__ar_torch(void) {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", AR_BUILT_FOR) != 0) Py_CLEAR(m);
+  return m;
+}

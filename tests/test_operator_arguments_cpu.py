@@ -16,3 +16,17 @@ def test_every_finite_eps_is_taken(B):
         assert ops.forward(B, eps=eps, rows=ops.N(0)) == B.arSuccess
     for eps in (float("inf"), float("-inf"), float("nan"), -2.0 ** -149):
         assert ops.forward(B, eps=eps, rows=ops.N(0)) == B.arInvalidArgument
+
+
+@pytest.mark.parametrize("version", ["2.9.1+rocm7.0", "2.10.0+rocm9.9"])
+def test_a_module_built_for_another_torch_is_not_used(B, monkeypatch, version):
+    """The extension module reads torch's C++ objects: another torch lays them out differently."""
+    import torch
+    module = B._torch_calls()
+    assert "torch " + torch.__version__ in module.built_for
+    monkeypatch.setattr(B, "_torch_calls_module", None)
+    monkeypatch.setattr(torch, "__version__", version)
+    with pytest.raises(ImportError, match="was built for"):
+        B.arLayerNorm([torch.zeros(4, 8)], [torch.zeros(4, 8)])
+    monkeypatch.undo()
+    assert B._torch_calls() is module
