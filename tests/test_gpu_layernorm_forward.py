@@ -1,4 +1,4 @@
-"""Layer norm forward: rows whose mean has to come out to the last bit."""
+"""Layer norm forward: every layout at its edges, and rows whose mean has to come out to the last bit."""
 import op_util as ou
 import pytest
 import test_gpu_layernorm as ln
@@ -40,3 +40,19 @@ def test_rows_of_one_value(B, dt, cols):
     assert torch.equal(ys[0].cpu(), bet[0].to(dt).expand(len(VALUES), cols))
     ou.within(s[0], torch.full((len(VALUES),), 1e-5, dtype=torch.float64).rsqrt(), 1e-5 ** -0.5 * 4 * ou.U,
               torch.float32, "rstd")
+
+
+def edges(dt):
+    """The least and the largest width of each layout; rows of less than a vector, and past registers."""
+    v = 4 if dt == torch.float32 else 8
+    tops = [16, 32, 64, 128, 192, 256, 512, 768, 1024, 1536, 2048, 3072, 4096]
+    return [1, v - 1, v] + [w for lo, hi in zip([0] + tops, tops) for w in (lo * v + 1, hi * v) if w > v] + [4096 * v + 1]
+
+
+@pytest.mark.parametrize("dt,wt,cols", [(d, w, c) for d, w in ou.TYPES for c in edges(d)], ids=str)
+def test_every_layout_and_its_edges(B, dt, wt, cols):
+    """Dense rows, padded ones at odd addresses over themselves, and without weights or statistics."""
+    xs, _, gam, bet = ln.inputs([9, 0, 4], cols, dt, wt, cols)
+    ln.check_forward(xs, gam, bet, 1e-5, *ln.run_forward(B, xs, gam, bet, 1e-5))
+    ln.check_forward(xs, gam, bet, 1e-5, *ln.run_forward(B, xs, gam, bet, 1e-5, 3, 1, inplace=True))
+    ln.check_forward(xs, None, None, 1e-5, *ln.run_forward(B, xs, None, None, 1e-5, stats=False))
