@@ -552,7 +552,8 @@ arResult_t arAllReduceNoAlloc(const void* const* sendbufs, void* const* recvbufs
  *              rank may have 0 (its pointers are not looked at then, those of
  *              dgamma and dbeta in arLayerNormBackward apart).
  *  nranks      1..AR_MAX_RANKS.
- *  cols        1..2^30; strides at least cols.
+ *  cols        1..2^30; strides at least cols, rows[r] times a stride at most
+ *              2^48 elements.
  *  eps         finite, >= 0.
  * The statistics are 32-bit: a row whose sum passes 3.4e38 has an infinite
  * mean, one whose squared deviations add up past it rstd 0; with eps 0 the

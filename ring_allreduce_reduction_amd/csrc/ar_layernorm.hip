@@ -838,7 +838,7 @@ bool shapeOk(const size_t* rows, int nranks, size_t cols, Shape* s) {
   return true;
 }
 
-bool strideOk(size_t stride, size_t cols) { return stride >= cols && stride <= (size_t)1 << 32; }
+bool strideOk(size_t stride, size_t cols) { return stride >= cols && stride <= (size_t)1 << 48; }
 
 bool aligned(const void* p, int esz) { return p != nullptr && (uintptr_t)p % (uintptr_t)esz == 0; }
 

@@ -75,3 +75,25 @@ def test_sums_of_wide_rows(B, dt, rows, monkeypatch):
     want, bound, _, _ = ou.ln_backward(dy, x, means, rstds, None)
     ou.within(out[:4], want, bound, dt, "dx")
     assert all(torch.equal(out[i], out[1]) for i in range(4, rows))
+
+
+@pytest.mark.parametrize("rows", [2, 3])
+def test_row_strides_past_32_bits(B, rows):
+    """bf16 rows 2^32 + 8 elements apart."""
+    cols, stride = 777, (1 << 32) + 8
+    xs, dys, gam, bet = ln.inputs([rows], cols, torch.bfloat16, torch.float32, rows)
+    X, D, Y = (torch.empty((rows - 1) * stride + cols, dtype=torch.bfloat16, device="cuda")
+               .as_strided((rows, cols), (stride, 1)) for _ in range(3))
+    X.copy_(xs[0])
+    D.copy_(dys[0])
+    m, s = [torch.empty(rows, device="cuda")], [torch.empty(rows, device="cuda")]
+    B.arLayerNorm([X], [Y], [gam[0].cuda()], [bet[0].cuda()], m, s)
+    torch.cuda.synchronize()
+    ln.check_forward(xs, gam, bet, 1e-5, [Y.contiguous()], m, s)
+    gg, gb = [torch.empty(cols, device="cuda")], [torch.empty(cols, device="cuda")]
+    B.arLayerNormBackward([D], [X], m, s, [gam[0].cuda()], [Y], gg, gb)
+    torch.cuda.synchronize()
+    ln.check_backward(dys, xs, gam, [Y.contiguous()], gg, gb, [m[0].cpu()], [s[0].cpu()])
+    B.arLayerNormBackward([D], [X], m, s, [gam[0].cuda()], [D], gg, gb)
+    torch.cuda.synchronize()
+    ln.check_backward(dys, xs, gam, [D.contiguous()], gg, gb, [m[0].cpu()], [s[0].cpu()])

@@ -30,3 +30,13 @@ def test_a_module_built_for_another_torch_is_not_used(B, monkeypatch, version):
         B.arLayerNorm([torch.zeros(4, 8)], [torch.zeros(4, 8)])
     monkeypatch.undo()
     assert B._torch_calls() is module
+
+
+def test_row_strides(B):
+    """At least the row's width, and no limit but that a rank's rows stay inside 2^48 elements."""
+    for stride in (16, (1 << 32) + 1, 1 << 48):
+        assert ops.forward(B, xs=stride, ys=stride, rows=ops.N(0)) == B.arSuccess
+    for stride in (15, (1 << 48) + 1, 1 << 63):
+        assert ops.forward(B, xs=stride, ys=stride, rows=ops.N(0)) == B.arInvalidArgument
+    far = dict(x=ops.P(1 << 20), y=ops.P((1 << 20) + 64), xs=1 << 47, ys=1 << 47)
+    assert ops.forward(B, rows=ops.N(3), **far) == B.arInvalidArgument
