@@ -555,9 +555,10 @@ arResult_t arAllReduceNoAlloc(const void* const* sendbufs, void* const* recvbufs
  *  cols        1..2^30; strides at least cols, rows[r] times a stride at most
  *              2^48 elements.
  *  eps         finite, >= 0.
- * The statistics are 32-bit: a row whose sum passes 3.4e38 has an infinite
- * mean, one whose squared deviations add up past it rstd 0; with eps 0 the
- * deviations must be large enough for their squares too (above 1e-19).
+ * The statistics are 32-bit.  Where a partial sum of a row's values passes
+ * 3.4e38 its mean and y are infinite or NaN; where only one of its squared
+ * deviations does, rstd is 0 and y is beta.  With eps 0 the deviations must be
+ * large enough for their squares (above 1e-19).
  * Errors: arInvalidArgument (nothing enqueued), arInvalidUsage in an open
  * group, arHipError, arSystemError.
  */

@@ -56,3 +56,20 @@ def test_every_layout_and_its_edges(B, dt, wt, cols):
     ln.check_forward(xs, gam, bet, 1e-5, *ln.run_forward(B, xs, gam, bet, 1e-5))
     ln.check_forward(xs, gam, bet, 1e-5, *ln.run_forward(B, xs, gam, bet, 1e-5, 3, 1, inplace=True))
     ln.check_forward(xs, None, None, 1e-5, *ln.run_forward(B, xs, None, None, 1e-5, stats=False))
+
+
+@pytest.mark.parametrize("dt,cols", [(t, c) for t in COLS for c in COLS[t]], ids=str)
+def test_range_of_the_statistics(B, dt, cols):
+    """eps 0: rows of tiny and of large spread as any others; past the range, what the header says."""
+    g = torch.Generator().manual_seed(cols)
+    gam, bet = [ou.rows_of(g, (cols,), torch.float32, 0.3, 1.0)], [ou.rows_of(g, (cols,), torch.float32)]
+    for size in (1e-18, 1e16):
+        x = [ou.rows_of(g, (3, cols), dt, size, size)]
+        ln.check_forward(x, gam, bet, 0.0, *ln.run_forward(B, x, gam, bet, 0.0))
+    x = ou.rows_of(g, (3, cols), dt)
+    x[0] = 3e38                                   # the sum overflows
+    x[1] = torch.tensor([1e20, -1e20]).repeat(cols)[:cols].to(dt)   # the squares alone do
+    ys, m, s = ln.run_forward(B, [x], gam, bet, 1e-5)
+    assert not torch.isfinite(m[0][0]) and not torch.isfinite(ys[0][0].float()).any()
+    assert torch.isfinite(m[0][1]) and s[0][1] == 0 and torch.equal(ys[0][1].cpu(), bet[0].to(dt))
+    ln.check_forward([x[2:]], gam, bet, 1e-5, [ys[0][2:]], [m[0][2:]], [s[0][2:]])
