@@ -615,7 +615,8 @@ typedef struct arTensorList* arTensorList_t;
  *            itself (in place) or memory that overlaps no other tensor.  NULL:
  *            the list is only for arGradNorm.
  * The arrays are copied; the tensors themselves are the caller's and must stay
- * where they are while the list is used.  Allocates device memory (32 bytes a
+ * where they are while the list is used: gradients that are allocated anew
+ * need a new list.  Allocates device memory (32 bytes a
  * tile) and copies to it synchronously: not for capture.
  * Errors: arInvalidArgument (bad pointers, counts, types; outputs that
  * overlap; more than 2^25 tiles), arHipError, arSystemError.
@@ -654,7 +655,8 @@ arResult_t arGradNorm(arTensorList_t list, arNormKind_t kind, float scale, float
 /*
  * arGradClip -- arGradNorm, then every tensor scaled to its dst:
  *   dst = src * (scale * c),   c = 1 if norm + eps <= maxNorm, else maxNorm / (norm + eps).
- * The factor scale * c is formed in 64 bits and rounded to a float once; the
+ * The factor scale * c is formed in 64 bits and rounded to a float once (below
+ * 1.2e-38 it keeps fewer bits, as any float); the
  * products are rounded once to the tensor's type.  norm (device, may be NULL)
  * receives the norm before clipping.  A NaN norm makes every output NaN, an
  * infinite one (with a finite maxNorm) makes finite values 0 and infinities

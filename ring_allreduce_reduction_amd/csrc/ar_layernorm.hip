@@ -91,7 +91,7 @@ __device__ __forceinline__ void forRow(int n, F f, G g) {
 
 // Rows too wide for registers, and rows of less than one vector: a workgroup
 // per row, which is read three times (from the caches after the first).  2
-// ranks of 1000 rows of 40000 bf16: 87 us with 1024 threads and 8 workgroups a
+// ranks of 1000 rows of 40000 bf16: 87 us (95 on another box) with 1024 threads and 8 workgroups a
 // CU, 94 with 2, 106 with 512 threads, 117 with 256.  A thread adds its vectors'
 // sums up in 64 bits: a row of 2^20 columns is 1024 values a thread, whose
 // roundings to 32 bits moved the mean of a row of 1000.1 by 0.01.
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(BLOCK) layerNormBackwardRows(const LnArgs a) {
 }
 
 // The weights' sums of such rows, and dx where the rows' sums are given (so x and
-// dy are read twice in all: 2 ranks of 1000 rows of 40000 bf16 173 us; 210 with
+// dy are read twice in all: 2 ranks of 1000 rows of 40000 bf16 174 us; 210 with
 // dx from the rows' kernel and a third reading here): a thread
 // per vector of columns and slice of the rows, four rows at a time; ONE takes
 // single columns (rows of less than a vector and the columns behind the last
@@ -662,8 +662,9 @@ __device__ __forceinline__ float joinSlices(F value) {
 
 // Few rows in one launch: the first workgroups take a row each and write dx,
 // the others take 8 vectors of columns and add all rows up (32 slices of them,
-// joined through LDS).  Everything is read twice, from the caches, but no
-// partial sums leave a workgroup.  dx must not be written over x or dy.  256
+// joined through LDS).  x and dy are read twice for dx (its sums first) and once
+// for the weights, from the caches after the first time, but no partial sums
+// leave a workgroup.  dx must not be written over x or dy.  256
 // rows of 768 to 8192 columns bf16 4.3-7.1 us, 6.9-15.3 in two launches; 512
 // rows 5.3-10.5 and 6.2-16.9; 1024 rows of 256 columns 8.4 and 6.6: no more
 // than 512 rows come here.
