@@ -201,15 +201,6 @@ void* workspaceOf(PyObject* o, size_t need, Devices* devices) {
   return t.data_ptr();
 }
 
-long longAttribute(PyObject* o, const char* name) {
-  PyObject* v = PyObject_GetAttrString(o, name);
-  if (v == nullptr) throw PythonError();
-  const long n = PyLong_AsLong(v);
-  Py_DECREF(v);
-  if (PyErr_Occurred()) throw PythonError();
-  return n;
-}
-
 // A torch stream, a raw handle, or None: torch's current stream.  A stream of
 // another device than the tensors' would run the kernels there.
 void* streamOf(PyObject* o, const Devices& devices) {
@@ -224,7 +215,14 @@ void* streamOf(PyObject* o, const Devices& devices) {
   void* p = PyLong_AsVoidPtr(handle);
   Py_DECREF(handle);
   if (PyErr_Occurred()) throw PythonError();
-  const long d = longAttribute(o, "device_index");
+  PyObject* index = PyObject_GetAttrString(o, "device_index");   // torch's streams have one
+  if (index == nullptr) {
+    PyErr_Clear();
+    return p;
+  }
+  const long d = PyLong_AsLong(index);
+  Py_DECREF(index);
+  if (PyErr_Occurred()) throw PythonError();
   if (devices.current >= 0 && d != devices.current)
     fail("the stream is on cuda:%ld, the current device is cuda:%d", d, devices.current);
   return p;

@@ -123,3 +123,17 @@ def test_a_stream_of_another_device_is_refused(B):
                 call(StreamElsewhere(here + 1))
             call(StreamElsewhere(here))
         torch.cuda.synchronize()
+
+
+def test_any_object_with_a_stream_handle_is_a_stream(B):
+    """One that does not name a device is taken at its word, as a raw handle is."""
+    class Handle:
+        cuda_stream = 0
+    x = torch.ones(4, 8, device="cuda")
+    y, norm = torch.full_like(x, 9.0), torch.empty(1, device="cuda")
+    B.arLayerNorm([x], [y], stream=Handle())
+    with B.TensorList([x]) as lst:
+        ws = torch.empty(lst.workspace(), dtype=torch.uint8, device="cuda")
+        B.arGradNorm(lst, norm, workspace=ws, stream=Handle())
+        torch.cuda.synchronize()
+    assert (y == 0).all() and abs(norm.item() - 32 ** 0.5) <= 1e-6
