@@ -804,7 +804,7 @@ BackwardCut backwardCut(int cols, int esz) {
   if (vecs <= 32) return {32, 1, 8, 2 * kOpsCUs};
   if (vecs <= 64) return {64, 1, 4, 2 * kOpsCUs};
   if (vecs <= 128) return {64, 2, 4, 4 * kOpsCUs};
-  const int pieces = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : vecs <= 3072 ? 3 : 4;
+  const int pieces = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : vecs <= 3 * 1024 ? 3 : 4;
   const int waves = ((vecs + pieces - 1) / pieces + kWave - 1) / kWave;
   return {waves * kWave, pieces, 1, (waves <= 12 ? 12 / waves : 1) * kOpsCUs};
 }
@@ -953,7 +953,7 @@ struct Forward {
     if (vecs <= 1024) return launchForward<DT, WT, 512, 2, 2>(a, st);
     if (vecs <= 1536) return launchForward<DT, WT, 512, 3, 2>(a, st);
     if (vecs <= 2048) return launchForward<DT, WT, 512, 4, 2>(a, st);
-    if (vecs <= 3072) return launchForward<DT, WT, 1024, 3, 1>(a, st);
+    if (vecs <= 3 * 1024) return launchForward<DT, WT, 1024, 3, 1>(a, st);
     if (vecs <= 4096) return launchForward<DT, WT, 1024, 4, 1>(a, st);
     return launchRows<DT, WT, 1024>(a, st);
   }

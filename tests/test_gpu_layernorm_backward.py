@@ -7,7 +7,7 @@ import torch
 
 pytestmark = pytest.mark.gpu
 
-# one width of each layout: vectors of a row up to 16, 32, 64, 128, 256, 512, 1024, 2048, 3072, 4096, past them, and
+# one width of each layout: vectors of a row up to 16, 32, 64, 128, 256, 512, 1 to 4 times 1024, past them, and
 # less than one vector (16-bit rows: 8 columns a vector, of which registers hold 2048)
 COLS = {torch.float32: [3, 40, 100, 200, 500, 1000, 2000, 4000, 6000, 10000, 14000, 17000],
         torch.bfloat16: [7, 90, 200, 500, 1000, 2000, 4000, 8000, 12000, 17000]}
@@ -43,7 +43,7 @@ def test_rows_of_extreme_spread(B, dt, cols, size, grad):
 def edges(dt):
     """The least and the largest width of each layout; rows of less than a vector, and past registers."""
     v, last = (4, 4096) if dt == torch.float32 else (8, 2048)
-    tops = [t for t in (16, 32, 64, 128, 256, 512, 1024, 2048, 3072, 4096) if t <= last]
+    tops = [t for t in (16, 32, 64, 128, 256, 512, 1024, 2048, 3 * 1024, 4096) if t <= last]
     return [1, v - 1, v] + [w for lo, hi in zip([0] + tops, tops) for w in (lo * v + 1, hi * v) if w > v] + [last * v + 1]
 
 

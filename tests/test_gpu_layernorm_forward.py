@@ -45,7 +45,7 @@ def test_rows_of_one_value(B, dt, cols):
 def edges(dt):
     """The least and the largest width of each layout; rows of less than a vector, and past registers."""
     v = 4 if dt == torch.float32 else 8
-    tops = [16, 32, 64, 128, 192, 256, 512, 768, 1024, 1536, 2048, 3072, 4096]
+    tops = [16, 32, 64, 128, 192, 256, 512, 768, 1024, 1536, 2048, 3 * 1024, 4096]
     return [1, v - 1, v] + [w for lo, hi in zip([0] + tops, tops) for w in (lo * v + 1, hi * v) if w > v] + [4096 * v + 1]
 
 
