@@ -518,7 +518,10 @@ arResult_t arAllReduceNoAlloc(const void* const* sendbufs, void* const* recvbufs
 /* ------------------------------------------------------------------------
  * Operators of a training or serving step around its AllReduce: the norm a
  * layer applies to every rank's rows, whose weights' gradient is a sum over
- * all of them; and the global norm and clipping of the reduced gradients.
+ * all of them; the global norm and clipping of the reduced gradients; dropout
+ * with what stands around it after a row-parallel layer; the tokens'
+ * log-probabilities where the ranks share the vocabulary; and a policy loss
+ * over every rank's tokens.
  * Like arAllReduceNoAlloc these calls need no communicator: each only
  * enqueues kernels on `stream` (of the current device, which holds every
  * buffer), in which no workgroup waits for another, and
@@ -666,6 +669,169 @@ arResult_t arGradNorm(arTensorList_t list, arNormKind_t kind, float scale, float
  */
 arResult_t arGradClip(arTensorList_t list, arNormKind_t kind, float scale, float maxNorm, float eps, float* norm,
                       void* workspace, size_t workspaceBytes, void* stream);
+
+/*
+ * arDropoutAdd -- what follows the AllReduce of a row-parallel layer, on every
+ * rank's rows in one launch (ranks beyond 16 in further launches of 16):
+ *   y = residual + k * s * (x + bias),
+ * where k is 1 for the elements that stay and 0 for the others, which are
+ * dropped with probability p, and s = 1 / (1 - p).  A dropped element is the
+ * residual's value (0 without one), whatever x holds there.
+ *  x, residual, y (host arrays of nranks device pointers) rank r's rows[r] rows
+ *              of `cols` elements of `dtype`, each with its row stride in
+ *              elements; residual may be NULL (0).  y[r] may be x[r] or
+ *              residual[r] with equal strides (in place); otherwise an output
+ *              must not overlap any other buffer.
+ *  bias        (host array or NULL: 0) rank r's copy, `cols` elements of `wtype`
+ *              (dtype or arFloat32).
+ *  rows, nranks, cols, strides  as in arLayerNorm.
+ *  p           0..1.  It is held as T / 65536, T = floor(65536 p + 1/2), and s =
+ *              65536 / (65536 - T): the mean over draws is x + bias exactly.
+ *              T = 0 keeps and T = 65536 drops every element.
+ *  firstRow    (host, nranks, or NULL) the index of rank r's first row in the
+ *              whole batch: its row i draws as row firstRow[r] + i.  Ranks that
+ *              hold the same rows give the same index and draw the same, ranks
+ *              with other rows other ones.  NULL: the ranks' rows follow each
+ *              other.  firstRow[r] + rows[r] at most 2^32.
+ *  seed, offset, step  what else the draw depends on: `seed` of a run, `offset`
+ *              of a layer and step; `step` (device, may be NULL) is added to
+ *              offset (modulo 2^64) and read when the kernel runs, so that a
+ *              replayed graph draws anew when the program has changed it.
+ * The draw of row R and column c: half c % 2 (the lower one first) of word
+ * (c % 8) / 2 of Philox4x32-10 [Salmon, Moraes, Dror, Shaw, "Parallel random
+ * numbers: as easy as 1, 2, 3", 2011] with the counter {c / 8, R, offset's
+ * lower word, its upper word} and the key {seed's lower word, its upper word};
+ * the element stays where these 16 bits are T or more.  It depends on nothing
+ * else: not on the ranks, strides, types or how the rows are shared out.
+ * y is formed in 32 bits and rounded once.
+ * Errors: as arLayerNorm.
+ */
+arResult_t arDropoutAdd(const void* const* x, const void* const* bias, const void* const* residual, void* const* y,
+                        const size_t* rows, const uint64_t* firstRow, int nranks, size_t cols, size_t xStride,
+                        size_t residualStride, size_t yStride, double p, uint64_t seed, uint64_t offset,
+                        const uint64_t* step, arDataType_t dtype, arDataType_t wtype, void* stream);
+
+/*
+ * arDropoutAddBackward -- the gradients of arDropoutAdd, from the same draw
+ * (that of the residual is dy itself):
+ *   dx = k * s * dy,   dbias = sum of dx (unrounded) over all ranks' rows,
+ * the latter written to every rank, as an AllReduce would.
+ *  dy, dx      (host arrays) as x and y of arDropoutAdd; dx may be NULL (only
+ *              dbias), and dx[r] may be dy[r] with equal strides.
+ *  dbias       (host array or NULL) nranks buffers of `cols` elements of
+ *              `wtype`; written with zeros when no rank has a row.
+ *  workspace, workspaceBytes  see above; may be NULL / 0 when dbias is.
+ * Other arguments and errors as arDropoutAdd; also arInvalidArgument when the
+ * workspace is too small or both dx and dbias are NULL.
+ */
+arResult_t arDropoutAddBackward(const void* const* dy, void* const* dx, void* const* dbias, const size_t* rows,
+                                const uint64_t* firstRow, int nranks, size_t cols, size_t dyStride, size_t dxStride,
+                                double p, uint64_t seed, uint64_t offset, const uint64_t* step, arDataType_t dtype,
+                                arDataType_t wtype, void* workspace, size_t workspaceBytes, void* stream);
+
+/* arDropoutAddBackwardWorkspace -- the workspace bytes of an
+ * arDropoutAddBackward with these rows and columns (a pure function). */
+arResult_t arDropoutAddBackwardWorkspace(const size_t* rows, int nranks, size_t cols, size_t* bytes);
+
+/*
+ * arTokenLogprob -- the log-probability of every row's target token, from
+ * logits whose vocabulary is cut over the ranks (what a user of AllReduce
+ * forms from three of them: largest value, sum, target's logit).  Over a row's
+ * logits x in all shards, with target t:
+ *   top = max x,   logSum = ln(sum of exp(scale * (x - top))),
+ *   logp = scale * (x[t] - top) - logSum.
+ *  logits    (host array of nranks device pointers) rank r's shard: `rows` rows
+ *            of cols[r] elements of `dtype`, row i at i * strides[r] elements.
+ *  cols      (host, nranks) the shards' widths, each at most 2^30, 0 allowed (its
+ *            pointer is not looked at then), not all 0.  Rank 0 holds the
+ *            vocabulary's first cols[0] tokens, rank 1 those behind them, ...
+ *  strides   (host, nranks, or NULL: cols) at least 1 and cols[r]; rows times a
+ *            stride at most 2^48.
+ *  nranks    1..AR_MAX_RANKS.    rows  0..2^31-1.
+ *  targets   (device) `rows` indices into the vocabulary.  A negative one marks
+ *            a row that is ignored: its logits are not read, its logp, top and
+ *            logSum are 0.  One past the vocabulary gives NaN.
+ *  scale     finite, > 0: one over the sampling temperature.
+ *  logp      (device) `rows` floats.
+ *  top, logSum  (device, each may be NULL) `rows` floats for
+ *            arTokenLogprobBackward; scale * top + logSum is the logarithm of the
+ *            sum of all exponentials.
+ *  workspace, workspaceBytes  see above; may be NULL / 0 where
+ *            arTokenLogprobWorkspace reports 0.
+ * Masks: a logit of -inf, or of the type's lowest value beside ordinary ones,
+ * has probability 0; logits that all have the lowest value are equally likely.
+ * logp is -inf for such a target, and NaN where a row has a NaN or +inf
+ * logit or nothing but -inf: then there is no distribution.
+ * Outputs must not overlap any other buffer.
+ * Errors: arInvalidArgument (nothing enqueued), arInvalidUsage in an open
+ * group, arHipError, arSystemError.
+ */
+arResult_t arTokenLogprob(const void* const* logits, const size_t* cols, const size_t* strides, int nranks,
+                          size_t rows, const int64_t* targets, float scale, float* logp, float* top, float* logSum,
+                          arDataType_t dtype, void* workspace, size_t workspaceBytes, void* stream);
+
+/* arTokenLogprobWorkspace -- the workspace bytes of an arTokenLogprob with
+ * these rows and shards (a pure function; 0 where there are rows enough). */
+arResult_t arTokenLogprobWorkspace(size_t rows, const size_t* cols, int nranks, size_t* bytes);
+
+/*
+ * arTokenLogprobBackward -- the gradient of the logits from that of logp:
+ *   dlogits[j] = scale * dlogp * ([j = t] - exp(scale * (x[j] - top) - logSum)),
+ * formed in 32 bits and rounded once.
+ *  dlogp     (device) `rows` floats.  Rows whose dlogp is 0 (a token that was
+ *            clipped) and ignored rows receive zeros; their logits are not read.
+ *  top, logSum  what arTokenLogprob wrote.
+ *  dlogits, dlogitsStrides  (host arrays) as logits and strides; dlogits[r] may
+ *            be logits[r] with equal strides (in place).
+ * A target past the vocabulary gives a row of NaN (zeros where dlogp is 0).
+ * Other arguments and errors as arTokenLogprob.
+ */
+arResult_t arTokenLogprobBackward(const float* dlogp, const void* const* logits, const size_t* cols,
+                                  const size_t* strides, int nranks, size_t rows, const int64_t* targets, float scale,
+                                  const float* top, const float* logSum, void* const* dlogits,
+                                  const size_t* dlogitsStrides, arDataType_t dtype, void* stream);
+
+/*
+ * arPolicyLoss -- the clipped policy loss with a KL term, its mean over every
+ * rank's tokens, and its gradient.  For a token's logp, old (under the policy
+ * that sampled it), ref (under a reference), advantage A and weight w:
+ *   ratio = exp(logp - old),
+ *   loss  = -min(A ratio, A clamp(ratio, 1 - clipLow, 1 + clipHigh)),
+ *   kl    = exp(ref - logp) - (ref - logp) - 1,
+ *   L     = sum over all ranks' tokens of w (loss + klCoef kl) / D,
+ *   dlogp = gradScale w / D (g + klCoef (1 - exp(ref - logp))),
+ * g = 0 where A > 0 and ratio > 1 + clipHigh or A < 0 and ratio < 1 - clipLow
+ * (clipped), else -A ratio.
+ *  logp, old, advantage  (host arrays of nranks device pointers) tokens[r] floats.
+ *  ref       (host array, or NULL: no KL term, klCoef must be 0).
+ *  weight    (host array, or NULL: 1) >= 0.  A token of weight 0 is left out:
+ *            nothing else of it is looked at, and its dlogp is 0.
+ *  dlogp     (host array, or NULL) tokens[r] floats; dlogp[r] may be logp[r].
+ *  tokens    (host, nranks) at most 2^31-1 together; a rank may have 0 (its
+ *            pointers are not looked at then).
+ *  clipLow, clipHigh  0..1, and >= 0 (may be infinite).
+ *  klCoef    finite, >= 0.
+ *  denominator  D, finite and > 0, or 0: the sum of all weights.  Where D is 0
+ *            (no token has a weight) L and every dlogp are 0.
+ *  gradScale finite; a loss scale.
+ *  stats     (device) five floats: L, the mean of loss, the mean of kl, the
+ *            clipped tokens' share (means and share weighted, over D), the sum of
+ *            the weights.
+ *  workspace, workspaceBytes  see above; may be NULL / 0 where
+ *            arPolicyLossWorkspace reports 0.
+ * A token's terms and all sums are formed in 64 bits: which tokens are clipped
+ * does not depend on roundings, and a small kl keeps its bits.
+ * Outputs must not overlap any other buffer.  Errors: as arTokenLogprob.
+ */
+arResult_t arPolicyLoss(const float* const* logp, const float* const* old, const float* const* ref,
+                        const float* const* advantage, const float* const* weight, float* const* dlogp,
+                        const size_t* tokens, int nranks, double clipLow, double clipHigh, double klCoef,
+                        double denominator, double gradScale, float* stats, void* workspace, size_t workspaceBytes,
+                        void* stream);
+
+/* arPolicyLossWorkspace -- the workspace bytes of an arPolicyLoss over these
+ * tokens (a pure function; 0 for few tokens). */
+arResult_t arPolicyLossWorkspace(const size_t* tokens, int nranks, size_t* bytes);
 
 const char* arGetErrorString(arResult_t result);
 

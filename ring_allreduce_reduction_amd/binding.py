@@ -121,6 +121,18 @@ def lib():
         L.arTensorListDestroy.argtypes = [vp]
         L.arGradNorm.argtypes = [vp, c_int, c_f, vp, vp, c_sz, vp]
         L.arGradClip.argtypes = [vp, c_int, c_f, c_f, c_f, vp, vp, c_sz, vp]
+        c_d, c_u64 = ctypes.c_double, ctypes.c_uint64
+        u64s = ctypes.POINTER(c_u64)
+        L.arDropoutAdd.argtypes = [vps, vps, vps, vps, szs, u64s, c_int, c_sz, c_sz, c_sz, c_sz, c_d, c_u64, c_u64, vp,
+                                   c_int, c_int, vp]
+        L.arDropoutAddBackward.argtypes = [vps, vps, vps, szs, u64s, c_int, c_sz, c_sz, c_sz, c_d, c_u64, c_u64, vp,
+                                           c_int, c_int, vp, c_sz, vp]
+        L.arDropoutAddBackwardWorkspace.argtypes = [szs, c_int, c_sz, szs]
+        L.arTokenLogprob.argtypes = [vps, szs, szs, c_int, c_sz, vp, c_f, vp, vp, vp, c_int, vp, c_sz, vp]
+        L.arTokenLogprobWorkspace.argtypes = [c_sz, szs, c_int, szs]
+        L.arTokenLogprobBackward.argtypes = [vp, vps, szs, szs, c_int, c_sz, vp, c_f, vp, vp, vps, szs, c_int, vp]
+        L.arPolicyLoss.argtypes = [vps, vps, vps, vps, vps, vps, szs, c_int, c_d, c_d, c_d, c_d, c_d, vp, vp, c_sz, vp]
+        L.arPolicyLossWorkspace.argtypes = [szs, c_int, szs]
         L.arDestroy.argtypes = [vp]
         L.arSetDebug.argtypes = [vp, c_int, ctypes.c_int64]
         L.arGetErrorString.argtypes = [c_int]
@@ -132,7 +144,9 @@ def lib():
                    "arCommGetAsyncError", "arCommAbort", "arCommCount", "arDestroy", "arSetDebug",
                    "arAllReduceNoAlloc", "arTuneTableTime", "arCommFootprint", "arLayerNorm", "arLayerNormBackward",
                    "arLayerNormBackwardWorkspace", "arTensorListCreate", "arTensorListWorkspace",
-                   "arTensorListDestroy", "arGradNorm", "arGradClip"):
+                   "arTensorListDestroy", "arGradNorm", "arGradClip", "arDropoutAdd", "arDropoutAddBackward",
+                   "arDropoutAddBackwardWorkspace", "arTokenLogprob", "arTokenLogprobWorkspace",
+                   "arTokenLogprobBackward", "arPolicyLoss", "arPolicyLossWorkspace"):
             getattr(L, fn).restype = c_int
         _lib = L
     return _lib
@@ -457,7 +471,9 @@ def _torch_calls():
                               "python ring_allreduce_reduction_amd/build.py)" % (getattr(module, "built_for", "another torch"), built_for()))
         module.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in
                       (L.arLayerNorm, L.arLayerNormBackward, L.arLayerNormBackwardWorkspace, L.arTensorListCreate,
-                       L.arGradNorm, L.arGradClip)])
+                       L.arGradNorm, L.arGradClip, L.arDropoutAdd, L.arDropoutAddBackward,
+                       L.arDropoutAddBackwardWorkspace, L.arTokenLogprob, L.arTokenLogprobBackward,
+                       L.arTokenLogprobWorkspace, L.arPolicyLoss, L.arPolicyLossWorkspace)])
         _torch_calls_module = module
     return _torch_calls_module
 
@@ -577,6 +593,92 @@ def arGradClip(lst, norm, maxNorm, eps=1e-6, kind=arNorm2, scale=1.0, workspace=
     """The norm, and every tensor times scale * min(1, maxNorm / (norm + eps)) into the list's outputs.  norm may
     be None."""
     _grad_call(lst, kind, scale, float(maxNorm), eps, norm, workspace, stream, "arGradClip")
+
+
+def arDropoutAdd(xs, ys, p, seed, offset=0, step=None, biases=None, residuals=None, firstRows=None, stream=None):
+    """ys = residuals + dropout(xs + biases) over every rank's rows.  xs, ys, residuals: one tensor per rank, as in
+    arLayerNorm; biases: the ranks' copies, of the rows' type or float32; ys may be xs or residuals.  p: the share
+    that is dropped; seed, offset (0..2^64-1) and step (an int64 device tensor of one element, added to offset when
+    the kernel runs) say which draw; firstRows: the index of each rank's first row in the whole batch, equal for ranks
+    that hold the same rows (None: the ranks' rows follow each other)."""
+    rc = _torch_calls().dropout_add(xs, ys, float(p), seed, offset, step, biases, residuals, firstRows, stream)
+    if rc:
+        _check(rc, "arDropoutAdd")
+
+
+def arDropoutAddBackwardWorkspace(rows, cols):
+    """Bytes of workspace of an arDropoutAddBackward over ranks with these rows."""
+    b = ctypes.c_size_t()
+    _check(lib().arDropoutAddBackwardWorkspace((ctypes.c_size_t * len(rows))(*rows), len(rows), int(cols),
+                                               ctypes.byref(b)), "arDropoutAddBackwardWorkspace")
+    return b.value
+
+
+def arDropoutAddBackward(dys, dxs, p, seed, offset=0, step=None, dbiases=None, firstRows=None, workspace=None,
+                         stream=None):
+    """The gradients of arDropoutAdd with the same draw: dxs (may be dys, or None), and dbiases (or None), each
+    rank's copy of the sum over all ranks' rows.  workspace: a device tensor of arDropoutAddBackwardWorkspace bytes
+    that no other running call uses; None allocates one."""
+    call = _torch_calls().dropout_add_backward
+    rc = call(dys, dxs, float(p), seed, offset, step, dbiases, firstRows, workspace, stream)
+    if rc < 0:   # the bytes of the workspace that is missing
+        rc = call(dys, dxs, float(p), seed, offset, step, dbiases, firstRows, _workspace(-rc, stream), stream)
+    if rc:
+        _check(rc, "arDropoutAddBackward")
+
+
+def arTokenLogprobWorkspace(rows, cols):
+    """Bytes of workspace of an arTokenLogprob of this many rows over shards of these widths."""
+    b = ctypes.c_size_t()
+    _check(lib().arTokenLogprobWorkspace(int(rows), (ctypes.c_size_t * len(cols))(*cols), len(cols), ctypes.byref(b)),
+           "arTokenLogprobWorkspace")
+    return b.value
+
+
+def arTokenLogprob(logits, targets, logp, top=None, logSum=None, scale=1.0, workspace=None, stream=None):
+    """logp = the log-probability of every row's target from logits whose vocabulary is cut over the ranks.  logits:
+    one (rows, columns) tensor per rank, contiguous or 2-D with padded rows, widths of their own; targets: int64, one
+    a row, negative for rows to ignore; logp, top, logSum: float32, one a row (top and logSum for
+    arTokenLogprobBackward).  scale: one over the temperature.  workspace: a device tensor of arTokenLogprobWorkspace
+    bytes that no other running call uses; None allocates one where it is needed."""
+    call = _torch_calls().token_logprob
+    rc = call(logits, targets, logp, top, logSum, float(scale), workspace, stream)
+    if rc < 0:   # the bytes of the workspace that is missing
+        rc = call(logits, targets, logp, top, logSum, float(scale), _workspace(-rc, stream), stream)
+    if rc:
+        _check(rc, "arTokenLogprob")
+
+
+def arTokenLogprobBackward(dlogp, logits, targets, top, logSum, dlogits, scale=1.0, stream=None):
+    """The gradient of the logits (dlogits may be logits) from dlogp and what arTokenLogprob wrote."""
+    rc = _torch_calls().token_logprob_backward(dlogp, logits, targets, top, logSum, dlogits, float(scale), stream)
+    if rc:
+        _check(rc, "arTokenLogprobBackward")
+
+
+def arPolicyLossWorkspace(tokens):
+    """Bytes of workspace of an arPolicyLoss over ranks with these tokens."""
+    b = ctypes.c_size_t()
+    _check(lib().arPolicyLossWorkspace((ctypes.c_size_t * len(tokens))(*tokens), len(tokens), ctypes.byref(b)),
+           "arPolicyLossWorkspace")
+    return b.value
+
+
+def arPolicyLoss(logps, olds, advantages, stats, refs=None, weights=None, dlogps=None, clipLow=0.2, clipHigh=0.2,
+                 klCoef=0.0, denominator=0.0, gradScale=1.0, workspace=None, stream=None):
+    """The clipped policy loss with a KL term, its mean over every rank's tokens, and its gradient dlogps (may be
+    logps, or None).  Lists of one float32 tensor per rank, one value a token; weights 0 leave tokens out.  stats:
+    five floats, the loss, its policy and KL parts, the clipped share, the sum of the weights.  denominator 0: the
+    sum of the weights.  workspace: a device tensor of arPolicyLossWorkspace bytes that no other running call uses;
+    None allocates one where it is needed."""
+    call = _torch_calls().policy_loss
+    args = (logps, olds, refs, advantages, weights, dlogps, float(clipLow), float(clipHigh), float(klCoef),
+            float(denominator), float(gradScale), stats)
+    rc = call(*args, workspace, stream)
+    if rc < 0:   # the bytes of the workspace that is missing
+        rc = call(*args, _workspace(-rc, stream), stream)
+    if rc:
+        _check(rc, "arPolicyLoss")
 
 
 class Comm:

@@ -14,7 +14,8 @@ LIB = os.path.join(HERE, "libar.so")
 OBJ = os.path.join(HERE, "_build")
 SOURCES = ["ar_kernels_ring_simple.hip", "ar_kernels_ring_ll.hip", "ar_kernels_ring_ll128.hip", "ar_kernels_ring_batch.hip",
            "ar_kernels_ring_rs.hip", "ar_kernels_ring_ag.hip", "ar_kernels_tree.hip", "ar_kernels_tree_batch.hip",
-           "ar_kernels.hip", "ar_noalloc.hip", "ar_layernorm.hip", "ar_gradnorm.hip",
+           "ar_kernels.hip", "ar_noalloc.hip", "ar_layernorm.hip", "ar_gradnorm.hip", "ar_dropout.hip",
+           "ar_logprob.hip", "ar_policy.hip",
            "ar_comm.cpp", "ar_tune.cpp", "ar_group.cpp", "ar_api.cpp"]
 ARCH = os.environ.get("AR_OFFLOAD_ARCH", "gfx950")
 ROCM_LIB = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "lib")

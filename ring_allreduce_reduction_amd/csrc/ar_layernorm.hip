@@ -12,18 +12,12 @@
 #include <new>
 #include <vector>
 
-#include "ar_api.h"
-#include "ar_internal.h"
-#include "ar_ops.h"
+#include "ar_rows.h"
 
 namespace ar {
 namespace {
 
-// Ranks per launch: their pointers travel in the kernel arguments, which every
-// launch copies (1 KB; with 32 ranks' a one-row call took 0.4-1 us longer).
-constexpr int kLnRanks = 16;
-constexpr size_t kLnMaxCols = (size_t)1 << 30;
-constexpr int64_t kLnMaxRows = 0x7fffffff;   // of all ranks
+constexpr int kLnRanks = kOpRanks;
 constexpr int kLnBlock = 256;
 
 struct LnArgs {
@@ -766,14 +760,6 @@ __global__ void __launch_bounds__(kSumBlock) layerNormWeightGrads(const LnSumArg
   }
 }
 
-// A launch holds fewer than 2^32 threads along its grid: `blocks` workgroups
-// of `block` threads, as many as fit into half of that.  The kernels of the
-// weights' gradients step through the columns that are left over.
-unsigned gridOf(int64_t blocks, int block) {
-  const int64_t most = ((int64_t)1 << 31) / block;
-  return (unsigned)(blocks < most ? blocks : most);
-}
-
 // How a backward launch is cut: `threads` threads hold a row, `pieces` vectors
 // each (0 threads: the kernels for rows that registers do not hold), and at
 // most `most` workgroups.
@@ -821,74 +807,10 @@ int partialRows(int64_t rows, const BackwardCut& k) {
   return (int)(most < 1 ? 1 : most > k.most ? k.most : most);
 }
 
-struct Shape {
-  int64_t total = 0;
-  int launches = 0;
-};
-
-// Row counts, widths and strides every entry checks alike.
-bool shapeOk(const size_t* rows, int nranks, size_t cols, Shape* s) {
-  if (rows == nullptr || nranks < 1 || nranks > AR_MAX_RANKS || cols < 1 || cols > kLnMaxCols) return false;
-  s->total = 0;
-  for (int r = 0; r < nranks; ++r) {
-    if (rows[r] > (size_t)kLnMaxRows) return false;
-    s->total += (int64_t)rows[r];
-  }
-  if (s->total > kLnMaxRows) return false;
-  s->launches = (nranks + kLnRanks - 1) / kLnRanks;
-  return true;
-}
-
-bool strideOk(size_t stride, size_t cols) { return stride >= cols && stride <= (size_t)1 << 48; }
-
-bool aligned(const void* p, int esz) { return p != nullptr && (uintptr_t)p % (uintptr_t)esz == 0; }
-
-int64_t rowsOfLaunch(const size_t* rows, int nranks, int first) {
-  int64_t n = 0;
-  for (int r = first; r < nranks && r < first + kLnRanks; ++r) n += (int64_t)rows[r];
-  return n;
-}
-
-// Adds a rank's row buffer to the overlap check; false for a bad pointer.
-bool addRows(std::vector<Extent>& v, const void* p, size_t rows, size_t cols, size_t stride, int esz, bool output,
-             int pair) {
-  if (rows == 0) return true;
-  if (!aligned(p, esz) || rows > ((size_t)1 << 48) / stride) return false;
-  v.push_back(Extent{(uintptr_t)p, cols * (size_t)esz, rows, stride * (size_t)esz, output, pair});
-  return true;
-}
-
-bool addFlat(std::vector<Extent>& v, const void* p, size_t count, int esz, bool output) {
-  return addRows(v, p, count ? 1 : 0, count, count, esz, output, -1);
-}
-
-template <template <int, int> class F, typename... A>
-hipError_t byTypes(int dtype, int wtype, A... args) {
-  if (wtype == arFloat32) {
-    if (dtype == arFloat32) return F<arFloat32, arFloat32>::run(args...);
-    if (dtype == arFloat16) return F<arFloat16, arFloat32>::run(args...);
-    return F<arBfloat16, arFloat32>::run(args...);
-  }
-  if (dtype == arFloat16) return F<arFloat16, arFloat16>::run(args...);
-  return F<arBfloat16, arBfloat16>::run(args...);
-}
-
-// Shares `most` workgroups of `groups` rows at a time out among the ranks by
-// their rows, at least one to a rank with rows (so more than `most` only where
-// there are more such ranks); returns the grid.
+// Shares `most` workgroups of `groups` rows at a time out among the ranks;
+// returns the grid.
 int shareBlocks(LnArgs* a, int groups, int most) {
-  const int64_t rows = a->rowStart[a->nranks];
-  int ranks = 0;
-  for (int r = 0; r < a->nranks; ++r) ranks += a->rowStart[r + 1] > a->rowStart[r];
-  const double share = most > ranks ? (double)(most - ranks) / (double)rows : 0.0;
-  a->blockStart[0] = 0;
-  for (int r = 0; r < a->nranks; ++r) {
-    const int64_t n = a->rowStart[r + 1] - a->rowStart[r];
-    const int64_t full = (n + groups - 1) / groups;
-    const int64_t mine = n == 0 ? 0 : (int64_t)((double)n * share) + 1;
-    a->blockStart[r + 1] = a->blockStart[r] + (int)(mine < full ? mine : full);
-  }
-  return a->blockStart[a->nranks];
+  return shareOut(a->rowStart, a->nranks, groups, most, a->blockStart);
 }
 
 // What RowPieces assumes: all of a thread's vectors but the last lie inside the

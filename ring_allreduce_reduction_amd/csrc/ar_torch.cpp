@@ -32,6 +32,22 @@ typedef arResult_t (*ListCreateFn)(arTensorList_t*, int, const void* const*, voi
                                    const arDataType_t*);
 typedef arResult_t (*GradNormFn)(arTensorList_t, arNormKind_t, float, float*, void*, size_t, void*);
 typedef arResult_t (*GradClipFn)(arTensorList_t, arNormKind_t, float, float, float, float*, void*, size_t, void*);
+typedef arResult_t (*DropoutAddFn)(const void* const*, const void* const*, const void* const*, void* const*,
+                                   const size_t*, const uint64_t*, int, size_t, size_t, size_t, size_t, double,
+                                   uint64_t, uint64_t, const uint64_t*, arDataType_t, arDataType_t, void*);
+typedef arResult_t (*DropoutAddBackwardFn)(const void* const*, void* const*, void* const*, const size_t*,
+                                           const uint64_t*, int, size_t, size_t, size_t, double, uint64_t, uint64_t,
+                                           const uint64_t*, arDataType_t, arDataType_t, void*, size_t, void*);
+typedef arResult_t (*ShardWorkspaceFn)(size_t, const size_t*, int, size_t*);
+typedef arResult_t (*TokenLogprobFn)(const void* const*, const size_t*, const size_t*, int, size_t, const int64_t*,
+                                     float, float*, float*, float*, arDataType_t, void*, size_t, void*);
+typedef arResult_t (*TokenLogprobBackwardFn)(const float*, const void* const*, const size_t*, const size_t*, int,
+                                             size_t, const int64_t*, float, const float*, const float*, void* const*,
+                                             const size_t*, arDataType_t, void*);
+typedef arResult_t (*TokenWorkspaceFn)(const size_t*, int, size_t*);
+typedef arResult_t (*PolicyLossFn)(const float* const*, const float* const*, const float* const*, const float* const*,
+                                   const float* const*, float* const*, const size_t*, int, double, double, double,
+                                   double, double, float*, void*, size_t, void*);
 
 LayerNormFn gLayerNorm;
 LayerNormBackwardFn gLayerNormBackward;
@@ -39,6 +55,14 @@ WorkspaceFn gWorkspace;
 ListCreateFn gListCreate;
 GradNormFn gGradNorm;
 GradClipFn gGradClip;
+DropoutAddFn gDropoutAdd;
+DropoutAddBackwardFn gDropoutAddBackward;
+WorkspaceFn gDropoutWorkspace;
+TokenLogprobFn gTokenLogprob;
+TokenLogprobBackwardFn gTokenLogprobBackward;
+ShardWorkspaceFn gTokenLogprobWorkspace;
+PolicyLossFn gPolicyLoss;
+TokenWorkspaceFn gPolicyLossWorkspace;
 
 // A Python error is set and the call ends.
 struct PythonError {};
@@ -256,12 +280,13 @@ bool arguments(Py_ssize_t given, Py_ssize_t want) {
 }
 
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind takes six addresses");
+  constexpr int kEntries = 14;
+  if (n != kEntries) {
+    PyErr_Format(PyExc_TypeError, "bind takes %d addresses", kEntries);
     return nullptr;
   }
-  void* p[6];
-  for (int i = 0; i < 6; ++i) p[i] = PyLong_AsVoidPtr(args[i]);
+  void* p[kEntries];
+  for (int i = 0; i < kEntries; ++i) p[i] = PyLong_AsVoidPtr(args[i]);
   if (PyErr_Occurred()) return nullptr;
   gLayerNorm = (LayerNormFn)p[0];
   gLayerNormBackward = (LayerNormBackwardFn)p[1];
@@ -269,6 +294,14 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
   gListCreate = (ListCreateFn)p[3];
   gGradNorm = (GradNormFn)p[4];
   gGradClip = (GradClipFn)p[5];
+  gDropoutAdd = (DropoutAddFn)p[6];
+  gDropoutAddBackward = (DropoutAddBackwardFn)p[7];
+  gDropoutWorkspace = (WorkspaceFn)p[8];
+  gTokenLogprob = (TokenLogprobFn)p[9];
+  gTokenLogprobBackward = (TokenLogprobBackwardFn)p[10];
+  gTokenLogprobWorkspace = (ShardWorkspaceFn)p[11];
+  gPolicyLoss = (PolicyLossFn)p[12];
+  gPolicyLossWorkspace = (TokenWorkspaceFn)p[13];
   Py_RETURN_NONE;
 }
 
@@ -422,12 +455,282 @@ PyObject* gradNorm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// What a dropout draws from: probability, seed, offset, the step on the device,
+// the index of each rank's first row.
+struct Draw {
+  double p;
+  uint64_t seed, offset;
+  const uint64_t* step = nullptr;
+  bool hasFirst = false;
+  uint64_t first[AR_MAX_RANKS];
+
+  static uint64_t word(PyObject* o) {
+    PyObject* index = PyNumber_Index(o);
+    if (index == nullptr) throw PythonError();
+    const uint64_t v = PyLong_AsUnsignedLongLong(index);
+    Py_DECREF(index);
+    if (PyErr_Occurred()) throw PythonError();
+    return v;
+  }
+
+  // args: p, seed, offset, step
+  Draw(PyObject* const* args, PyObject* firstRows, int n, Devices* devices) {
+    p = PyFloat_AsDouble(args[0]);
+    if (PyErr_Occurred()) throw PythonError();
+    seed = word(args[1]);
+    offset = word(args[2]);
+    if (args[3] != Py_None) {
+      const at::Tensor& t = tensorOf(args[3]);
+      if (t.scalar_type() != at::kLong || t.numel() != 1) fail("step must be an int64 tensor of one element");
+      devices->see(t);
+      step = (const uint64_t*)t.data_ptr();
+    }
+    if (firstRows == Py_None) return;
+    PyObject* fast = PySequence_Fast(firstRows, "expected a list of the ranks' first rows");
+    if (fast == nullptr) throw PythonError();
+    hasFirst = true;
+    const Py_ssize_t got = PySequence_Fast_GET_SIZE(fast);
+    try {
+      if (got != n) fail("need %d first rows, got %zd", n, got);
+      for (int r = 0; r < n; ++r) first[r] = word(PySequence_Fast_GET_ITEM(fast, r));
+    } catch (const PythonError&) {
+      Py_DECREF(fast);
+      throw;
+    }
+    Py_DECREF(fast);
+  }
+};
+
+// dropout_add(xs, ys, p, seed, offset, step, biases, residuals, firstRows, stream) -> result code
+PyObject* dropoutAdd(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!arguments(n, 10)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    Call c;
+    const List xs(args[0]);
+    c.start(xs, args + 6, 1);
+    void *x[AR_MAX_RANKS], *y[AR_MAX_RANKS], *b[AR_MAX_RANKS], *z[AR_MAX_RANKS];
+    const size_t xStride = c.rowBuffers("input", xs, x, true);
+    const List ys(args[1]);
+    const size_t yStride = c.rowBuffers("output", ys, y, false);
+    const bool bias = args[6] != Py_None, residual = args[7] != Py_None;
+    if (bias) c.flatBuffers("bias", args[6], c.weights, false, b);
+    size_t zStride = (size_t)c.cols;
+    if (residual) {
+      const List zs(args[7]);
+      zStride = c.rowBuffers("residual", zs, z, false);
+    }
+    const Draw d(args + 2, args[8], c.n, &c.devices);
+    c.devices.check();
+    void* stream = streamOf(args[9], c.devices);
+    return result([&] {
+      return gDropoutAdd(x, bias ? b : nullptr, residual ? z : nullptr, y, c.rows, d.hasFirst ? d.first : nullptr, c.n,
+                         (size_t)c.cols, xStride, zStride, yStride, d.p, d.seed, d.offset, d.step, codeOf(c.type),
+                         codeOf(c.weights), stream);
+    });
+  });
+}
+
+// dropout_add_backward(dys, dxs, p, seed, offset, step, dbiases, firstRows, workspace, stream) -> result code, or the
+// bytes of workspace it needs as a negative number where workspace is None and it needs one
+PyObject* dropoutAddBackward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!arguments(n, 10)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    Call c;
+    const List dys(args[0]);
+    c.start(dys, args + 6, 1);
+    void *dy[AR_MAX_RANKS], *dx[AR_MAX_RANKS], *b[AR_MAX_RANKS];
+    const size_t dyStride = c.rowBuffers("output gradient", dys, dy, true);
+    const bool hasDx = args[1] != Py_None, bias = args[6] != Py_None;
+    size_t dxStride = (size_t)c.cols;
+    if (hasDx) {
+      const List dxs(args[1]);
+      dxStride = c.rowBuffers("input gradient", dxs, dx, false);
+    }
+    if (bias) c.flatBuffers("bias gradient", args[6], c.weights, false, b);
+    const Draw d(args + 2, args[7], c.n, &c.devices);
+    size_t need = 0;
+    void* workspace = nullptr;
+    if (bias) {
+      const arResult_t r = gDropoutWorkspace(c.rows, c.n, (size_t)c.cols, &need);
+      if (r != arSuccess) return PyLong_FromLong((long)r);
+      workspace = workspaceOf(args[8], need, &c.devices);
+    }
+    c.devices.check();
+    if (need > 0 && workspace == nullptr) return PyLong_FromLongLong(-(long long)need);
+    void* stream = streamOf(args[9], c.devices);
+    return result([&] {
+      return gDropoutAddBackward(dy, hasDx ? dx : nullptr, bias ? b : nullptr, c.rows, d.hasFirst ? d.first : nullptr,
+                                 c.n, (size_t)c.cols, dyStride, dxStride, d.p, d.seed, d.offset, d.step,
+                                 codeOf(c.type), codeOf(c.weights), workspace, need, stream);
+    });
+  });
+}
+
+// Logits cut over the ranks: one (rows, columns) buffer each, its own width and
+// row stride.
+struct Shards {
+  int n = 0;
+  int64_t rows = 0;
+  at::ScalarType type = at::kFloat;
+  size_t cols[AR_MAX_RANKS], strides[AR_MAX_RANKS];
+  void* at[AR_MAX_RANKS];
+
+  // `like`: the logits whose gradients these are, or null.
+  Shards(const char* what, PyObject* o, const Shards* like, Devices* devices) {
+    const List l(o);
+    n = l.n;
+    if (n < 1) fail("need at least one rank");
+    if (like && n != like->n) fail("need %d %s buffers, got %d", like->n, what, n);
+    for (int r = 0; r < n; ++r) {
+      const at::Tensor& t = l[r];
+      const int64_t dim = t.dim();
+      if (!floatType(t.scalar_type()) || dim < 1)
+        fail("%s buffers must be float32, float16 or bfloat16 tensors of at least one dimension", what);
+      if (r == 0) type = t.scalar_type();
+      if (t.scalar_type() != (like ? like->type : type))
+        fail("%s buffer %d is %s, expected %s like the others", what, r, typeName(t.scalar_type()),
+             typeName(like ? like->type : type));
+      int64_t k = 1;
+      for (int64_t i = 0; i + 1 < dim; ++i) k *= t.size(i);
+      if (r == 0) rows = k;
+      if (k != (like ? like->rows : rows))
+        fail("%s buffer %d has %lld rows, expected %lld", what, r, (long long)k, (long long)(like ? like->rows : rows));
+      const int64_t width = t.size(-1);
+      if (like && (size_t)width != like->cols[r])
+        fail("%s buffer %d has %lld columns, expected %lld", what, r, (long long)width, (long long)like->cols[r]);
+      int64_t s = width;
+      if (!t.is_contiguous()) {
+        if (dim != 2 || (width > 1 && t.stride(1) != 1) || (k > 1 && t.stride(0) < width))
+          fail("%s buffer %d must have contiguous rows", what, r);
+        if (k > 1) s = t.stride(0);
+      }
+      devices->see(t);
+      cols[r] = (size_t)width;
+      strides[r] = (size_t)(s > 0 ? s : 1);
+      at[r] = t.data_ptr();
+    }
+  }
+};
+
+// A dense tensor of `count` elements of type t, or null for None where that is allowed.
+void* denseOf(const char* what, PyObject* o, at::ScalarType t, int64_t count, bool optional, Devices* devices) {
+  if (optional && o == Py_None) return nullptr;
+  const at::Tensor& b = tensorOf(o);
+  if (b.scalar_type() != t) fail("%s is %s, expected %s", what, typeName(b.scalar_type()), typeName(t));
+  if (!b.is_contiguous() || b.numel() != count)
+    fail("%s must hold %lld contiguous elements", what, (long long)count);
+  devices->see(b);
+  return b.data_ptr();
+}
+
+// token_logprob(logits, targets, logp, top, logSum, scale, workspace, stream) -> result code, or the bytes of
+// workspace it needs as a negative number where workspace is None and it needs one
+PyObject* tokenLogprob(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!arguments(n, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    Devices devices;
+    const Shards x("logits", args[0], nullptr, &devices);
+    const int64_t* targets = (const int64_t*)denseOf("targets", args[1], at::kLong, x.rows, false, &devices);
+    float* logp = (float*)denseOf("logp", args[2], at::kFloat, x.rows, false, &devices);
+    float* top = (float*)denseOf("top", args[3], at::kFloat, x.rows, true, &devices);
+    float* logSum = (float*)denseOf("logSum", args[4], at::kFloat, x.rows, true, &devices);
+    const float scale = (float)PyFloat_AsDouble(args[5]);
+    if (PyErr_Occurred()) return nullptr;
+    size_t need = 0;
+    const arResult_t r = gTokenLogprobWorkspace((size_t)x.rows, x.cols, x.n, &need);
+    if (r != arSuccess) return PyLong_FromLong((long)r);
+    void* workspace = need > 0 ? workspaceOf(args[6], need, &devices) : nullptr;
+    devices.check();
+    if (need > 0 && workspace == nullptr) return PyLong_FromLongLong(-(long long)need);
+    void* stream = streamOf(args[7], devices);
+    return result([&] {
+      return gTokenLogprob(x.at, x.cols, x.strides, x.n, (size_t)x.rows, targets, scale, logp, top, logSum,
+                           codeOf(x.type), workspace, need, stream);
+    });
+  });
+}
+
+// token_logprob_backward(dlogp, logits, targets, top, logSum, dlogits, scale, stream) -> result code
+PyObject* tokenLogprobBackward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!arguments(n, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    Devices devices;
+    const Shards x("logits", args[1], nullptr, &devices);
+    const float* dlogp = (const float*)denseOf("dlogp", args[0], at::kFloat, x.rows, false, &devices);
+    const int64_t* targets = (const int64_t*)denseOf("targets", args[2], at::kLong, x.rows, false, &devices);
+    const float* top = (const float*)denseOf("top", args[3], at::kFloat, x.rows, false, &devices);
+    const float* logSum = (const float*)denseOf("logSum", args[4], at::kFloat, x.rows, false, &devices);
+    const Shards dx("logits gradient", args[5], &x, &devices);
+    const float scale = (float)PyFloat_AsDouble(args[6]);
+    if (PyErr_Occurred()) return nullptr;
+    devices.check();
+    void* stream = streamOf(args[7], devices);
+    return result([&] {
+      return gTokenLogprobBackward(dlogp, x.at, x.cols, x.strides, x.n, (size_t)x.rows, targets, scale, top, logSum,
+                                   dx.at, dx.strides, codeOf(x.type), stream);
+    });
+  });
+}
+
+// policy_loss(logps, olds, refs, advantages, weights, dlogps, clipLow, clipHigh, klCoef, denominator, gradScale,
+// stats, workspace, stream) -> result code, or the bytes of workspace it needs as a negative number where workspace
+// is None and it needs one
+PyObject* policyLoss(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  if (!arguments(n, 14)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    static const char* const kWhat[6] = {"logp", "old logp", "reference logp", "advantage", "weight", "logp gradient"};
+    Devices devices;
+    size_t tokens[AR_MAX_RANKS];
+    float* p[6][AR_MAX_RANKS];
+    bool has[6];
+    int ranks = 0;
+    for (int k = 0; k < 6; ++k) {
+      has[k] = args[k] != Py_None;
+      if (!has[k] && (k == 2 || k == 4 || k == 5)) continue;
+      const List l(args[k]);
+      if (k == 0) ranks = l.n;
+      if (ranks < 1) fail("need at least one rank");
+      if (l.n != ranks) fail("need %d %s buffers, got %d", ranks, kWhat[k], l.n);
+      for (int r = 0; r < ranks; ++r) {
+        const at::Tensor& t = l[r];
+        if (t.scalar_type() != at::kFloat)
+          fail("%s buffer %d is %s, expected torch.float32", kWhat[k], r, typeName(t.scalar_type()));
+        if (k == 0) tokens[r] = (size_t)t.numel();
+        if (!t.is_contiguous() || (size_t)t.numel() != tokens[r])
+          fail("%s buffer %d must hold %lld contiguous elements", kWhat[k], r, (long long)tokens[r]);
+        devices.see(t);
+        p[k][r] = (float*)t.data_ptr();
+      }
+    }
+    double v[5];
+    for (int i = 0; i < 5; ++i) v[i] = PyFloat_AsDouble(args[6 + i]);
+    if (PyErr_Occurred()) return nullptr;
+    float* stats = (float*)denseOf("stats", args[11], at::kFloat, 5, false, &devices);
+    size_t need = 0;
+    const arResult_t r = gPolicyLossWorkspace(tokens, ranks, &need);
+    if (r != arSuccess) return PyLong_FromLong((long)r);
+    void* workspace = need > 0 ? workspaceOf(args[12], need, &devices) : nullptr;
+    devices.check();
+    if (need > 0 && workspace == nullptr) return PyLong_FromLongLong(-(long long)need);
+    void* stream = streamOf(args[13], devices);
+    return result([&] {
+      return gPolicyLoss(p[0], p[1], has[2] ? p[2] : nullptr, p[3], has[4] ? p[4] : nullptr, has[5] ? p[5] : nullptr,
+                         tokens, ranks, v[0], v[1], v[2], v[3], v[4], stats, workspace, need, stream);
+    });
+  });
+}
+
 #define FAST(f) ((PyCFunction)(void (*)(void))(f))
 PyMethodDef kMethods[] = {{"bind", FAST(bind), METH_FASTCALL, nullptr},
                           {"layer_norm", FAST(layerNorm), METH_FASTCALL, nullptr},
                           {"layer_norm_backward", FAST(layerNormBackward), METH_FASTCALL, nullptr},
                           {"tensor_list", FAST(tensorList), METH_FASTCALL, nullptr},
                           {"grad_norm", FAST(gradNorm), METH_FASTCALL, nullptr},
+                          {"dropout_add", FAST(dropoutAdd), METH_FASTCALL, nullptr},
+                          {"dropout_add_backward", FAST(dropoutAddBackward), METH_FASTCALL, nullptr},
+                          {"token_logprob", FAST(tokenLogprob), METH_FASTCALL, nullptr},
+                          {"token_logprob_backward", FAST(tokenLogprobBackward), METH_FASTCALL, nullptr},
+                          {"policy_loss", FAST(policyLoss), METH_FASTCALL, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_ar_torch", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
