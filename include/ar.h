@@ -819,8 +819,9 @@ arResult_t arTokenLogprobBackward(const float* dlogp, const void* const* logits,
  *            the weights.
  *  workspace, workspaceBytes  see above; may be NULL / 0 where
  *            arPolicyLossWorkspace reports 0.
- * A token's terms and all sums are formed in 64 bits: which tokens are clipped
- * does not depend on roundings, and a small kl keeps its bits.
+ * Which tokens are clipped is decided in 64 bits, so that it does not depend on
+ * roundings; all sums are in 64 bits; a token's terms are formed in 32 (a ratio
+ * past 3.4e38 is infinite), a small kl with all its bits.
  * Outputs must not overlap any other buffer.  Errors: as arTokenLogprob.
  */
 arResult_t arPolicyLoss(const float* const* logp, const float* const* old, const float* const* ref,

@@ -7,11 +7,13 @@
 //   kl = exp(f - l) - (f - l) - 1,
 //   L = sum w (loss + beta kl) / W,  W = the sum of all weights or given,
 //   dL/dl = w / W (-A r [not clipped] + beta (1 - exp(f - l))).
-// The mean is over all ranks, so the gradient needs a sum of every token
-// first: two passes, the second from the caches.  A token's terms are formed
-// in 64 bits: whether its ratio passes a bound is a comparison of numbers that
-// nearly agree, kl is a difference of nearly equal numbers, and the sums may be
-// long.
+// The mean is over all ranks, so the gradient's factor is a sum over every
+// token: the first pass leaves the sums and the gradients short of that factor,
+// the second multiplies them by it.  Whether a ratio passes a bound is decided
+// by differences in 64 bits against the bounds' logarithms, since these are
+// numbers that may nearly agree; the sums are in 64 bits; what lies between is
+// formed in 32, kl by its series where it is a difference of nearly equal
+// numbers.
 #include <cmath>
 #include <new>
 #include <vector>
@@ -22,10 +24,12 @@ namespace ar {
 namespace {
 
 constexpr int kPolBlock = 256;
-constexpr int kPolSums = 4;            // weighted loss, kl, clipped tokens, weights
-constexpr int kPolGrid = 2 * kOpsCUs;  // workgroups, and partial sums, of a launch at most
-constexpr int kPolFew = 4096;          // tokens of one workgroup's launch
+constexpr int kPolSums = 4;            // weights, weighted loss, kl, clipped tokens
+constexpr int kPolGrid = 4 * kOpsCUs;  // workgroups, and partial sums, of a launch's first pass at most
+constexpr int kPolVec = 4;             // tokens of a thread at a time
 constexpr int kPolFewBlock = 1024;
+constexpr int kPolFewEach = 4;
+constexpr int kPolFew = kPolFewBlock * kPolFewEach;   // tokens of one workgroup's launch
 
 struct PolArgs {
   const float* logp[kOpRanks];
@@ -41,28 +45,40 @@ struct PolArgs {
   double* partial;                     // kPolSums rows of `partials`; the first pass: from this launch's first
   float* stats;                        // where the launch writes them, or null
   double logLow, logHigh;              // log(1 - low), log(1 + high)
-  double low, high;                    // 1 - low, 1 + high
+  float low, high;                     // 1 - low, 1 + high
   double klCoef, denominator, gradScale;
 };
 
 struct Token {
-  double loss, kl, clipped, dlogp;
+  float loss, kl, dlogp;
+  bool clipped;
 };
+
+// exp(d) - 1 and exp(d) - 1 - d, below |d| = 1 from the exponential's series
+// through d^12 (what is left out is 2^-31 of the result): there they are
+// differences of nearly equal numbers.
+__device__ __forceinline__ float2 expLess(float d) {
+  float s = 1.0f;
+#pragma unroll
+  for (int n = 12; n > 2; --n) s = fmaf(d * (1.0f / n), s, 1.0f);
+  const float near = 0.5f * d * d * s, e = expf(d) - 1.0f;
+  return fabsf(d) < 1.0f ? make_float2(near + d, near) : make_float2(e, e - d);
+}
 
 __device__ __forceinline__ Token tokenOf(const PolArgs& a, float logp, float old, float advantage, bool hasRef,
                                          float ref) {
   Token t;
-  const double change = (double)logp - (double)old, adv = advantage;
-  const bool up = adv > 0.0 && change > a.logHigh, down = adv < 0.0 && change < a.logLow;
-  const double ratio = exp(change);
-  t.clipped = up || down ? 1.0 : 0.0;
-  t.loss = -adv * (up ? a.high : down ? a.low : ratio);
-  t.dlogp = up || down ? 0.0 : -adv * ratio;
-  t.kl = 0.0;
+  const double change = (double)logp - (double)old;
+  const bool up = advantage > 0.0f && change > a.logHigh, down = advantage < 0.0f && change < a.logLow;
+  const float ratio = expf((float)change);
+  t.clipped = up || down;
+  t.loss = -advantage * (up ? a.high : down ? a.low : ratio);
+  t.dlogp = t.clipped ? 0.0f : -advantage * ratio;
+  t.kl = 0.0f;
   if (hasRef) {
-    const double d = (double)ref - (double)logp, e = expm1(d);
-    t.kl = e - d;
-    t.dlogp -= a.klCoef * e;
+    const float2 less = expLess((float)((double)ref - (double)logp));
+    t.kl = less.y;
+    t.dlogp -= (float)a.klCoef * less.x;
   }
   return t;
 }
@@ -73,31 +89,34 @@ __device__ __forceinline__ double waveSum64(double v) {
   return v;
 }
 
-// Sums of four over a workgroup; every thread receives them.
-template <int BLOCK>
-__device__ __forceinline__ void blockSums(double (&s)[kPolSums], double (*lds)[kPolSums]) {
+// N sums over a workgroup; every thread receives them.
+template <int BLOCK, int N>
+__device__ __forceinline__ void blockSums(double (&s)[N], double (*lds)[N]) {
 #pragma unroll
-  for (int k = 0; k < kPolSums; ++k) s[k] = waveSum64(s[k]);
+  for (int k = 0; k < N; ++k) s[k] = waveSum64(s[k]);
   if (threadIdx.x % kWave == 0)
 #pragma unroll
-    for (int k = 0; k < kPolSums; ++k) lds[threadIdx.x / kWave][k] = s[k];
+    for (int k = 0; k < N; ++k) lds[threadIdx.x / kWave][k] = s[k];
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kPolSums; ++k) {
+  for (int k = 0; k < N; ++k) {
     s[k] = lds[0][k];
     for (int w = 1; w < BLOCK / kWave; ++w) s[k] += lds[w][k];
   }
 }
 
-__device__ __forceinline__ void addToken(const PolArgs& a, int r, int i, double (&s)[kPolSums]) {
-  const double w = a.weight[r] ? (double)a.weight[r][i] : 1.0;
-  if (w == 0.0) return;
-  const Token t = tokenOf(a, a.logp[r][i], a.old[r][i], a.advantage[r][i], a.ref[r] != nullptr,
-                          a.ref[r] ? a.ref[r][i] : 0.0f);
-  s[0] += w * t.loss;
-  s[1] += w * t.kl;
-  s[2] += w * t.clipped;
-  s[3] += w;
+// Adds a token up and returns its gradient short of the common factor.  One of
+// weight 0 is left out, whatever its other values are.
+__device__ __forceinline__ float addToken(const PolArgs& a, float logp, float old, float advantage, bool hasRef,
+                                          float ref, float weight, double (&s)[kPolSums]) {
+  if (weight == 0.0f) return 0.0f;
+  const Token t = tokenOf(a, logp, old, advantage, hasRef, ref);
+  const double w = weight;
+  s[0] += w;
+  s[1] += w * (double)t.loss;
+  s[2] += w * (double)t.kl;
+  s[3] += t.clipped ? w : 0.0;
+  return weight * t.dlogp;
 }
 
 __device__ __forceinline__ double partOf(const PolArgs& a, double weights) {
@@ -106,85 +125,153 @@ __device__ __forceinline__ double partOf(const PolArgs& a, double weights) {
 }
 
 __device__ __forceinline__ void putStats(const PolArgs& a, const double (&s)[kPolSums]) {
-  const double part = partOf(a, s[3]), policy = s[0] * part, kl = s[1] * part;
+  const double part = partOf(a, s[0]), policy = s[1] * part, kl = s[2] * part;
   a.stats[0] = (float)(policy + a.klCoef * kl);
   a.stats[1] = (float)policy;
   a.stats[2] = (float)kl;
-  a.stats[3] = (float)(s[2] * part);
-  a.stats[4] = (float)s[3];
+  a.stats[3] = (float)(s[3] * part);
+  a.stats[4] = (float)s[0];
 }
 
-__device__ __forceinline__ void putGrad(const PolArgs& a, int r, int i, double factor) {
-  const double w = a.weight[r] ? (double)a.weight[r][i] : 1.0;
-  float d = 0.0f;
-  if (w != 0.0 && factor != 0.0) {
-    const Token t = tokenOf(a, a.logp[r][i], a.old[r][i], a.advantage[r][i], a.ref[r] != nullptr,
-                            a.ref[r] ? a.ref[r][i] : 0.0f);
-    d = (float)(factor * w * t.dlogp);
-  }
-  a.dlogp[r][i] = d;
+// A gradient and the factor it was short of; 0 where nothing counts, whatever
+// the gradient is.
+__device__ __forceinline__ float timesFactor(float d, double factor) {
+  return factor != 0.0 ? (float)((double)d * factor) : 0.0f;
 }
 
-// A workgroup's rank, and its share of that rank's tokens: every step-th from
-// the first.
+// A workgroup's rank, and a thread's share of that rank's tokens: every
+// step-th vector from the first, and one of the few tokens behind the last.
 struct PolPlace {
-  int rank, first, step, count;
+  int rank, count, whole;
+  int64_t first, step;
 };
 
 __device__ __forceinline__ PolPlace polPlace(const PolArgs& a) {
   PolPlace p;
   p.rank = 0;
   while ((int)blockIdx.x >= a.blockStart[p.rank + 1]) ++p.rank;
-  p.first = ((int)blockIdx.x - a.blockStart[p.rank]) * kPolBlock + (int)threadIdx.x;
-  p.step = (a.blockStart[p.rank + 1] - a.blockStart[p.rank]) * kPolBlock;
+  const int block = (int)blockIdx.x - a.blockStart[p.rank];
   p.count = a.start[p.rank + 1] - a.start[p.rank];
+  p.whole = p.count / kPolVec * kPolVec;
+  p.first = ((int64_t)block * kPolBlock + threadIdx.x) * kPolVec;
+  p.step = (int64_t)(a.blockStart[p.rank + 1] - a.blockStart[p.rank]) * kPolBlock * kPolVec;
   return p;
+}
+
+// Calls f(first token) for a thread's vectors, then g(token) for its part of
+// the rest, which the rank's first workgroup takes.
+template <typename F, typename G>
+__device__ __forceinline__ void forTokens(const PolPlace& p, F f, G g) {
+#pragma unroll 2
+  for (int64_t i = p.first; i < p.whole; i += p.step) f(i);
+  const int64_t i = p.whole + p.first / kPolVec;
+  if (i < p.count) g(i);
 }
 
 __global__ void __launch_bounds__(kPolBlock) policySums(const PolArgs a) {
   __shared__ double lds[kPolBlock / kWave][kPolSums];
   const PolPlace at = polPlace(a);
+  const float *logp = a.logp[at.rank], *old = a.old[at.rank], *ref = a.ref[at.rank];
+  const float *advantage = a.advantage[at.rank], *weight = a.weight[at.rank];
+  float* dlogp = a.dlogp[at.rank];
   double s[kPolSums] = {0.0, 0.0, 0.0, 0.0};
-  for (int64_t i = at.first; i < at.count; i += at.step) addToken(a, at.rank, (int)i, s);
+  forTokens(
+      at,
+      [&](int64_t i) {
+        typedef FloatVec<kPolVec> Vec;
+        const Vec l = loadVec<float, kPolVec>(logp + i), o = loadVec<float, kPolVec>(old + i);
+        const Vec v = loadVec<float, kPolVec>(advantage + i);
+        const Vec f = ref ? loadVec<float, kPolVec>(ref + i) : (Vec)0.0f;
+        const Vec w = weight ? loadVec<float, kPolVec>(weight + i) : (Vec)1.0f;
+        Vec d;
+#pragma unroll
+        for (int e = 0; e < kPolVec; ++e) d[e] = addToken(a, l[e], o[e], v[e], ref != nullptr, f[e], w[e], s);
+        if (dlogp) storeVec<float, kPolVec>(dlogp + i, d);
+      },
+      [&](int64_t i) {
+        const float d = addToken(a, logp[i], old[i], advantage[i], ref != nullptr, ref ? ref[i] : 0.0f,
+                                 weight ? weight[i] : 1.0f, s);
+        if (dlogp) dlogp[i] = d;
+      });
   blockSums<kPolBlock>(s, lds);
   if (threadIdx.x == 0)
 #pragma unroll
     for (int k = 0; k < kPolSums; ++k) a.partial[(size_t)k * a.partials + blockIdx.x] = s[k];
 }
 
+// The sums of the first pass in one order for every workgroup, and what they
+// are needed for: the stats, and each gradient's factor.
 __global__ void __launch_bounds__(kPolBlock) policyGrad(const PolArgs a) {
-  __shared__ double lds[kPolBlock / kWave][kPolSums];
-  double s[kPolSums] = {0.0, 0.0, 0.0, 0.0};
-  for (int i = threadIdx.x; i < a.partials; i += kPolBlock)
+  __shared__ double lds[kPolBlock / kWave][1], ldsAll[kPolBlock / kWave][kPolSums];
+  double weights[1] = {0.0};
+  for (int i = threadIdx.x; i < a.partials; i += kPolBlock) weights[0] += a.partial[i];
+  blockSums<kPolBlock>(weights, lds);
+  if (a.stats && blockIdx.x == 0) {
+    double s[kPolSums] = {0.0, 0.0, 0.0, 0.0};
+    for (int i = threadIdx.x; i < a.partials; i += kPolBlock)
 #pragma unroll
-    for (int k = 0; k < kPolSums; ++k) s[k] += a.partial[(size_t)k * a.partials + i];
-  blockSums<kPolBlock>(s, lds);
-  if (a.stats && blockIdx.x == 0 && threadIdx.x == 0) putStats(a, s);
+      for (int k = 0; k < kPolSums; ++k) s[k] += a.partial[(size_t)k * a.partials + i];
+    blockSums<kPolBlock>(s, ldsAll);
+    if (threadIdx.x == 0) putStats(a, s);
+  }
   if (a.start[a.nranks] == 0) return;   // a launch for the stats alone
   const PolPlace at = polPlace(a);
-  if (a.dlogp[at.rank] == nullptr) return;
-  const double factor = a.gradScale * partOf(a, s[3]);
-  for (int64_t i = at.first; i < at.count; i += at.step) putGrad(a, at.rank, (int)i, factor);
+  float* dlogp = a.dlogp[at.rank];
+  if (dlogp == nullptr) return;
+  const double factor = a.gradScale * partOf(a, weights[0]);
+  forTokens(
+      at,
+      [&](int64_t i) {
+        FloatVec<kPolVec> d = loadVec<float, kPolVec>(dlogp + i);
+#pragma unroll
+        for (int e = 0; e < kPolVec; ++e) d[e] = timesFactor(d[e], factor);
+        storeVec<float, kPolVec>(dlogp + i, d);
+      },
+      [&](int64_t i) { dlogp[i] = timesFactor(dlogp[i], factor); });
 }
 
-// Few tokens: one workgroup, one launch.
+// Few tokens: one workgroup, one launch, the gradients kept in registers until
+// their factor is known.
 __global__ void __launch_bounds__(kPolFewBlock) policyFew(const PolArgs a) {
   __shared__ double lds[kPolFewBlock / kWave][kPolSums];
-  double s[kPolSums] = {0.0, 0.0, 0.0, 0.0};
+  // the ranks' buffers, to be indexed by a token's place among all of them
+  __shared__ struct { const float *logp, *old, *ref, *advantage, *weight; float* dlogp; } at[kOpRanks];
   for (int r = 0; r < a.nranks; ++r)
-    for (int i = threadIdx.x; i < a.start[r + 1] - a.start[r]; i += kPolFewBlock) addToken(a, r, i, s);
+    if ((int)threadIdx.x == r) at[r] = {a.logp[r], a.old[r], a.ref[r], a.advantage[r], a.weight[r], a.dlogp[r]};
+  __syncthreads();
+  const int count = a.start[a.nranks];
+  double s[kPolSums] = {0.0, 0.0, 0.0, 0.0};
+  float d[kPolFewEach];
+  int rank[kPolFewEach], place[kPolFewEach];
+#pragma unroll
+  for (int k = 0; k < kPolFewEach; ++k) {
+    const int token = (int)threadIdx.x + k * kPolFewBlock;
+    rank[k] = 0;
+    place[k] = token;
+    for (int r = 1; r < a.nranks; ++r)
+      if (token >= a.start[r]) {
+        rank[k] = r;
+        place[k] = token - a.start[r];
+      }
+    if (token >= count) continue;
+    const auto& p = at[rank[k]];
+    const int i = place[k];
+    d[k] = addToken(a, p.logp[i], p.old[i], p.advantage[i], p.ref != nullptr, p.ref ? p.ref[i] : 0.0f,
+                    p.weight ? p.weight[i] : 1.0f, s);
+  }
   blockSums<kPolFewBlock>(s, lds);
   if (threadIdx.x == 0) putStats(a, s);
-  const double factor = a.gradScale * partOf(a, s[3]);
-  for (int r = 0; r < a.nranks; ++r) {
-    if (a.dlogp[r] == nullptr) continue;
-    for (int i = threadIdx.x; i < a.start[r + 1] - a.start[r]; i += kPolFewBlock) putGrad(a, r, i, factor);
+  const double factor = a.gradScale * partOf(a, s[0]);
+#pragma unroll
+  for (int k = 0; k < kPolFewEach; ++k) {
+    if ((int)threadIdx.x + k * kPolFewBlock < count && at[rank[k]].dlogp)
+      at[rank[k]].dlogp[place[k]] = timesFactor(d[k], factor);
   }
 }
 
 // Workgroups, and partial sums, of a launch of `tokens` tokens.
 int polBlocks(int64_t tokens) {
-  const int64_t full = (tokens + kPolBlock - 1) / kPolBlock;
+  const int64_t full = (tokens + kPolBlock * kPolVec - 1) / (kPolBlock * kPolVec);
   return (int)(full < kPolGrid ? full : kPolGrid);
 }
 
@@ -221,7 +308,7 @@ void fillTokens(PolArgs* a, const float* const* logp, const float* const* old, c
     a->dlogp[r] = any && dlogp ? dlogp[k] : nullptr;
   }
   const int64_t n = a->start[a->nranks];
-  if (n > 0) shareOut(a->start, a->nranks, kPolBlock, polBlocks(n), a->blockStart);
+  if (n > 0) shareOut(a->start, a->nranks, kPolBlock * kPolVec, polBlocks(n), a->blockStart);
   else a->blockStart[a->nranks] = 0;
 }
 
@@ -261,8 +348,8 @@ arResult_t policyLoss(const float* const* logp, const float* const* old, const f
   }
   if (outputsOverlap(v)) return arInvalidArgument;
   PolArgs a{};
-  a.low = 1.0 - clipLow;
-  a.high = 1.0 + clipHigh;
+  a.low = (float)(1.0 - clipLow);
+  a.high = (float)(1.0 + clipHigh);
   a.logLow = std::log1p(-clipLow);
   a.logHigh = std::log1p(clipHigh);
   a.klCoef = klCoef;

@@ -107,7 +107,29 @@ def policy(logps, olds, refs, advantages, weights, low, high, kl_coef, denominat
     def mean(v):
         return torch.where(zero, 0.0, w * v).sum() * part
 
+    # What 32 bits are off.  The ratio: its logarithm's rounding, the exponential (2 U), the product with A.
+    change = (logp - old).abs()
+    d_pg = U * (change + 4) * (adv * ratio).abs()
+    d_loss = torch.where(clipped, 2 * U * loss.abs(), d_pg)
+    d_kl = torch.zeros_like(loss)
+    d_grad = torch.where(clipped, 0.0, d_pg)
+    if refs is not None:
+        # the difference's rounding moves kl by |d (exp(d) - 1)| U and exp(d) - 1 by |d| exp(d) U; the series' factors
+        # and products 8 U of kl; past 1 the exponential 2 U, the differences' roundings
+        e, less, far = torch.exp(d), torch.expm1(d).abs(), d.abs() >= 1
+        d_kl = U * (d.abs() * less + 8 * kl + torch.where(far, 2 * e + less, 0.0))
+        d_less = d_kl + U * (d.abs() * e + less + 2 * d.abs())
+        d_grad = d_grad + kl_coef * (d_less + 3 * U * less)
+    d_grad = (d_grad + 3 * U * g.abs()) * (grad_scale * part * w).abs()
     stats = torch.stack((mean(loss) + kl_coef * mean(kl), mean(loss), mean(kl), mean(clipped.double()), total))
-    size = torch.stack((mean(loss.abs()) + kl_coef * mean(kl.abs()), mean(loss.abs()), mean(kl.abs()), mean(clipped.double()), total))
+    # sums in 64 bits of n terms: n 2^-53 of the terms' sizes
+    n = loss.numel() + 64
+
+    def off(v, dv):
+        return mean(dv) + n * 2.0 ** -53 * mean(v.abs())
+
+    bounds = torch.stack((off(loss, d_loss) + kl_coef * off(kl, d_kl) + 2.0 ** -53 * 8 * mean(loss.abs()), off(loss, d_loss), off(kl, d_kl),
+                          n * 2.0 ** -53 * mean(clipped.double()), n * 2.0 ** -53 * w.abs().sum()))
+    widths = [len(t) for t in logps]
     grads = torch.where(zero, 0.0, grad_scale * part * w * g)
-    return stats, size, list(grads.split([len(t) for t in logps]))
+    return stats, bounds, list(grads.split(widths)), list(torch.where(zero, 0.0, d_grad + n * 2.0 ** -53 * grads.abs()).split(widths))
