@@ -641,19 +641,6 @@ __global__ void __launch_bounds__(kLnBlock) layerNormBackwardColumns(const LnArg
   }
 }
 
-// The sum of N slices' values in eight chains, joined in pairs: an eighth of the
-// roundings of one chain.
-template <int N, typename F>
-__device__ __forceinline__ float joinSlices(F value) {
-  static_assert(N % 8 == 0, "eight chains");
-  float c[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) c[k] = value(k);
-#pragma unroll
-  for (int k = 8; k < N; ++k) c[k % 8] += value(k);
-  return ((c[0] + c[1]) + (c[2] + c[3])) + ((c[4] + c[5]) + (c[6] + c[7]));
-}
-
 // Few rows in one launch: the first workgroups take a row each and write dx,
 // the others take 8 vectors of columns and add all rows up (32 slices of them,
 // joined through LDS).  x and dy are read twice for dx (its sums first) and once

@@ -107,4 +107,17 @@ __device__ __forceinline__ float laneSum(float v) {
 
 __device__ __forceinline__ float waveSum(float v) { return laneSum<64>(v); }
 
+// The sum of N slices' values in eight chains, joined in pairs: an eighth of the
+// roundings of one chain.
+template <int N, typename F>
+__device__ __forceinline__ float joinSlices(F value) {
+  static_assert(N % 8 == 0, "eight chains");
+  float c[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) c[k] = value(k);
+#pragma unroll
+  for (int k = 8; k < N; ++k) c[k % 8] += value(k);
+  return ((c[0] + c[1]) + (c[2] + c[3])) + ((c[4] + c[5]) + (c[6] + c[7]));
+}
+
 }  // namespace ar
