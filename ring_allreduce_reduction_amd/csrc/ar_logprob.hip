@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kLpBlock = 256;
 constexpr int kLpVecs = 4;       // of a thread in flight
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 struct LpArgs {
   const void* x[kOpRanks];
@@ -27,7 +27,6 @@ struct LpArgs {
   int64_t xStride[kOpRanks], dxStride[kOpRanks];
   int64_t colStart[kOpRanks + 1];   // shard r holds columns [colStart[r], colStart[r + 1]) of the vocabulary
   int pieceStart[kOpRanks + 1];     // and pieces [pieceStart[r], pieceStart[r + 1]) of the launch
-  int pieceCols;
   int64_t vocabulary;               // the columns of every launch's shards
   const int64_t* targets;
   const float* dlogp;
@@ -63,42 +62,87 @@ __device__ __forceinline__ Running join(const Running& a, const Running& b, floa
   return r;
 }
 
+// N more logits.  The exponents are scaleLog2e x less the largest's, `ref`, in
+// one rounding each; what ref itself was rounded by is taken off the sum.
+// Where ref would overflow (rows of nothing but the lowest value) differences
+// come first.
 template <int N>
 __device__ __forceinline__ void meet(Running* run, const float (&f)[N], float c) {
   float top = run->top;
 #pragma unroll
   for (int e = 0; e < N; ++e) top = fmaxf(top, f[e]);
-  const float base = baseOf(top);
-  float s[4] = {run->sum * expOf(run->top, base, c), 0.0f, 0.0f, 0.0f};
+  const float base = baseOf(top), ref = base * c;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (fabsf(ref) < 0x1p125f) {
 #pragma unroll
-  for (int e = 0; e < N; ++e) s[e % 4] += expOf(f[e], base, c);
+    for (int e = 0; e < N; ++e) s[e % 4] += __builtin_amdgcn_exp2f(fmaf(f[e], c, -ref));
+    const float off = fmaf(base, c, -ref) * -kLn2;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s[k] = fmaf(s[k], off, s[k]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[e % 4] += expOf(f[e], base, c);
+  }
+  run->sum = fmaf(run->sum, expOf(run->top, base, c), (s[0] + s[1]) + (s[2] + s[3]));
   run->top = top;
-  run->sum = (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// A workgroup's share [from, to) of a shard's row.
-template <int DT, int BLOCK>
-__device__ __forceinline__ void meetColumns(Running* run, const typename Elem<DT>::type* x, int64_t from, int64_t to,
-                                            float c) {
+// Loads past the caches or through them.
+template <typename T, int V, bool STREAM>
+__device__ __forceinline__ typename VecOf<T, V>::type loadAs(const T* p) {
+  return STREAM ? loadStream<T, V>(p) : loadVec<T, V>(p);
+}
+
+// A row's part [from, to) as a workgroup takes it: [first, last) by vectors that
+// start at 16 bytes of `p`, the row, and the few elements around them one a
+// thread.
+struct Part {
+  int64_t from, first, last, to;
+};
+
+template <typename T, int V>
+__device__ __forceinline__ Part partOf(const T* p, int64_t from, int64_t to) {
+  const int64_t first = from + (int64_t)((0 - (uintptr_t)(p + from)) % 16 / sizeof(T));
+  if (first >= to) return Part{from, to, to, to};
+  return Part{from, first, first + (to - first) / V * V, to};
+}
+
+// Calls f(column) for a thread's vectors, STEP columns apart, then g(column)
+// for its one of the rest.  `thread` counts from 0 among those that share p.
+template <int V, int STEP, typename F, typename G>
+__device__ __forceinline__ void forPart(const Part& p, int thread, F f, G g) {
+  for (int64_t c = p.first + thread * V; c < p.last; c += STEP) f(c);
+  const int64_t head = p.first - p.from, rest = head + (p.to - p.last);   // at most 2 (V - 1)
+  if (thread < rest) g(thread < head ? p.from + thread : p.last + (thread - head));
+}
+
+// THREADS threads' part of a shard's row: four vectors a thread in flight, -inf
+// past the last one.
+template <int DT, int THREADS, bool STREAM>
+__device__ __forceinline__ void meetColumns(Running* run, int thread, const typename Elem<DT>::type* x, int64_t from,
+                                            int64_t to, float c) {
   typedef typename Elem<DT>::type T;
   constexpr int V = kVec<DT>;
-  const int64_t whole = from + (to - from) / V * V;
-  for (int64_t i = from + threadIdx.x * V; i < whole; i += (int64_t)BLOCK * V * kLpVecs) {
-    typename VecOf<T, V>::type v[kLpVecs];
+  typedef typename VecOf<T, V>::type Vec;
+  const Part part = partOf<T, V>(x, from, to);
+  forPart<V, THREADS * V * kLpVecs>(
+      part, thread,
+      [&](int64_t i) {
+        Vec v[kLpVecs];
 #pragma unroll
-    for (int u = 0; u < kLpVecs; ++u) {
-      v[u] = (typename VecOf<T, V>::type)(T)-INFINITY;
-      if (i + u * BLOCK * V < whole) v[u] = loadVec<T, V>(x + i + u * BLOCK * V);
-    }
-    float f[V * kLpVecs];
+        for (int k = 0; k < kLpVecs; ++k) {
+          v[k] = (Vec)(T)-INFINITY;
+          if (i + k * THREADS * V < part.last) v[k] = loadAs<T, V, STREAM>(x + i + k * THREADS * V);
+        }
+        float f[V * kLpVecs];
 #pragma unroll
-    for (int e = 0; e < V * kLpVecs; ++e) f[e] = (float)v[e / V][e % V];
-    meet(run, f, c);
-  }
-  if (whole + threadIdx.x < to) {
-    const float f[1] = {(float)x[whole + threadIdx.x]};
-    meet(run, f, c);
-  }
+        for (int e = 0; e < V * kLpVecs; ++e) f[e] = (float)v[e / V][e % V];
+        meet(run, f, c);
+      },
+      [&](int64_t i) {
+        const float f[1] = {(float)x[i]};
+        meet(run, f, c);
+      });
 }
 
 // Over a workgroup; thread 0 receives it.
@@ -127,69 +171,106 @@ __device__ __forceinline__ float targetLogit(const LpArgs& a, int64_t row, int64
   return NAN;
 }
 
-__device__ __forceinline__ void putRow(const LpArgs& a, int64_t row, const Running& run, float logit) {
+template <typename A>
+__device__ __forceinline__ void putRow(const A& a, int64_t row, const Running& run, float logit) {
   const float logSum = logf(run.sum);
   a.logp[row] = (logit - run.top) * a.scale - logSum;
   if (a.top) a.top[row] = run.top;
   if (a.logSum) a.logSum[row] = logSum;
 }
 
-__device__ __forceinline__ void putIgnored(const LpArgs& a, int64_t row) {
+template <typename A>
+__device__ __forceinline__ void putIgnored(const A& a, int64_t row) {
   a.logp[row] = 0.0f;
   if (a.top) a.top[row] = 0.0f;
   if (a.logSum) a.logSum[row] = 0.0f;
 }
 
-// A workgroup a row.
-template <int DT, int BLOCK>
+// How the threads of tokenLogprobRows share rows out.
+enum {
+  kAllTogether,   // a workgroup a row, all its threads on a shard at a time
+  kShardEach,     // a workgroup a row, a wavefront a shard at a time
+  kRowEach        // a wavefront a row
+};
+
+template <int DT, int BLOCK, int SHARE, bool STREAM>
 __global__ void __launch_bounds__(BLOCK) tokenLogprobRows(const LpArgs a) {
-  __shared__ Running lds[BLOCK / kWave];
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  typedef typename Elem<DT>::type T;
+  constexpr int WAVES = BLOCK / kWave, ROWS = SHARE == kRowEach ? WAVES : 1;
+  constexpr int THREADS = SHARE == kAllTogether ? BLOCK : kWave;
+  __shared__ Running lds[WAVES];
+  const int wave = (int)threadIdx.x / kWave, lane = (int)threadIdx.x % kWave;
+  const int thread = SHARE == kAllTogether ? (int)threadIdx.x : lane;
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + (ROWS > 1 ? wave : 0); row < a.rows; row += (int64_t)gridDim.x * ROWS) {
+    const bool first = ROWS > 1 ? lane == 0 : threadIdx.x == 0;
     const int64_t t = a.targets[row];
     if (t < 0) {
-      if (threadIdx.x == 0) putIgnored(a, row);
+      if (first) putIgnored(a, row);
       continue;
     }
     float logit = 0.0f;
-    if (threadIdx.x == 0) logit = targetLogit<DT>(a, row, t);
+    if (first) logit = targetLogit<DT>(a, row, t);
     Running run = nothing();
-    for (int r = 0; r < a.nranks; ++r)
-      meetColumns<DT, BLOCK>(&run, (const typename Elem<DT>::type*)a.x[r] + row * a.xStride[r], 0,
-                             a.colStart[r + 1] - a.colStart[r], a.scaleLog2e);
-    run = joinBlock<BLOCK>(run, a.scaleLog2e, lds);
-    if (threadIdx.x == 0) putRow(a, row, run, logit);
+    for (int r = SHARE == kShardEach ? wave : 0; r < a.nranks; r += SHARE == kShardEach ? WAVES : 1)
+      meetColumns<DT, THREADS, STREAM>(&run, thread, (const T*)a.x[r] + row * a.xStride[r], 0,
+                                       a.colStart[r + 1] - a.colStart[r], a.scaleLog2e);
+    run = joinBlock<(ROWS > 1 ? kWave : BLOCK)>(run, a.scaleLog2e, lds);
+    if (first) putRow(a, row, run, logit);
   }
+}
+
+// A workgroup's piece of its shard: shard r's columns cut into as many equal
+// parts (but for 16 columns) as it has pieces.
+struct PieceAt {
+  int rank;
+  int64_t from, to;
+};
+
+__device__ __forceinline__ PieceAt pieceAt(const LpArgs& a) {
+  PieceAt p;
+  p.rank = 0;
+  while ((int)blockIdx.x >= a.pieceStart[p.rank + 1]) ++p.rank;
+  const unsigned pieces = a.pieceStart[p.rank + 1] - a.pieceStart[p.rank], piece = blockIdx.x - a.pieceStart[p.rank];
+  const unsigned cols = (unsigned)(a.colStart[p.rank + 1] - a.colStart[p.rank]);
+  const unsigned each = ((cols + pieces - 1) / pieces + 15) / 16 * 16;
+  p.from = (int64_t)each * piece < cols ? (int64_t)each * piece : cols;
+  p.to = p.from + each < cols ? p.from + each : cols;
+  return p;
 }
 
 // Few rows, or more shards than a launch holds: a workgroup a piece of a row
 // leaves the piece's running values; tokenLogprobJoin joins them.
 template <int DT>
 __global__ void __launch_bounds__(kLpBlock) tokenLogprobPieces(const LpArgs a) {
+  typedef typename Elem<DT>::type T;
   __shared__ Running lds[kLpBlock / kWave];
-  const int piece = blockIdx.x;
-  int r = 0;
-  while (piece >= a.pieceStart[r + 1]) ++r;
-  const int64_t from = (int64_t)(piece - a.pieceStart[r]) * a.pieceCols, cols = a.colStart[r + 1] - a.colStart[r];
-  const int64_t to = from + a.pieceCols < cols ? from + a.pieceCols : cols;
+  const PieceAt p = pieceAt(a);
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     const int64_t t = a.targets[row];
     if (t < 0) continue;
+    const T* x = (const T*)a.x[p.rank] + row * a.xStride[p.rank];
+    // the piece that holds the target leaves its logit
+    const int64_t at = t - a.colStart[p.rank];
+    if (threadIdx.x == 0 && at >= p.from && at < p.to) a.logp[row] = (float)x[at];
     Running run = nothing();
-    meetColumns<DT, kLpBlock>(&run, (const typename Elem<DT>::type*)a.x[r] + row * a.xStride[r], from, to,
-                              a.scaleLog2e);
+    meetColumns<DT, kLpBlock, false>(&run, (int)threadIdx.x, x, p.from, p.to, a.scaleLog2e);
     run = joinBlock<kLpBlock>(run, a.scaleLog2e, lds);
-    if (threadIdx.x == 0) {
-      a.partial[row * a.pieces + piece] = make_float2(run.top, run.sum);
-      // the piece that holds the target leaves its logit
-      const int64_t at = t - a.colStart[r];
-      if (at >= from && at < to)
-        a.logp[row] = (float)((const typename Elem<DT>::type*)a.x[r])[row * a.xStride[r] + at];
-    }
+    if (threadIdx.x == 0) a.partial[row * a.pieces + blockIdx.x] = make_float2(run.top, run.sum);
   }
 }
 
+// What tokenLogprobJoin needs of a call.
+struct LpJoinArgs {
+  const int64_t* targets;
+  float *logp, *top, *logSum;
+  const float2* partial;
+  int64_t vocabulary;
+  int pieces, rows;
+  float scale, scaleLog2e;
+};
+
 // A wavefront a row.
-__global__ void __launch_bounds__(kWave) tokenLogprobJoin(const LpArgs a) {
+__global__ void __launch_bounds__(kWave) tokenLogprobJoin(const LpJoinArgs a) {
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const int64_t t = a.targets[row];
     if (t < 0) {
@@ -206,72 +287,82 @@ __global__ void __launch_bounds__(kWave) tokenLogprobJoin(const LpArgs a) {
   }
 }
 
-template <int DT>
+template <int DT, bool STREAM>
 __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpArgs a) {
   typedef typename Elem<DT>::type T;
   constexpr int V = kVec<DT>;
   typedef typename VecOf<T, V>::type Vec;
-  const int piece = blockIdx.x;
-  int r = 0;
-  while (piece >= a.pieceStart[r + 1]) ++r;
-  const int64_t from = (int64_t)(piece - a.pieceStart[r]) * a.pieceCols, cols = a.colStart[r + 1] - a.colStart[r];
-  const int64_t to = from + a.pieceCols < cols ? from + a.pieceCols : cols;
-  const int64_t whole = from + (to - from) / V * V;
+  const PieceAt p = pieceAt(a);
+  const auto store = [](T* to, const Vec& v) {
+    if (STREAM) storeStream<T, V>(to, v);
+    else storeVec<T, V>(to, v);
+  };
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    const T* x = (const T*)a.x[r] + row * a.xStride[r];
-    T* dx = (T*)a.dx[r] + row * a.dxStride[r];
-    const int64_t t = a.targets[row];
-    float g = t < 0 ? 0.0f : a.dlogp[row] * a.scale;
-    if (g == 0.0f) {
-      for (int64_t i = from + threadIdx.x * V; i < whole; i += kLpBlock * V) storeVec<T, V>(dx + i, (Vec)(T)0.0f);
-      if (whole + threadIdx.x < to) dx[whole + threadIdx.x] = (T)0.0f;
-      continue;
-    }
-    if (t >= a.vocabulary) g = NAN;
-    const float base = baseOf(a.top[row]), logSum = a.logSum[row] * kLog2e;
-    const int64_t at = t - a.colStart[r];
-    for (int64_t i = from + threadIdx.x * V; i < whole; i += kLpBlock * V) {
-      const Vec v = loadVec<T, V>(x + i);
-      Vec out;
+    const int64_t t = a.targets[row], at = t - a.colStart[p.rank];
+    const float d = a.dlogp[row] * a.scale, base = baseOf(a.top[row]), logSum = a.logSum[row] * kLog2e;
+    const float g = t < 0 ? 0.0f : t < a.vocabulary || d == 0.0f ? d : NAN;
+    const T* x = (const T*)a.x[p.rank] + row * a.xStride[p.rank];
+    T* dx = (T*)a.dx[p.rank] + row * a.dxStride[p.rank];
+    const Part part = partOf<T, V>(dx, p.from, p.to);
+    const auto element = [&](float v, int64_t c) {
+      const float q = __builtin_amdgcn_exp2f(fmaf(v - base, a.scaleLog2e, -logSum));
+      return (T)(g * ((c == at ? 1.0f : 0.0f) - q));
+    };
+    if (g == 0.0f)
+      forPart<V, kLpBlock * V>(
+          part, (int)threadIdx.x, [&](int64_t c) { store(dx + c, (Vec)(T)0.0f); }, [&](int64_t c) { dx[c] = (T)0.0f; });
+    else
+      forPart<V, kLpBlock * V>(
+          part, (int)threadIdx.x,
+          [&](int64_t c) {
+            const Vec v = loadAs<T, V, STREAM>(x + c);
+            Vec out;
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float p = __builtin_amdgcn_exp2f(fmaf((float)v[e] - base, a.scaleLog2e, -logSum));
-        out[e] = (T)(g * ((i + e == at ? 1.0f : 0.0f) - p));
-      }
-      storeVec<T, V>(dx + i, out);
-    }
-    if (whole + threadIdx.x < to) {
-      const int64_t i = whole + threadIdx.x;
-      const float p = __builtin_amdgcn_exp2f(fmaf((float)x[i] - base, a.scaleLog2e, -logSum));
-      dx[i] = (T)(g * ((i == at ? 1.0f : 0.0f) - p));
-    }
+            for (int e = 0; e < V; ++e) out[e] = element((float)v[e], c + e);
+            store(dx + c, out);
+          },
+          [&](int64_t c) { dx[c] = element((float)x[c], c); });
   }
 }
 
-constexpr int kLpPiece = 8192;         // columns of a piece, at least
-constexpr int kLpRowsMost = 16 * kOpsCUs;
-
-// The columns of a piece: a pure function of the shards, so that the workspace
-// is known from them.
+// How a call is cut, a pure function of its shapes: a workgroup or a wavefront
+// a row, or pieces of rows.
 struct LpCut {
-  bool whole;        // a workgroup a row
-  int pieceCols;
+  bool whole;
+  int pieceCols;     // columns of a piece, at most
   int64_t pieces;    // of all shards
 };
 
+// Pieces need a second launch, so they are for few rows: 300 rows x 8 x 16000
+// bf16 20.6 us in pieces, 19.3 a workgroup a row; 700 x 5 x 10007 fp32 23.2 and
+// 19.8; one row 6.  A piece is 8192 columns, or down to 2048
+// where they are few (backward 96 rows x 4 x 8003 fp32 6.2 us, 6.8 without;
+// more than two a CU gained nothing).
 LpCut lpCut(const size_t* cols, int nranks, size_t rows) {
   LpCut k;
-  k.whole = nranks <= kOpRanks && rows >= 4 * (size_t)kOpsCUs;
-  k.pieceCols = kLpPiece;
-  // a workgroup's grid of pieces stays small against a long vocabulary's
-  while (true) {
+  k.whole = nranks <= kOpRanks && rows >= (size_t)kOpsCUs;
+  k.pieceCols = 8192;
+  const auto count = [&] {
     k.pieces = 0;
     for (int r = 0; r < nranks; ++r) k.pieces += (int64_t)((cols[r] + k.pieceCols - 1) / k.pieceCols);
-    if (k.pieces <= 4096) break;
+  };
+  count();
+  while (k.pieceCols > 2048 && (int64_t)rows * k.pieces < 2 * kOpsCUs) {
+    k.pieceCols /= 2;
+    count();
+  }
+  while (k.pieces > 4096) {   // the workspace stays small beside a long vocabulary
     k.pieceCols *= 2;
+    count();
   }
   return k;
 }
+
+// Calls whose logits are more than the caches hold load (and backward store)
+// past them: 8192 rows x 8 x 16000 bf16 305 us, 345 through them; backward 673
+// and 725.  Below that the backward pass, which reads the logits again, is better
+// off: 512 rows (262 MB moved) 50 and 41.
+constexpr size_t kLpStream = (size_t)256 << 20;
 
 // Shards: their count, widths and strides.
 bool shardsOk(const size_t* cols, const size_t* strides, int nranks, size_t rows, int64_t* vocabulary) {
@@ -296,7 +387,6 @@ arResult_t lpWorkspace(size_t rows, const size_t* cols, int nranks, size_t* byte
 void fillShards(LpArgs* a, const void* const* x, const size_t* cols, const size_t* strides, int nranks, int first,
                 int pieceCols) {
   a->nranks = nranks - first < kOpRanks ? nranks - first : kOpRanks;
-  a->pieceCols = pieceCols;
   int64_t at = 0;
   for (int r = 0; r < first; ++r) at += (int64_t)cols[r];
   a->colStart[0] = at;
@@ -317,9 +407,26 @@ dim3 pieceGrid(const LpArgs& a) {
 
 template <int DT>
 struct LpRows {
-  static hipError_t run(const LpArgs& a, hipStream_t st) {
-    const int grid = a.rows < kLpRowsMost ? a.rows : kLpRowsMost;
-    return launchKernel(tokenLogprobRows<DT, kLpBlock>, dim3(grid), dim3(kLpBlock), a, st);
+  template <int BLOCK, int SHARE>
+  static hipError_t launch(const LpArgs& a, bool stream, hipStream_t st) {
+    constexpr int ROWS = SHARE == kRowEach ? BLOCK / kWave : 1;
+    return launchKernel(stream ? tokenLogprobRows<DT, BLOCK, SHARE, true> : tokenLogprobRows<DT, BLOCK, SHARE, false>,
+                        dim3(gridOf((a.rows + ROWS - 1) / ROWS, BLOCK)), dim3(BLOCK), a, st);
+  }
+  static hipError_t run(const LpArgs& a, bool stream, hipStream_t st) {
+    constexpr int V = kVec<DT>;
+    // From four shards on a wavefront takes a shard at a time: shards rarely
+    // fill the vectors that a whole workgroup has in flight (8192 rows x 8 x 5000
+    // bf16 115 us, 139 with 256 threads together, 191 with 512; 8000 158, 162,
+    // 205; 16000 317, 315, 308).  Fewer shards: rows of a few vectors go to a
+    // wavefront each (20000 x 2000 19 us, 43 with a workgroup; 4096 x 8000 15.3,
+    // 15.5), others to workgroups as wide as their vectors fill (4096 x 50257 70
+    // us with 512, 75 with 256).
+    if (a.nranks > 4) return launch<512, kShardEach>(a, stream, st);
+    if (a.nranks == 4) return launch<kLpBlock, kShardEach>(a, stream, st);
+    if (a.vocabulary <= 16 * kWave * V) return launch<kLpBlock, kRowEach>(a, stream, st);
+    if (a.vocabulary / a.nranks < 3 * 512 * V) return launch<kLpBlock, kAllTogether>(a, stream, st);
+    return launch<512, kAllTogether>(a, stream, st);
   }
 };
 
@@ -332,8 +439,9 @@ struct LpPieces {
 
 template <int DT>
 struct LpBackward {
-  static hipError_t run(const LpArgs& a, hipStream_t st) {
-    return launchKernel(tokenLogprobBackward<DT>, pieceGrid(a), dim3(kLpBlock), a, st);
+  static hipError_t run(const LpArgs& a, bool stream, hipStream_t st) {
+    return launchKernel(stream ? tokenLogprobBackward<DT, true> : tokenLogprobBackward<DT, false>,
+                        pieceGrid(a), dim3(kLpBlock), a, st);
   }
 };
 
@@ -377,8 +485,9 @@ arResult_t lpForward(const void* const* logits, const size_t* cols, const size_t
   a.vocabulary = vocabulary;
   a.pieces = (int)k.pieces;
   if (k.whole) {
+    const size_t bytes = rows * (size_t)vocabulary * (size_t)elemSize(dtype);
     fillShards(&a, logits, cols, strides, nranks, 0, k.pieceCols);
-    return byType<LpRows, const LpArgs&, hipStream_t>(dtype, a, st) == hipSuccess ? arSuccess : arHipError;
+    return byType<LpRows, const LpArgs&, bool, hipStream_t>(dtype, a, bytes > kLpStream, st) == hipSuccess ? arSuccess : arHipError;
   }
   int piece = 0;
   for (int first = 0; first < nranks; first += kOpRanks) {
@@ -388,9 +497,9 @@ arResult_t lpForward(const void* const* logits, const size_t* cols, const size_t
     if (a.pieceStart[a.nranks] > 0 && byType<LpPieces, const LpArgs&, hipStream_t>(dtype, a, st) != hipSuccess)
       return arHipError;
   }
-  a.partial = (float2*)workspace;
-  const int grid = a.rows < kLpRowsMost ? a.rows : kLpRowsMost;
-  return launchKernel(tokenLogprobJoin, dim3(grid), dim3(kWave), a, st) == hipSuccess ? arSuccess : arHipError;
+  const LpJoinArgs j = {targets, logp, top, logSum, (const float2*)workspace, vocabulary, a.pieces, a.rows, scale,
+                        a.scaleLog2e};
+  return launchKernel(tokenLogprobJoin, dim3(gridOf(a.rows, kWave)), dim3(kWave), j, st) == hipSuccess ? arSuccess : arHipError;
 }
 
 arResult_t lpBackward(const float* dlogp, const void* const* logits, const size_t* cols, const size_t* strides,
@@ -423,13 +532,14 @@ arResult_t lpBackward(const float* dlogp, const void* const* logits, const size_
   a.scaleLog2e = (float)((double)scale * 1.44269504088896340736);
   a.vocabulary = vocabulary;
   const LpCut k = lpCut(cols, nranks, rows);
+  const size_t bytes = 2 * rows * (size_t)vocabulary * (size_t)esz;
   for (int first = 0; first < nranks; first += kOpRanks) {
     fillShards(&a, logits, cols, strides, nranks, first, k.pieceCols);
     for (int r = 0; r < a.nranks; ++r) {
       a.dx[r] = cols[first + r] > 0 ? dlogits[first + r] : nullptr;
       a.dxStride[r] = (int64_t)(dstrides ? dstrides[first + r] : cols[first + r]);
     }
-    if (a.pieceStart[a.nranks] > 0 && byType<LpBackward, const LpArgs&, hipStream_t>(dtype, a, st) != hipSuccess)
+    if (a.pieceStart[a.nranks] > 0 && byType<LpBackward, const LpArgs&, bool, hipStream_t>(dtype, a, bytes > kLpStream, st) != hipSuccess)
       return arHipError;
   }
   return arSuccess;
