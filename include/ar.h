@@ -715,7 +715,8 @@ arResult_t arDropoutAdd(const void* const* x, const void* const* bias, const voi
  * arDropoutAddBackward -- the gradients of arDropoutAdd, from the same draw
  * (that of the residual is dy itself):
  *   dx = k * s * dy,   dbias = sum of dx (unrounded) over all ranks' rows,
- * the latter written to every rank, as an AllReduce would.
+ * the latter written to every rank, as an AllReduce would.  Ranks that hold the
+ * same rows each count: give one of them where their sum is wanted once.
  *  dy, dx      (host arrays) as x and y of arDropoutAdd; dx may be NULL (only
  *              dbias), and dx[r] may be dy[r] with equal strides.
  *  dbias       (host array or NULL) nranks buffers of `cols` elements of

@@ -320,12 +320,15 @@ DropCut dropCut(int cols, int block) {
 // Workgroups that come and go keep a closer window over memory than ones that
 // last: forward 245 us with 256 workgroups a CU in all, 262 with 128, 280 with
 // 32, 267-271 with 512 and more; backward 181 with 32 a CU, 187 with 16, 190
-// with 8, 185 with 64.  Backward a slice has 32 rows at least, so that its
-// partial sums stay small beside them (2537 rows of 2047 11.8 us; 16 rows 11.7,
-// 64 13.2; of 2048 11.0, 11.3, 11.3).
+// with 8, 185 with 64.  Backward a slice costs a row of partial sums to write
+// and read, so it has 32 rows at least (2537 rows of 2047 11.8 us; 16 rows 11.7,
+// 64 13.2; of 2048 11.0, 11.3, 11.3) and there are at most two a CU (160000 rows
+// of 100 21 us, 23 with four, 28 with eight, 44 with 20; of 512 66, 69, 68, 78).
 int dropSlices(int64_t rows, const DropCut& k, bool sums) {
   const int64_t once = (int64_t)1 << k.rowsLog, each = sums && once < 32 ? 32 : once;
-  const int64_t most = (sums ? 32 : 256) * kOpsCUs / k.tiles, full = (rows + each - 1) / each;
+  int64_t most = (sums ? 32 : 256) * kOpsCUs / k.tiles;
+  const int64_t full = (rows + each - 1) / each;
+  if (sums && most > 2 * kOpsCUs) most = 2 * kOpsCUs;
   return (int)(full < most ? full : most < 1 ? 1 : most);
 }
 

@@ -25,11 +25,17 @@ namespace {
 
 constexpr int kPolBlock = 256;
 constexpr int kPolSums = 4;            // weights, weighted loss, kl, clipped tokens
-constexpr int kPolGrid = 4 * kOpsCUs;  // workgroups, and partial sums, of a launch's first pass at most
+// Workgroups, and partial sums, of a launch's first pass at most: 8 x 262144
+// tokens 18.2 us with 2 a CU, 18.3 with 4, 21.9 with 8, whose sums cost as much
+// as their tokens; 8 x 100000 10.8, 11.2, 12.0.  Two vectors a thread in flight
+// 19.6; the second pass, which takes as many, gained nothing from 4 or 8.
+constexpr int kPolGrid = 2 * kOpsCUs;
 constexpr int kPolVec = 4;             // tokens of a thread at a time
 constexpr int kPolFewBlock = 1024;
-constexpr int kPolFewEach = 4;
-constexpr int kPolFew = kPolFewBlock * kPolFewEach;   // tokens of one workgroup's launch
+constexpr int kPolFewEach = 5;
+// Tokens of one workgroup's launch: its wavefronts' parts of 64, less what the
+// ranks leave of their last ones.
+constexpr int kPolFew = kPolFewBlock * kPolFewEach - kOpRanks * kWave;
 
 struct PolArgs {
   const float* logp[kOpRanks];
@@ -54,15 +60,20 @@ struct Token {
   bool clipped;
 };
 
+__device__ __forceinline__ float expFast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
+
 // exp(d) - 1 and exp(d) - 1 - d, below |d| = 1 from the exponential's series
 // through d^12 (what is left out is 2^-31 of the result): there they are
 // differences of nearly equal numbers.
 __device__ __forceinline__ float2 expLess(float d) {
-  float s = 1.0f;
+  constexpr double kOver[13] = {0, 0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320,
+                                1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600};
+  float s = (float)kOver[12];
 #pragma unroll
-  for (int n = 12; n > 2; --n) s = fmaf(d * (1.0f / n), s, 1.0f);
-  const float near = 0.5f * d * d * s, e = expf(d) - 1.0f;
-  return fabsf(d) < 1.0f ? make_float2(near + d, near) : make_float2(e, e - d);
+  for (int n = 11; n >= 2; --n) s = fmaf(s, d, (float)kOver[n]);
+  const float near = d * d * s, e = expFast(d) - 1.0f;
+  const bool small = fabsf(d) < 1.0f;
+  return make_float2(small ? near + d : e, small ? near : e - d);
 }
 
 __device__ __forceinline__ Token tokenOf(const PolArgs& a, float logp, float old, float advantage, bool hasRef,
@@ -70,7 +81,7 @@ __device__ __forceinline__ Token tokenOf(const PolArgs& a, float logp, float old
   Token t;
   const double change = (double)logp - (double)old;
   const bool up = advantage > 0.0f && change > a.logHigh, down = advantage < 0.0f && change < a.logLow;
-  const float ratio = expf((float)change);
+  const float ratio = expFast((float)change);
   t.clipped = up || down;
   t.loss = -advantage * (up ? a.high : down ? a.low : ratio);
   t.dlogp = t.clipped ? 0.0f : -advantage * ratio;
@@ -83,23 +94,32 @@ __device__ __forceinline__ Token tokenOf(const PolArgs& a, float logp, float old
   return t;
 }
 
-__device__ __forceinline__ double waveSum64(double v) {
+// Sums over a workgroup; every thread receives them.
+template <int BLOCK>
+__device__ __forceinline__ double blockSum64(double s, double* lds) {
 #pragma unroll
-  for (int m = 1; m < kWave; m *= 2) v += __shfl_xor(v, m);
-  return v;
+  for (int m = 1; m < kWave; m *= 2) s += __shfl_xor(s, m);
+  if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = s;
+  __syncthreads();
+  s = lds[0];
+  for (int w = 1; w < BLOCK / kWave; ++w) s += lds[w];
+  return s;
 }
 
-// N sums over a workgroup; every thread receives them.
-template <int BLOCK, int N>
-__device__ __forceinline__ void blockSums(double (&s)[N], double (*lds)[N]) {
+// Four sums at once: neighbours hand each other the halves they do not keep, so
+// that after two steps a lane holds one of the four and 7 exchanges do for 24.
+template <int BLOCK>
+__device__ __forceinline__ void blockSums(double (&s)[kPolSums], double (*lds)[kPolSums]) {
+  const bool odd = threadIdx.x & 1, second = threadIdx.x & 2;
+  const double a = (odd ? s[2] : s[0]) + __shfl_xor(odd ? s[0] : s[2], 1);
+  const double b = (odd ? s[3] : s[1]) + __shfl_xor(odd ? s[1] : s[3], 1);
+  double v = (second ? b : a) + __shfl_xor(second ? a : b, 2);
 #pragma unroll
-  for (int k = 0; k < N; ++k) s[k] = waveSum64(s[k]);
-  if (threadIdx.x % kWave == 0)
-#pragma unroll
-    for (int k = 0; k < N; ++k) lds[threadIdx.x / kWave][k] = s[k];
+  for (int m = 4; m < kWave; m *= 2) v += __shfl_xor(v, m);
+  if (threadIdx.x % kWave < kPolSums) lds[threadIdx.x / kWave][(odd ? 2 : 0) + (second ? 1 : 0)] = v;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
+  for (int k = 0; k < kPolSums; ++k) {
     s[k] = lds[0][k];
     for (int w = 1; w < BLOCK / kWave; ++w) s[k] += lds[w][k];
   }
@@ -109,14 +129,14 @@ __device__ __forceinline__ void blockSums(double (&s)[N], double (*lds)[N]) {
 // weight 0 is left out, whatever its other values are.
 __device__ __forceinline__ float addToken(const PolArgs& a, float logp, float old, float advantage, bool hasRef,
                                           float ref, float weight, double (&s)[kPolSums]) {
-  if (weight == 0.0f) return 0.0f;
   const Token t = tokenOf(a, logp, old, advantage, hasRef, ref);
+  const bool counts = weight != 0.0f;
   const double w = weight;
   s[0] += w;
-  s[1] += w * (double)t.loss;
-  s[2] += w * (double)t.kl;
+  s[1] = fma(w, (double)(counts ? t.loss : 0.0f), s[1]);
+  s[2] = fma(w, (double)(counts ? t.kl : 0.0f), s[2]);
   s[3] += t.clipped ? w : 0.0;
-  return weight * t.dlogp;
+  return counts ? weight * t.dlogp : 0.0f;
 }
 
 __device__ __forceinline__ double partOf(const PolArgs& a, double weights) {
@@ -162,9 +182,9 @@ __device__ __forceinline__ PolPlace polPlace(const PolArgs& a) {
 // the rest, which the rank's first workgroup takes.
 template <typename F, typename G>
 __device__ __forceinline__ void forTokens(const PolPlace& p, F f, G g) {
-#pragma unroll 2
-  for (int64_t i = p.first; i < p.whole; i += p.step) f(i);
-  const int64_t i = p.whole + p.first / kPolVec;
+  int64_t i = p.first;
+  for (; i < p.whole; i += p.step) f(i);
+  i = p.whole + p.first / kPolVec;
   if (i < p.count) g(i);
 }
 
@@ -175,10 +195,10 @@ __global__ void __launch_bounds__(kPolBlock) policySums(const PolArgs a) {
   const float *advantage = a.advantage[at.rank], *weight = a.weight[at.rank];
   float* dlogp = a.dlogp[at.rank];
   double s[kPolSums] = {0.0, 0.0, 0.0, 0.0};
+  typedef FloatVec<kPolVec> Vec;
   forTokens(
       at,
       [&](int64_t i) {
-        typedef FloatVec<kPolVec> Vec;
         const Vec l = loadVec<float, kPolVec>(logp + i), o = loadVec<float, kPolVec>(old + i);
         const Vec v = loadVec<float, kPolVec>(advantage + i);
         const Vec f = ref ? loadVec<float, kPolVec>(ref + i) : (Vec)0.0f;
@@ -202,10 +222,18 @@ __global__ void __launch_bounds__(kPolBlock) policySums(const PolArgs a) {
 // The sums of the first pass in one order for every workgroup, and what they
 // are needed for: the stats, and each gradient's factor.
 __global__ void __launch_bounds__(kPolBlock) policyGrad(const PolArgs a) {
-  __shared__ double lds[kPolBlock / kWave][1], ldsAll[kPolBlock / kWave][kPolSums];
-  double weights[1] = {0.0};
-  for (int i = threadIdx.x; i < a.partials; i += kPolBlock) weights[0] += a.partial[i];
-  blockSums<kPolBlock>(weights, lds);
+  __shared__ double lds[kPolBlock / kWave], ldsAll[kPolBlock / kWave][kPolSums];
+  typedef FloatVec<kPolVec> Vec;
+  // a thread's first gradients are on their way while the sums are joined
+  const bool any = a.start[a.nranks] > 0;   // else a launch for the stats alone
+  PolPlace at{};
+  if (any) at = polPlace(a);
+  float* dlogp = any ? a.dlogp[at.rank] : nullptr;
+  Vec ahead = (Vec)0.0f;
+  if (dlogp && at.first < at.whole) ahead = loadVec<float, kPolVec>(dlogp + at.first);
+  double weights = 0.0;
+  for (int i = threadIdx.x; i < a.partials; i += kPolBlock) weights += a.partial[i];
+  weights = blockSum64<kPolBlock>(weights, lds);
   if (a.stats && blockIdx.x == 0) {
     double s[kPolSums] = {0.0, 0.0, 0.0, 0.0};
     for (int i = threadIdx.x; i < a.partials; i += kPolBlock)
@@ -214,15 +242,12 @@ __global__ void __launch_bounds__(kPolBlock) policyGrad(const PolArgs a) {
     blockSums<kPolBlock>(s, ldsAll);
     if (threadIdx.x == 0) putStats(a, s);
   }
-  if (a.start[a.nranks] == 0) return;   // a launch for the stats alone
-  const PolPlace at = polPlace(a);
-  float* dlogp = a.dlogp[at.rank];
   if (dlogp == nullptr) return;
-  const double factor = a.gradScale * partOf(a, weights[0]);
+  const double factor = a.gradScale * partOf(a, weights);
   forTokens(
       at,
       [&](int64_t i) {
-        FloatVec<kPolVec> d = loadVec<float, kPolVec>(dlogp + i);
+        Vec d = i == at.first ? ahead : loadVec<float, kPolVec>(dlogp + i);
 #pragma unroll
         for (int e = 0; e < kPolVec; ++e) d[e] = timesFactor(d[e], factor);
         storeVec<float, kPolVec>(dlogp + i, d);
@@ -231,41 +256,36 @@ __global__ void __launch_bounds__(kPolBlock) policyGrad(const PolArgs a) {
 }
 
 // Few tokens: one workgroup, one launch, the gradients kept in registers until
-// their factor is known.
+// their factor is known.  A wavefront takes 64 tokens of a rank at a time.
 __global__ void __launch_bounds__(kPolFewBlock) policyFew(const PolArgs a) {
-  __shared__ double lds[kPolFewBlock / kWave][kPolSums];
-  // the ranks' buffers, to be indexed by a token's place among all of them
-  __shared__ struct { const float *logp, *old, *ref, *advantage, *weight; float* dlogp; } at[kOpRanks];
-  for (int r = 0; r < a.nranks; ++r)
-    if ((int)threadIdx.x == r) at[r] = {a.logp[r], a.old[r], a.ref[r], a.advantage[r], a.weight[r], a.dlogp[r]};
-  __syncthreads();
-  const int count = a.start[a.nranks];
+  constexpr int WAVES = kPolFewBlock / kWave;
+  __shared__ double lds[WAVES][kPolSums];
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave), lane = (int)threadIdx.x % kWave;
   double s[kPolSums] = {0.0, 0.0, 0.0, 0.0};
   float d[kPolFewEach];
-  int rank[kPolFewEach], place[kPolFewEach];
 #pragma unroll
   for (int k = 0; k < kPolFewEach; ++k) {
-    const int token = (int)threadIdx.x + k * kPolFewBlock;
-    rank[k] = 0;
-    place[k] = token;
-    for (int r = 1; r < a.nranks; ++r)
-      if (token >= a.start[r]) {
-        rank[k] = r;
-        place[k] = token - a.start[r];
-      }
-    if (token >= count) continue;
-    const auto& p = at[rank[k]];
-    const int i = place[k];
-    d[k] = addToken(a, p.logp[i], p.old[i], p.advantage[i], p.ref != nullptr, p.ref ? p.ref[i] : 0.0f,
-                    p.weight ? p.weight[i] : 1.0f, s);
+    const int piece = wave + k * WAVES;
+    d[k] = 0.0f;
+    if (piece >= a.blockStart[a.nranks]) continue;
+    int r = 0;
+    while (piece >= a.blockStart[r + 1]) ++r;
+    const int i = (piece - a.blockStart[r]) * kWave + lane;
+    if (i < a.start[r + 1] - a.start[r])
+      d[k] = addToken(a, a.logp[r][i], a.old[r][i], a.advantage[r][i], a.ref[r] != nullptr,
+                      a.ref[r] ? a.ref[r][i] : 0.0f, a.weight[r] ? a.weight[r][i] : 1.0f, s);
   }
   blockSums<kPolFewBlock>(s, lds);
   if (threadIdx.x == 0) putStats(a, s);
   const double factor = a.gradScale * partOf(a, s[0]);
 #pragma unroll
   for (int k = 0; k < kPolFewEach; ++k) {
-    if ((int)threadIdx.x + k * kPolFewBlock < count && at[rank[k]].dlogp)
-      at[rank[k]].dlogp[place[k]] = timesFactor(d[k], factor);
+    const int piece = wave + k * WAVES;
+    if (piece >= a.blockStart[a.nranks]) continue;
+    int r = 0;
+    while (piece >= a.blockStart[r + 1]) ++r;
+    const int i = (piece - a.blockStart[r]) * kWave + lane;
+    if (a.dlogp[r] && i < a.start[r + 1] - a.start[r]) a.dlogp[r][i] = timesFactor(d[k], factor);
   }
 }
 
@@ -293,7 +313,7 @@ arResult_t polWorkspace(const size_t* tokens, int nranks, size_t* bytes) {
 
 void fillTokens(PolArgs* a, const float* const* logp, const float* const* old, const float* const* ref,
                 const float* const* advantage, const float* const* weight, float* const* dlogp, const size_t* tokens,
-                int nranks, int first) {
+                int nranks, int first, bool few) {
   a->nranks = nranks - first < kOpRanks ? nranks - first : kOpRanks;
   a->start[0] = 0;
   for (int r = 0; r < a->nranks; ++r) {
@@ -308,7 +328,9 @@ void fillTokens(PolArgs* a, const float* const* logp, const float* const* old, c
     a->dlogp[r] = any && dlogp ? dlogp[k] : nullptr;
   }
   const int64_t n = a->start[a->nranks];
-  if (n > 0) shareOut(a->start, a->nranks, kPolBlock * kPolVec, polBlocks(n), a->blockStart);
+  if (few)   // a wavefront's parts
+    for (int r = 0; r < a->nranks; ++r) a->blockStart[r + 1] = a->blockStart[r] + ((int)tokens[r] + kWave - 1) / kWave;
+  else if (n > 0) shareOut(a->start, a->nranks, kPolBlock * kPolVec, polBlocks(n), a->blockStart);
   else a->blockStart[a->nranks] = 0;
 }
 
@@ -356,17 +378,17 @@ arResult_t policyLoss(const float* const* logp, const float* const* old, const f
   a.denominator = denominator;
   a.gradScale = gradScale;
   if (few) {
-    fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, 0);
+    fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, 0, true);
     a.stats = stats;
     return launchKernel(policyFew, dim3(1), dim3(kPolFewBlock), a, st) == hipSuccess ? arSuccess : arHipError;
   }
   for (int l = 0; l < s.launches; ++l) {
-    fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, l * kOpRanks);
+    fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, l * kOpRanks, false);
     a.partials += a.blockStart[a.nranks];
   }
   int partials = 0;
   for (int l = 0; l < s.launches; ++l) {
-    fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, l * kOpRanks);
+    fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, l * kOpRanks, false);
     const int grid = a.blockStart[a.nranks];
     if (grid == 0) continue;
     a.partial = (double*)workspace + partials;
@@ -375,7 +397,7 @@ arResult_t policyLoss(const float* const* logp, const float* const* old, const f
   }
   a.partial = (double*)workspace;
   for (int l = 0; l < s.launches; ++l) {
-    fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, l * kOpRanks);
+    fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, l * kOpRanks, false);
     a.stats = l == 0 ? stats : nullptr;
     const int grid = dlogp != nullptr ? a.blockStart[a.nranks] : 0;
     if (grid == 0 && l > 0) continue;

@@ -107,17 +107,18 @@ def policy(logps, olds, refs, advantages, weights, low, high, kl_coef, denominat
     def mean(v):
         return torch.where(zero, 0.0, w * v).sum() * part
 
-    # What 32 bits are off.  The ratio: its logarithm's rounding, the exponential (2 U), the product with A.
+    # What 32 bits are off.  The ratio: its logarithm's rounding, the product with log2(e) and that factor's own (2.5 U of
+    # the logarithm), the exponential (2 U, nothing below 2^-126), the product with A.
     change = (logp - old).abs()
-    d_pg = U * (change + 4) * (adv * ratio).abs()
+    d_pg = U * (2.5 * change + 4) * (adv * ratio).abs() + 2.0 ** -126 * adv.abs()
     d_loss = torch.where(clipped, 2 * U * loss.abs(), d_pg)
     d_kl = torch.zeros_like(loss)
     d_grad = torch.where(clipped, 0.0, d_pg)
     if refs is not None:
         # the difference's rounding moves kl by |d (exp(d) - 1)| U and exp(d) - 1 by |d| exp(d) U; the series' factors
-        # and products 8 U of kl; past 1 the exponential 2 U, the differences' roundings
+        # and products 8 U of kl; past 1 the exponential as the ratio's, the differences' roundings
         e, less, far = torch.exp(d), torch.expm1(d).abs(), d.abs() >= 1
-        d_kl = U * (d.abs() * less + 8 * kl + torch.where(far, 2 * e + less, 0.0))
+        d_kl = U * (d.abs() * less + 8 * kl + torch.where(far, (2 + 1.5 * d.abs()) * e + less + 2.0 ** -100, 0.0))
         d_less = d_kl + U * (d.abs() * e + less + 2 * d.abs())
         d_grad = d_grad + kl_coef * (d_less + 3 * U * less)
     d_grad = (d_grad + 3 * U * g.abs()) * (grad_scale * part * w).abs()

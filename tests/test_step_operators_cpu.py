@@ -129,7 +129,8 @@ def test_workspaces(B):
     for rows in ([0], [1], [100], [1 << 30], [5] * 72):
         for cols in (1, 33, 4096, 1 << 20):
             n = B.arDropoutAddBackwardWorkspace(rows, cols)
-            assert n % 16 == 0 and 4 * cols <= n <= 4 * (cols + 8) * (8 * 256 + 5 * 16)   # slices of all launches
+            # at most 512 partial sums a column, or 16 a launch
+            assert n % 16 == 0 and 4 * cols <= n <= 4 * (cols + 8) * max(512, 5 * 16)
     assert B.arTokenLogprobWorkspace(0, [5]) == 0
     for rows, cols in ((1, [16000] * 8), (1000, [9]), (1 << 20, [7] * 17), (3, [1 << 30] * 128)):
         n = B.arTokenLogprobWorkspace(rows, cols)
