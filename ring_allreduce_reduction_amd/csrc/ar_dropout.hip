@@ -224,7 +224,7 @@ template <int DT, bool SUMS, bool STREAM>
 __global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackward(const DropArgs a) {
   typedef typename Elem<DT>::type T;
   typedef Eight<DT, STREAM> E;
-  __shared__ float lds[SUMS ? kDropBackBlock : 1][kDropCols];
+  __shared__ float lds[SUMS ? kDropBackBlock / kWave : 1][kWave * kDropCols];
   const DropPlace at = placeOf<kDropBackBlock>(a);
   FloatVec<8> sum = (FloatVec<8>)0.0f;
   if (at.n > 0) {
@@ -247,16 +247,21 @@ __global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackward(const DropA
     });
   }
   if constexpr (SUMS) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) lds[threadIdx.x][e] = sum[e];
-    __syncthreads();
+    // the rows of a wavefront, then the wavefronts
     const int across = kDropBackBlock >> a.rowsLog;
+    for (int m = across; m < kWave; m *= 2)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor(sum[e], m);
+    const int wave = (int)threadIdx.x / kWave, lane = (int)threadIdx.x % kWave;
+    if (lane < across)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) lds[wave][lane * kDropCols + e] = sum[e];
+    __syncthreads();
     const int tile = (int)(blockIdx.x % (unsigned)a.tiles), slice = (int)(blockIdx.x / (unsigned)a.tiles);
-    float* partial = a.partial + (size_t)slice * a.partialCols + (size_t)tile * across * kDropCols;
-    for (int c = threadIdx.x; c < across * kDropCols && tile * across * kDropCols + c < a.cols; c += kDropBackBlock) {
-      float s = 0.0f;
-      for (int k = 0; k < 1 << a.rowsLog; ++k) s += lds[k * across + c / kDropCols][c % kDropCols];
-      partial[c] = s;
+    const int64_t first = (int64_t)tile * across * kDropCols, c = first + threadIdx.x;
+    if ((int)threadIdx.x < across * kDropCols && c < a.cols) {
+      const float all = joinSlices<kDropBackBlock / kWave>([&](int w) { return lds[w][threadIdx.x]; });
+      a.partial[(size_t)slice * a.partialCols + c] = all;
     }
   }
 }

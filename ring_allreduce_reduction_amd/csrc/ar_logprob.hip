@@ -145,20 +145,20 @@ __device__ __forceinline__ void meetColumns(Running* run, int thread, const type
       });
 }
 
-// Over a workgroup; thread 0 receives it.
-template <int BLOCK>
-__device__ __forceinline__ Running joinBlock(Running run, float c, Running* lds) {
+// Over THREADS threads of a workgroup side by side; the first one receives it.
+template <int THREADS>
+__device__ __forceinline__ Running joinThreads(Running run, float c, Running* lds) {
 #pragma unroll
-  for (int m = 1; m < kWave; m *= 2) {
+  for (int m = 1; m < kWave && m < THREADS; m *= 2) {
     const Running other = {__shfl_xor(run.top, m), __shfl_xor(run.sum, m)};
     run = join(run, other, c);
   }
-  if (BLOCK == kWave) return run;
+  if (THREADS <= kWave) return run;
   __syncthreads();   // lds may still be read from the row before
   if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = run;
   __syncthreads();
   if (threadIdx.x == 0)
-    for (int w = 1; w < BLOCK / kWave; ++w) run = join(run, lds[w], c);
+    for (int w = 1; w < THREADS / kWave; ++w) run = join(run, lds[w], c);
   return run;
 }
 
@@ -186,23 +186,20 @@ __device__ __forceinline__ void putIgnored(const A& a, int64_t row) {
   if (a.logSum) a.logSum[row] = 0.0f;
 }
 
-// How the threads of tokenLogprobRows share rows out.
-enum {
-  kAllTogether,   // a workgroup a row, all its threads on a shard at a time
-  kShardEach,     // a workgroup a row, a wavefront a shard at a time
-  kRowEach        // a wavefront a row
-};
-
-template <int DT, int BLOCK, int SHARE, bool STREAM>
+// ROW threads take a row, SHARD of them a shard at a time.
+template <int DT, int BLOCK, int ROW, int SHARD, bool STREAM>
 __global__ void __launch_bounds__(BLOCK) tokenLogprobRows(const LpArgs a) {
   typedef typename Elem<DT>::type T;
-  constexpr int WAVES = BLOCK / kWave, ROWS = SHARE == kRowEach ? WAVES : 1;
-  constexpr int THREADS = SHARE == kAllTogether ? BLOCK : kWave;
-  __shared__ Running lds[WAVES];
-  const int wave = (int)threadIdx.x / kWave, lane = (int)threadIdx.x % kWave;
-  const int thread = SHARE == kAllTogether ? (int)threadIdx.x : lane;
-  for (int64_t row = (int64_t)blockIdx.x * ROWS + (ROWS > 1 ? wave : 0); row < a.rows; row += (int64_t)gridDim.x * ROWS) {
-    const bool first = ROWS > 1 ? lane == 0 : threadIdx.x == 0;
+  static_assert(ROW == BLOCK || ROW <= kWave, "rows of a wavefront's parts meet no barrier");
+  constexpr int ROWS = BLOCK / ROW;
+  __shared__ Running lds[BLOCK / kWave];
+  const int thread = (int)threadIdx.x % SHARD;
+  // a wavefront's shards are its own
+  int shard = (int)threadIdx.x % ROW / SHARD;
+  if (SHARD >= kWave) shard = __builtin_amdgcn_readfirstlane(shard);
+  const bool first = threadIdx.x % ROW == 0;
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / ROW : 0); row < a.rows;
+       row += (int64_t)gridDim.x * ROWS) {
     const int64_t t = a.targets[row];
     if (t < 0) {
       if (first) putIgnored(a, row);
@@ -211,10 +208,10 @@ __global__ void __launch_bounds__(BLOCK) tokenLogprobRows(const LpArgs a) {
     float logit = 0.0f;
     if (first) logit = targetLogit<DT>(a, row, t);
     Running run = nothing();
-    for (int r = SHARE == kShardEach ? wave : 0; r < a.nranks; r += SHARE == kShardEach ? WAVES : 1)
-      meetColumns<DT, THREADS, STREAM>(&run, thread, (const T*)a.x[r] + row * a.xStride[r], 0,
-                                       a.colStart[r + 1] - a.colStart[r], a.scaleLog2e);
-    run = joinBlock<(ROWS > 1 ? kWave : BLOCK)>(run, a.scaleLog2e, lds);
+    for (int r = shard; r < a.nranks; r += ROW / SHARD)
+      meetColumns<DT, SHARD, STREAM>(&run, thread, (const T*)a.x[r] + row * a.xStride[r], 0,
+                                     a.colStart[r + 1] - a.colStart[r], a.scaleLog2e);
+    run = joinThreads<ROW>(run, a.scaleLog2e, lds);
     if (first) putRow(a, row, run, logit);
   }
 }
@@ -254,7 +251,7 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobPieces(const LpArgs a) {
     if (threadIdx.x == 0 && at >= p.from && at < p.to) a.logp[row] = (float)x[at];
     Running run = nothing();
     meetColumns<DT, kLpBlock, false>(&run, (int)threadIdx.x, x, p.from, p.to, a.scaleLog2e);
-    run = joinBlock<kLpBlock>(run, a.scaleLog2e, lds);
+    run = joinThreads<kLpBlock>(run, a.scaleLog2e, lds);
     if (threadIdx.x == 0) a.partial[row * a.pieces + blockIdx.x] = make_float2(run.top, run.sum);
   }
 }
@@ -282,22 +279,25 @@ __global__ void __launch_bounds__(kWave) tokenLogprobJoin(const LpJoinArgs a) {
       const float2 p = a.partial[row * a.pieces + i];
       run = join(run, Running{p.x, p.y}, a.scaleLog2e);
     }
-    run = joinBlock<kWave>(run, a.scaleLog2e, nullptr);
+    run = joinThreads<kWave>(run, a.scaleLog2e, nullptr);
     if (threadIdx.x == 0) putRow(a, row, run, t < a.vocabulary ? a.logp[row] : NAN);
   }
 }
 
-template <int DT, bool STREAM>
+// A workgroup takes a piece of kLpBlock / THREADS rows at a time.
+template <int DT, int THREADS, bool STREAM>
 __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpArgs a) {
   typedef typename Elem<DT>::type T;
-  constexpr int V = kVec<DT>;
+  constexpr int V = kVec<DT>, ROWS = kLpBlock / THREADS;
   typedef typename VecOf<T, V>::type Vec;
   const PieceAt p = pieceAt(a);
+  const int thread = (int)threadIdx.x % THREADS;
   const auto store = [](T* to, const Vec& v) {
     if (STREAM) storeStream<T, V>(to, v);
     else storeVec<T, V>(to, v);
   };
-  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+  for (int64_t row = (int64_t)blockIdx.y * ROWS + (ROWS > 1 ? threadIdx.x / THREADS : 0); row < a.rows;
+       row += (int64_t)gridDim.y * ROWS) {
     const int64_t t = a.targets[row], at = t - a.colStart[p.rank];
     const float d = a.dlogp[row] * a.scale, base = baseOf(a.top[row]), logSum = a.logSum[row] * kLog2e;
     const float g = t < 0 ? 0.0f : t < a.vocabulary || d == 0.0f ? d : NAN;
@@ -309,11 +309,11 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpArgs a)
       return (T)(g * ((c == at ? 1.0f : 0.0f) - q));
     };
     if (g == 0.0f)
-      forPart<V, kLpBlock * V>(
-          part, (int)threadIdx.x, [&](int64_t c) { store(dx + c, (Vec)(T)0.0f); }, [&](int64_t c) { dx[c] = (T)0.0f; });
+      forPart<V, THREADS * V>(
+          part, thread, [&](int64_t c) { store(dx + c, (Vec)(T)0.0f); }, [&](int64_t c) { dx[c] = (T)0.0f; });
     else
-      forPart<V, kLpBlock * V>(
-          part, (int)threadIdx.x,
+      forPart<V, THREADS * V>(
+          part, thread,
           [&](int64_t c) {
             const Vec v = loadAs<T, V, STREAM>(x + c);
             Vec out;
@@ -400,21 +400,33 @@ void fillShards(LpArgs* a, const void* const* x, const size_t* cols, const size_
   }
 }
 
-dim3 pieceGrid(const LpArgs& a) {
-  const int rows = a.rows < 65535 ? a.rows : 65535;
+// Workgroups of `each` rows at a time.
+dim3 pieceGrid(const LpArgs& a, int each) {
+  const int64_t groups = ((int64_t)a.rows + each - 1) / each, rows = groups < 65535 ? groups : 65535;
   return dim3((unsigned)a.pieceStart[a.nranks], (unsigned)rows);
 }
 
 template <int DT>
 struct LpRows {
-  template <int BLOCK, int SHARE>
+  template <int BLOCK, int ROW, int SHARD>
   static hipError_t launch(const LpArgs& a, bool stream, hipStream_t st) {
-    constexpr int ROWS = SHARE == kRowEach ? BLOCK / kWave : 1;
-    return launchKernel(stream ? tokenLogprobRows<DT, BLOCK, SHARE, true> : tokenLogprobRows<DT, BLOCK, SHARE, false>,
-                        dim3(gridOf((a.rows + ROWS - 1) / ROWS, BLOCK)), dim3(BLOCK), a, st);
+    constexpr int ROWS = BLOCK / ROW;
+    return launchKernel(stream ? tokenLogprobRows<DT, BLOCK, ROW, SHARD, true>
+                               : tokenLogprobRows<DT, BLOCK, ROW, SHARD, false>,
+                        dim3(gridOf(((int64_t)a.rows + ROWS - 1) / ROWS, BLOCK)), dim3(BLOCK), a, st);
   }
   static hipError_t run(const LpArgs& a, bool stream, hipStream_t st) {
     constexpr int V = kVec<DT>;
+    const int64_t columns = a.vocabulary / a.nranks;   // of a shard
+    // Narrow shards: 16 threads take one, alone on a row or four of them (8192
+    // rows x 8 x 250 bf16 16 us, 37 with a wavefront a shard, 62 with a workgroup;
+    // x 1000 26, 35; x 2000 48, 45; 1 x 256 4.7, 8.3 with a wavefront a row; 1 x
+    // 2000 8.6, 10.3, but 300 rows of it 6.3 and 4.6).
+    if (columns <= 128 * V) {
+      if (a.nranks < 4) return launch<kLpBlock, 16, 16>(a, stream, st);
+      // 300 rows x 8 x 1000 7.2 us, 5.9 with a wavefront a shard
+      if (columns <= 32 * V || a.rows >= 4 * kOpsCUs) return launch<kLpBlock, kWave, 16>(a, stream, st);
+    }
     // From four shards on a wavefront takes a shard at a time: shards rarely
     // fill the vectors that a whole workgroup has in flight (8192 rows x 8 x 5000
     // bf16 115 us, 139 with 256 threads together, 191 with 512; 8000 158, 162,
@@ -422,26 +434,41 @@ struct LpRows {
     // wavefront each (20000 x 2000 19 us, 43 with a workgroup; 4096 x 8000 15.3,
     // 15.5), others to workgroups as wide as their vectors fill (4096 x 50257 70
     // us with 512, 75 with 256).
-    if (a.nranks > 4) return launch<512, kShardEach>(a, stream, st);
-    if (a.nranks == 4) return launch<kLpBlock, kShardEach>(a, stream, st);
-    if (a.vocabulary <= 16 * kWave * V) return launch<kLpBlock, kRowEach>(a, stream, st);
-    if (a.vocabulary / a.nranks < 3 * 512 * V) return launch<kLpBlock, kAllTogether>(a, stream, st);
-    return launch<512, kAllTogether>(a, stream, st);
+    if (a.nranks > 4) return launch<512, 512, kWave>(a, stream, st);
+    if (a.nranks == 4) return launch<kLpBlock, kLpBlock, kWave>(a, stream, st);
+    if (a.vocabulary <= 16 * kWave * V) return launch<kLpBlock, kWave, kWave>(a, stream, st);
+    if (columns < 3 * 512 * V) return launch<kLpBlock, kLpBlock, kLpBlock>(a, stream, st);
+    return launch<512, 512, 512>(a, stream, st);
   }
 };
 
 template <int DT>
 struct LpPieces {
   static hipError_t run(const LpArgs& a, hipStream_t st) {
-    return launchKernel(tokenLogprobPieces<DT>, pieceGrid(a), dim3(kLpBlock), a, st);
+    return launchKernel(tokenLogprobPieces<DT>, pieceGrid(a, 1), dim3(kLpBlock), a, st);
   }
 };
 
 template <int DT>
 struct LpBackward {
+  template <int THREADS>
+  static hipError_t launch(const LpArgs& a, bool stream, hipStream_t st) {
+    return launchKernel(stream ? tokenLogprobBackward<DT, THREADS, true> : tokenLogprobBackward<DT, THREADS, false>,
+                        pieceGrid(a, kLpBlock / THREADS), dim3(kLpBlock), a, st);
+  }
   static hipError_t run(const LpArgs& a, bool stream, hipStream_t st) {
-    return launchKernel(stream ? tokenLogprobBackward<DT, true> : tokenLogprobBackward<DT, false>,
-                        pieceGrid(a), dim3(kLpBlock), a, st);
+    constexpr int V = kVec<DT>;
+    int64_t widest = 0;   // of the launch's shards
+    for (int r = 0; r < a.nranks; ++r) {
+      const int64_t c = a.colStart[r + 1] - a.colStart[r];
+      widest = c > widest ? c : widest;
+    }
+    // 8192 rows x 8 x 250 bf16: 15 us with 16 threads a row, 29 with 64, 92 with
+    // 256; x 500 23, 30, 92; x 1000 43, 38, 93; x 2000 154, 100, 125; x 4000 243,
+    // 188, 183.
+    if (widest <= 64 * V) return launch<16>(a, stream, st);
+    if (widest <= 256 * V) return launch<64>(a, stream, st);
+    return launch<kLpBlock>(a, stream, st);
   }
 };
 
