@@ -151,14 +151,14 @@ __device__ __forceinline__ DropPlace placeOf(const DropArgs& a) {
   return p;
 }
 
-// Calls f(row, load, settle, store) for a thread's rows.  The 8 elements, or
-// the fewer before a row's end, come with one load: at the end it moves back to
-// end with the row, so that all threads' loads go out alike, and `settle`
-// brings the elements to their places once they are there.  2537 rows of 2047
-// fp16 backward 15.5 us with the last elements loaded one by one, 12.2 so.
-// Rows of less than 8 elements are loaded one by one.
+// Calls f(load, settle, store), how a thread's elements of a row come and go.
+// The 8 elements, or the fewer before a row's end, come with one load: at the
+// end it moves back to end with the row, so that all threads' loads go out
+// alike, and `settle` brings the elements to their places once they are there.
+// 2537 rows of 2047 fp16 backward 15.5 us with the last elements loaded one by
+// one, 12.2 so.  Rows of less than 8 elements are loaded one by one.
 template <typename E, typename F>
-__device__ __forceinline__ void forRows(const DropPlace& at, int cols, F f) {
+__device__ __forceinline__ void withAccess(const DropPlace& at, int cols, F f) {
   typedef typename E::T T;
   const bool tail = at.n < kDropCols;
   const auto store = [&](T* row, const E& v) {
@@ -166,17 +166,15 @@ __device__ __forceinline__ void forRows(const DropPlace& at, int cols, F f) {
     else v.store(row);
   };
   if (cols < kDropCols) {
-    for (int64_t i = at.row; i < at.rows; i += at.step)
-      f(i, [&](E* v, const T* row) { v->loadFew(row, at.n); }, [](E*) {}, store);
+    f([&](E* v, const T* row) { v->loadFew(row, at.n); }, [](E*) {}, store);
     return;
   }
   const int back = tail ? kDropCols - at.n : 0;
-  for (int64_t i = at.row; i < at.rows; i += at.step)
-    f(i, [&](E* v, const T* row) { v->load(row - back); },
-      [&](E* v) {
-        if (tail) v->moveDown(back);
-      },
-      store);
+  f([&](E* v, const T* row) { v->load(row - back); },
+    [&](E* v) {
+      if (tail) v->moveDown(back);
+    },
+    store);
 }
 
 template <int DT, int WT, bool STREAM, bool RESIDUAL>
@@ -196,19 +194,21 @@ __device__ __forceinline__ void forwardRows(const DropArgs& a, const DropPlace& 
     if (at.n >= kDropCols) bias.load(from);
     else bias.loadFew(from, at.n);
   }
-  forRows<E>(at, a.cols, [&](int64_t i, auto load, auto settle, auto store) {
-    E v, z, out;
-    load(&v, x + i * a.xStride);
-    if (RESIDUAL) load(&z, residual + i * a.residualStride);
-    const Words w = wordsOf(a, offset, first + (uint32_t)i, at.group);
-    settle(&v);
-    if (RESIDUAL) settle(&z);
+  withAccess<E>(at, a.cols, [&](auto load, auto settle, auto store) {
+    for (int64_t i = at.row; i < at.rows; i += at.step) {
+      E v, z, out;
+      load(&v, x + i * a.xStride);
+      if (RESIDUAL) load(&z, residual + i * a.residualStride);
+      const Words w = wordsOf(a, offset, first + (uint32_t)i, at.group);
+      settle(&v);
+      if (RESIDUAL) settle(&z);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float r = RESIDUAL ? z[e] : 0.0f;
-      out.set(e, kept(w, e, a.threshold) ? fmaf(v[e] + bias[e], a.scale, r) : r);
+      for (int e = 0; e < 8; ++e) {
+        const float r = RESIDUAL ? z[e] : 0.0f;
+        out.set(e, kept(w, e, a.threshold) ? fmaf(v[e] + bias[e], a.scale, r) : r);
+      }
+      store(y + i * a.yStride, out);
     }
-    store(y + i * a.yStride, out);
   });
 }
 
@@ -232,18 +232,20 @@ __global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackward(const DropA
     const uint32_t first = a.firstRow[at.rank];
     const T* dy = (const T*)a.x[at.rank] + at.column;
     T* dx = a.y[at.rank] ? (T*)a.y[at.rank] + at.column : nullptr;
-    forRows<E>(at, a.cols, [&](int64_t i, auto load, auto settle, auto store) {
-      E v, out;
-      load(&v, dy + i * a.xStride);
-      const Words w = wordsOf(a, offset, first + (uint32_t)i, at.group);
-      settle(&v);
+    withAccess<E>(at, a.cols, [&](auto load, auto settle, auto store) {
+      for (int64_t i = at.row; i < at.rows; i += at.step) {
+        E v, out;
+        load(&v, dy + i * a.xStride);
+        const Words w = wordsOf(a, offset, first + (uint32_t)i, at.group);
+        settle(&v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = kept(w, e, a.threshold) ? v[e] : 0.0f;
-        if (SUMS) sum[e] += d;
-        out.set(e, d * a.scale);
+        for (int e = 0; e < 8; ++e) {
+          const float d = kept(w, e, a.threshold) ? v[e] : 0.0f;
+          if (SUMS) sum[e] += d;
+          out.set(e, d * a.scale);
+        }
+        if (dx) store(dx + i * a.yStride, out);
       }
-      if (dx) store(dx + i * a.yStride, out);
     });
   }
   if constexpr (SUMS) {
@@ -263,6 +265,85 @@ __global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackward(const DropA
       const float all = joinSlices<kDropBackBlock / kWave>([&](int w) { return lds[w][threadIdx.x]; });
       a.partial[(size_t)slice * a.partialCols + c] = all;
     }
+  }
+}
+
+// Few rows in one launch: a workgroup takes 64 columns of all of them, 64 rows
+// at a time, and writes their sums to every rank itself.  8192 columns: one row
+// 3.9 us, 5.9 in two launches; 64 rows of 8 ranks 5.7, 6.7; 256 7.3, 8.3; 512 9.8,
+// 9.0, where what it takes to draw the rows one after another bounds it (two or
+// four rows' loads ahead gained nothing).
+constexpr int kFewAcross = 8, kFewRows = 256;
+
+struct DropFewArgs {
+  DropArgs rows;
+  void* dbias[kOpRanks];
+};
+
+template <int DT, int WT>
+__global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackwardFew(const DropFewArgs w) {
+  typedef typename Elem<DT>::type T;
+  typedef typename Elem<WT>::type W;
+  typedef Eight<DT, false> E;
+  constexpr int WAVES = kDropBackBlock / kWave, COLS = kFewAcross * kDropCols;
+  __shared__ float lds[WAVES][COLS];
+  struct RowAt {
+    const T* dy;
+    T* dx;
+    uint32_t index;
+  };
+  __shared__ RowAt rows[kFewRows];
+  const DropArgs& a = w.rows;
+  for (int r = 0; r < a.nranks; ++r) {
+    const int from = a.rowStart[r], n = a.rowStart[r + 1] - from;
+    for (int i = threadIdx.x; i < n; i += kDropBackBlock)
+      rows[from + i] = RowAt{(const T*)a.x[r] + i * a.xStride, a.y[r] ? (T*)a.y[r] + i * a.yStride : nullptr,
+                             a.firstRow[r] + (uint32_t)i};
+  }
+  __syncthreads();
+  const uint64_t offset = a.offset + (a.step ? *a.step : 0);
+  const int total = a.rowStart[a.nranks];
+  for (int64_t tile = blockIdx.x; tile * COLS < a.cols; tile += gridDim.x) {
+    DropPlace at;
+    at.rank = 0;
+    at.group = (uint32_t)(tile * kFewAcross) + threadIdx.x % kFewAcross;
+    at.column = (int)at.group * kDropCols;
+    at.n = a.cols - at.column;
+    at.row = (int)threadIdx.x / kFewAcross;
+    at.rows = at.n > 0 ? total : 0;
+    at.step = kDropBackBlock / kFewAcross;
+    FloatVec<8> sum = (FloatVec<8>)0.0f;
+    withAccess<E>(at, a.cols, [&](auto load, auto settle, auto store) {
+      for (int i = at.row; i < at.rows; i += at.step) {
+        const RowAt row = rows[i];
+        E v, out;
+        load(&v, row.dy + at.column);
+        const Words words = wordsOf(a, offset, row.index, at.group);
+        settle(&v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = kept(words, e, a.threshold) ? v[e] : 0.0f;
+          sum[e] += d;
+          out.set(e, d * a.scale);
+        }
+        if (row.dx) store(row.dx + at.column, out);
+      }
+    });
+#pragma unroll
+    for (int m = kFewAcross; m < kWave; m *= 2)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor(sum[e], m);
+    const int wave = (int)threadIdx.x / kWave, lane = (int)threadIdx.x % kWave;
+    if (lane < kFewAcross)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) lds[wave][lane * kDropCols + e] = sum[e];
+    __syncthreads();
+    const int64_t c = tile * COLS + threadIdx.x;
+    if (threadIdx.x < COLS && c < a.cols) {
+      const float all = joinSlices<WAVES>([&](int k) { return lds[k][threadIdx.x]; });
+      for (int r = 0; r < a.nranks; ++r) ((W*)w.dbias[r])[c] = (W)(all * a.scale);
+    }
+    __syncthreads();   // before the next columns' sums
   }
 }
 
@@ -356,6 +437,16 @@ struct DropBackward {
     const auto kernel = a.partial ? (a.stream ? dropoutAddBackward<DT, true, true> : dropoutAddBackward<DT, true, false>)
                                   : (a.stream ? dropoutAddBackward<DT, false, true> : dropoutAddBackward<DT, false, false>);
     return launchKernel(kernel, grid, dim3(kDropBackBlock), a, st);
+  }
+};
+
+template <int DT, int WT>
+struct DropBackwardFew {
+  static hipError_t run(const DropFewArgs& w, hipStream_t st) {
+    constexpr int COLS = kFewAcross * kDropCols;
+    return launchKernel(dropoutAddBackwardFew<DT, WT>,
+                        dim3(gridOf(((int64_t)w.rows.cols + COLS - 1) / COLS, kDropBackBlock)), dim3(kDropBackBlock), w,
+                        st);
   }
 };
 
@@ -510,7 +601,8 @@ arResult_t dropBackward(const void* const* dy, void* const* dx, void* const* dbi
     if (!ok) return arInvalidArgument;
   }
   if (outputsOverlap(v)) return arInvalidArgument;
-  DropArgs a{};
+  DropFewArgs w{};
+  DropArgs& a = w.rows;
   fillDraw(&a, p, seed, offset, step);
   int partials = 0;
   const size_t bytes = (size_t)s.total * cols * (size_t)esz * (dx ? 2 : 1);
@@ -526,6 +618,11 @@ arResult_t dropBackward(const void* const* dy, void* const* dx, void* const* dbi
     a.xStride = (int64_t)dyStride;
     a.yStride = (int64_t)dxStride;
     a.stream = bytes > kDropStream;
+    if (dbias != nullptr && s.launches == 1 && s.total <= kFewRows) {
+      for (int r = 0; r < nranks; ++r) w.dbias[r] = dbias[r];
+      return byTypes<DropBackwardFew, const DropFewArgs&, hipStream_t>(dtype, wtype, w, st) == hipSuccess ? arSuccess
+                                                                                                          : arHipError;
+    }
     if (dbias != nullptr) a.partial = (float*)workspace + (size_t)partials * a.partialCols;
     const dim3 grid((unsigned)slices * (unsigned)a.tiles);
     if (byType<DropBackward, const DropArgs&, dim3, hipStream_t>(dtype, a, grid, st) != hipSuccess) return arHipError;

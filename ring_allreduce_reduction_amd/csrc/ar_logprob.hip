@@ -333,14 +333,16 @@ struct LpCut {
   int64_t pieces;    // of all shards
 };
 
-// Pieces need a second launch, so they are for few rows: 300 rows x 8 x 16000
-// bf16 20.6 us in pieces, 19.3 a workgroup a row; 700 x 5 x 10007 fp32 23.2 and
-// 19.8; one row 6.  A piece is 8192 columns, or down to 2048
-// where they are few (backward 96 rows x 4 x 8003 fp32 6.2 us, 6.8 without;
-// more than two a CU gained nothing).
+// Pieces need a second launch, so they are for few rows of a long vocabulary:
+// 64 rows x 8 x 16000 bf16 9.3 us in pieces, 10.9 a workgroup a row; 128 rows
+// 12.3, 12.4; 300 20.6, 19.3; one row x 8 x 4000 6.7, 5.4; x 8000 6.8, 7.0.  A
+// piece is 8192 columns, or down to 2048 where they are few (backward 96 rows x 4
+// x 8003 fp32 6.2 us, 6.8 without; more than two a CU gained nothing).
 LpCut lpCut(const size_t* cols, int nranks, size_t rows) {
   LpCut k;
-  k.whole = nranks <= kOpRanks && rows >= (size_t)kOpsCUs;
+  size_t vocabulary = 0;
+  for (int r = 0; r < nranks; ++r) vocabulary += cols[r];
+  k.whole = nranks <= kOpRanks && (rows >= (size_t)kOpsCUs / 2 || vocabulary <= 1 << 15);
   k.pieceCols = 8192;
   const auto count = [&] {
     k.pieces = 0;
@@ -421,11 +423,11 @@ struct LpRows {
     // Narrow shards: 16 threads take one, alone on a row or four of them (8192
     // rows x 8 x 250 bf16 16 us, 37 with a wavefront a shard, 62 with a workgroup;
     // x 1000 26, 35; x 2000 48, 45; 1 x 256 4.7, 8.3 with a wavefront a row; 1 x
-    // 2000 8.6, 10.3, but 300 rows of it 6.3 and 4.6).
-    if (columns <= 128 * V) {
+    // 2000 8.6, 10.3), where there are many rows: of 300 x 8 x 1000 7.2 us and 5.9
+    // with a wavefront a shard, 1 x 2000 6.3 and 4.6.
+    if (columns <= 128 * V && a.rows >= 4 * kOpsCUs) {
       if (a.nranks < 4) return launch<kLpBlock, 16, 16>(a, stream, st);
-      // 300 rows x 8 x 1000 7.2 us, 5.9 with a wavefront a shard
-      if (columns <= 32 * V || a.rows >= 4 * kOpsCUs) return launch<kLpBlock, kWave, 16>(a, stream, st);
+      return launch<kLpBlock, kWave, 16>(a, stream, st);
     }
     // From four shards on a wavefront takes a shard at a time: shards rarely
     // fill the vectors that a whole workgroup has in flight (8192 rows x 8 x 5000

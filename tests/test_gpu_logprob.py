@@ -12,7 +12,8 @@ pytestmark = pytest.mark.gpu
 
 DTYPES = [torch.float32, torch.float16, torch.bfloat16]
 INF, NAN = float("inf"), float("nan")
-SHARDS = [[1], [7], [64, 65], [1000], [3, 0, 2049, 1], [4096, 4096], [8191, 8193], [20000, 1, 9], [16000] * 8, [33] * 40]
+EMPTY = [0]   # shards without columns that calls get at their end: past 16 ranks rows are taken in pieces
+SHARDS = [[40000, 3], [12345] * 4, [1], [7], [64, 65], [1000], [3, 0, 2049, 1], [4096, 4096], [8191, 8193], [20000, 1, 9], [16000] * 8, [33] * 40]
 
 
 @pytest.fixture(scope="module")
@@ -38,8 +39,16 @@ def inputs(rows, shards, dt, seed, ignored=0.2, std=3.0):
     return xs, t
 
 
+@pytest.fixture(params=[0, 15], ids=["rows", "pieces"])
+def form(request):
+    """Both forms of a call with few rows, whatever its vocabulary."""
+    EMPTY[0] = request.param
+    yield request.param
+    EMPTY[0] = 0
+
+
 def on_device(xs, pad, offs):
-    return [dev(x, pad + r % 3, offs) for r, x in enumerate(xs)]
+    return [dev(x, pad + r % 3, offs) for r, x in enumerate(xs)] + [torch.empty(len(xs[0]), 0, dtype=xs[0].dtype, device="cuda")] * EMPTY[0]
 
 
 def run_forward(B, xs, targets, scale=1.0, pad=0, offs=0, stats=True, stream=None, workspace=None):
@@ -69,7 +78,7 @@ def statistics(xs, targets, scale):
 
 def run_backward(B, dlogp, xs, targets, top, log_sum, scale=1.0, pad=0, offs=0, inplace=False, stream=None):
     x = on_device(xs, pad, offs)
-    out = x if inplace else [dev(torch.full_like(t, NAN), pad + 1, offs) for t in xs]
+    out = x if inplace else on_device([torch.full_like(t, NAN) for t in xs], pad + 1, offs)
     t = targets.cuda()
     torch.cuda.synchronize()
     B.arTokenLogprobBackward(dlogp.cuda(), x, t, top.cuda(), log_sum.cuda(), out, scale, stream=stream)
@@ -116,7 +125,7 @@ def test_many_rows(B, rows, shards, dt):
 
 @pytest.mark.parametrize("rows", [1, 1200])
 @pytest.mark.parametrize("dt", DTYPES, ids=str)
-def test_padded_rows_odd_addresses_in_place(B, rows, dt):
+def test_padded_rows_odd_addresses_in_place(B, form, rows, dt):
     xs, t = inputs(rows, [129, 40, 513], dt, 3)
     for pad, offs in ((0, 1), (3, 0), (8, 5)):
         check_forward(run_forward(B, xs, t, pad=pad, offs=offs), xs, t)
@@ -126,14 +135,14 @@ def test_padded_rows_odd_addresses_in_place(B, rows, dt):
 
 
 @pytest.mark.parametrize("rows", [5, 1100])
-def test_logp_alone(B, rows):
+def test_logp_alone(B, form, rows):
     xs, t = inputs(rows, [300, 20], torch.bfloat16, 4)
     check_forward(run_forward(B, xs, t, stats=False), xs, t)
 
 
 @pytest.mark.parametrize("rows", [8, 1104])
 @pytest.mark.parametrize("dt", DTYPES, ids=str)
-def test_masks(B, rows, dt):
+def test_masks(B, form, rows, dt):
     """-inf and the type's lowest value as masks: beside ordinary logits, in whole shards, everywhere but the target,
     and (the lowest value) in a whole row."""
     low = torch.finfo(dt).min
@@ -164,7 +173,7 @@ def test_masks(B, rows, dt):
 
 
 @pytest.mark.parametrize("rows", [4, 1100])
-def test_masked_target(B, rows):
+def test_masked_target(B, form, rows):
     """logp is -inf; the gradient is that of the others."""
     xs, t = inputs(rows, [100, 60], torch.float32, 9, ignored=0.0)
     whole = torch.cat(xs, 1)
@@ -179,7 +188,7 @@ def test_masked_target(B, rows):
 
 
 @pytest.mark.parametrize("rows", [6, 1104])
-def test_rows_without_a_distribution(B, rows):
+def test_rows_without_a_distribution(B, form, rows):
     """NaN, +inf or nothing but -inf give NaN, in these rows and no others; ignored rows are not looked at."""
     xs, t = inputs(rows, [640, 333], torch.bfloat16, 11, ignored=0.0)
     xs[0][0, 17], xs[1][1, 330] = NAN, INF
@@ -201,7 +210,7 @@ def test_rows_without_a_distribution(B, rows):
 
 
 @pytest.mark.parametrize("rows", [4, 1100])
-def test_a_target_past_the_vocabulary(B, rows):
+def test_a_target_past_the_vocabulary(B, form, rows):
     xs, t = inputs(rows, [50, 70], torch.float32, 12, ignored=0.0)
     t[0], t[1] = 120, (1 << 62)
     t[2] = 119
@@ -214,7 +223,7 @@ def test_a_target_past_the_vocabulary(B, rows):
 
 
 @pytest.mark.parametrize("rows", [3, 1100])
-def test_far_logits(B, rows):
+def test_far_logits(B, form, rows):
     """Large offsets cancel, and neither large nor small logits overflow."""
     xs, t = inputs(rows, [900, 200], torch.float32, 13, ignored=0.0)
     for scale, shift in ((1.0, 1000.0), (1.0, -30000.0), (64.0, 0.0), (2.0 ** -10, 0.0)):
@@ -225,7 +234,7 @@ def test_far_logits(B, rows):
 
 
 @pytest.mark.parametrize("rows", [2, 1100])
-def test_equal_logits(B, rows):
+def test_equal_logits(B, form, rows):
     """Every token equally likely: logSum is ln n."""
     for v in (0.0, 5.5, -65000.0):
         xs = [torch.full((rows, c), v) for c in (1000, 24)]
@@ -258,7 +267,7 @@ def test_gradient_sums_to_zero_and_agrees_with_differences(B):
     assert ((slope - want).abs() <= third * h * h / 6 + 400 * ou.U / h * d.abs().double()).all()
 
 
-@pytest.mark.parametrize("rows,shards", [(3, [5000, 5001]), (1200, [500, 300])], ids=str)
+@pytest.mark.parametrize("rows,shards", [(3, [5000, 5001]), (3, [25000, 15001]), (1200, [500, 300])], ids=str)
 def test_graphs_replayed_side_by_side(B, rows, shards):
     """Two graphs, each with its own workspace, replayed on two streams with new logits."""
     sets = []

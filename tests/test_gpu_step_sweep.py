@@ -177,7 +177,7 @@ def test_a_stream_of_another_device_is_refused(B):
 def test_workspaces_are_allocated_where_none_is_given(B):
     """On the stream that uses them; too small ones are refused."""
     st = torch.cuda.Stream()
-    xs, t = lp.inputs(5, [3000, 2000], torch.float32, 2)
+    xs, t = lp.inputs(5, [30000, 20000], torch.float32, 2)
     lp.check_forward(lp.run_forward(B, xs, t, stream=st), xs, t)
     small = torch.empty(8, dtype=torch.uint8, device="cuda")
     with pytest.raises(ValueError, match="workspace must be contiguous and hold"):
@@ -197,7 +197,7 @@ def test_equal_calls_give_equal_bits(B):
     dys, _, _ = dp.inputs([900, 700], 1000, torch.float32, torch.float32, 4)
     a, b = (dp.run_backward(B, dys, torch.float32, 0.3)[1][0] for _ in range(2))
     assert torch.equal(a, b)
-    for rows, shards in ((3, [9000, 9000]), (1100, [900, 800])):
+    for rows, shards in ((3, [9000, 9000]), (3, [30000, 9000]), (1100, [900, 800])):
         xs, t = lp.inputs(rows, shards, torch.bfloat16, 3)
         a, b = (lp.run_forward(B, xs, t) for _ in range(2))
         assert all(torch.equal(u, v) for u, v in zip(a, b))
