@@ -772,7 +772,7 @@ arResult_t arTokenLogprob(const void* const* logits, const size_t* cols, const s
                           arDataType_t dtype, void* workspace, size_t workspaceBytes, void* stream);
 
 /* arTokenLogprobWorkspace -- the workspace bytes of an arTokenLogprob with
- * these rows and shards (a pure function; 0 where there are rows enough). */
+ * these rows and shards (a pure function; 0 where one launch does). */
 arResult_t arTokenLogprobWorkspace(size_t rows, const size_t* cols, int nranks, size_t* bytes);
 
 /*

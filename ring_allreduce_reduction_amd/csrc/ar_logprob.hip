@@ -33,8 +33,8 @@ struct LpArgs {
   float* logp;
   float* top;
   float* logSum;
-  float2* partial;                  // the row's pieces' (largest value, sum), `pieces` a row, this launch's first
-  int pieces;
+  float2* partial;                  // (largest value, sum) of a row's parts, `parts` a row, this launch's first; or null
+  int parts;
   int rows, nranks;
   float scale, scaleLog2e;
 };
@@ -162,13 +162,20 @@ __device__ __forceinline__ Running joinThreads(Running run, float c, Running* ld
   return run;
 }
 
-// The target's logit, read early; NaN for a target past the vocabulary.
+// The target's logit, read early; NaN where the launch's shards have none.
 template <int DT>
 __device__ __forceinline__ float targetLogit(const LpArgs& a, int64_t row, int64_t t) {
   for (int r = 0; r < a.nranks; ++r)
     if (t >= a.colStart[r] && t < a.colStart[r + 1])
       return (float)((const typename Elem<DT>::type*)a.x[r])[row * a.xStride[r] + (t - a.colStart[r])];
   return NAN;
+}
+
+// Of several launches each leaves the running values of its shards, and the one
+// with the target its logit, for tokenLogprobJoin.
+__device__ __forceinline__ void putPart(const LpArgs& a, int64_t row, int64_t t, const Running& run, float logit) {
+  a.partial[row * a.parts] = make_float2(run.top, run.sum);
+  if (t >= a.colStart[0] && t < a.colStart[a.nranks]) a.logp[row] = logit;
 }
 
 template <typename A>
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(BLOCK) tokenLogprobRows(const LpArgs a) {
        row += (int64_t)gridDim.x * ROWS) {
     const int64_t t = a.targets[row];
     if (t < 0) {
-      if (first) putIgnored(a, row);
+      if (first && !a.partial) putIgnored(a, row);
       continue;
     }
     float logit = 0.0f;
@@ -212,7 +219,8 @@ __global__ void __launch_bounds__(BLOCK) tokenLogprobRows(const LpArgs a) {
       meetColumns<DT, SHARD, STREAM>(&run, thread, (const T*)a.x[r] + row * a.xStride[r], 0,
                                      a.colStart[r + 1] - a.colStart[r], a.scaleLog2e);
     run = joinThreads<ROW>(run, a.scaleLog2e, lds);
-    if (first) putRow(a, row, run, logit);
+    if (first && a.partial) putPart(a, row, t, run, logit);
+    else if (first) putRow(a, row, run, logit);
   }
 }
 
@@ -235,8 +243,7 @@ __device__ __forceinline__ PieceAt pieceAt(const LpArgs& a) {
   return p;
 }
 
-// Few rows, or more shards than a launch holds: a workgroup a piece of a row
-// leaves the piece's running values; tokenLogprobJoin joins them.
+// Few rows of a long vocabulary: a workgroup a piece of a row leaves the piece's running values; tokenLogprobJoin joins them.
 template <int DT>
 __global__ void __launch_bounds__(kLpBlock) tokenLogprobPieces(const LpArgs a) {
   typedef typename Elem<DT>::type T;
@@ -252,7 +259,7 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobPieces(const LpArgs a) {
     Running run = nothing();
     meetColumns<DT, kLpBlock, false>(&run, (int)threadIdx.x, x, p.from, p.to, a.scaleLog2e);
     run = joinThreads<kLpBlock>(run, a.scaleLog2e, lds);
-    if (threadIdx.x == 0) a.partial[row * a.pieces + blockIdx.x] = make_float2(run.top, run.sum);
+    if (threadIdx.x == 0) a.partial[row * a.parts + blockIdx.x] = make_float2(run.top, run.sum);
   }
 }
 
@@ -262,7 +269,7 @@ struct LpJoinArgs {
   float *logp, *top, *logSum;
   const float2* partial;
   int64_t vocabulary;
-  int pieces, rows;
+  int parts, rows;
   float scale, scaleLog2e;
 };
 
@@ -275,8 +282,8 @@ __global__ void __launch_bounds__(kWave) tokenLogprobJoin(const LpJoinArgs a) {
       continue;
     }
     Running run = nothing();
-    for (int i = threadIdx.x; i < a.pieces; i += kWave) {
-      const float2 p = a.partial[row * a.pieces + i];
+    for (int i = threadIdx.x; i < a.parts; i += kWave) {
+      const float2 p = a.partial[row * a.parts + i];
       run = join(run, Running{p.x, p.y}, a.scaleLog2e);
     }
     run = joinThreads<kWave>(run, a.scaleLog2e, nullptr);
@@ -325,12 +332,12 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpArgs a)
   }
 }
 
-// How a call is cut, a pure function of its shapes: a workgroup or a wavefront
-// a row, or pieces of rows.
+// How a call is cut, a pure function of its shapes: a launch's shards of a row
+// at once, or pieces of them.
 struct LpCut {
   bool whole;
   int pieceCols;     // columns of a piece, at most
-  int64_t pieces;    // of all shards
+  int64_t parts;     // of a row: pieces of all shards, or launches; 1 needs no join
 };
 
 // Pieces need a second launch, so they are for few rows of a long vocabulary:
@@ -342,21 +349,22 @@ LpCut lpCut(const size_t* cols, int nranks, size_t rows) {
   LpCut k;
   size_t vocabulary = 0;
   for (int r = 0; r < nranks; ++r) vocabulary += cols[r];
-  k.whole = nranks <= kOpRanks && (rows >= (size_t)kOpsCUs / 2 || vocabulary <= 1 << 15);
+  k.whole = rows >= (size_t)kOpsCUs / 2 || vocabulary <= 1 << 15;
   k.pieceCols = 8192;
   const auto count = [&] {
-    k.pieces = 0;
-    for (int r = 0; r < nranks; ++r) k.pieces += (int64_t)((cols[r] + k.pieceCols - 1) / k.pieceCols);
+    k.parts = 0;
+    for (int r = 0; r < nranks; ++r) k.parts += (int64_t)((cols[r] + k.pieceCols - 1) / k.pieceCols);
   };
   count();
-  while (k.pieceCols > 2048 && (int64_t)rows * k.pieces < 2 * kOpsCUs) {
+  while (k.pieceCols > 2048 && (int64_t)rows * k.parts < 2 * kOpsCUs) {
     k.pieceCols /= 2;
     count();
   }
-  while (k.pieces > 4096) {   // the workspace stays small beside a long vocabulary
+  while (k.parts > 4096) {   // the workspace stays small beside a long vocabulary
     k.pieceCols *= 2;
     count();
   }
+  if (k.whole) k.parts = (nranks + kOpRanks - 1) / kOpRanks;
   return k;
 }
 
@@ -382,7 +390,7 @@ arResult_t lpWorkspace(size_t rows, const size_t* cols, int nranks, size_t* byte
   int64_t vocabulary;
   if (bytes == nullptr || !shardsOk(cols, nullptr, nranks, rows, &vocabulary)) return arInvalidArgument;
   const LpCut k = lpCut(cols, nranks, rows);
-  *bytes = k.whole ? 0 : (rows * (size_t)k.pieces * sizeof(float2) + 15) / 16 * 16;
+  *bytes = k.whole && k.parts == 1 ? 0 : (rows * (size_t)k.parts * sizeof(float2) + 15) / 16 * 16;
   return arSuccess;
 }
 
@@ -419,7 +427,7 @@ struct LpRows {
   }
   static hipError_t run(const LpArgs& a, bool stream, hipStream_t st) {
     constexpr int V = kVec<DT>;
-    const int64_t columns = a.vocabulary / a.nranks;   // of a shard
+    const int64_t all = a.colStart[a.nranks] - a.colStart[0], columns = all / a.nranks;   // of a shard
     // Narrow shards: 16 threads take one, alone on a row or four of them (8192
     // rows x 8 x 250 bf16 16 us, 37 with a wavefront a shard, 62 with a workgroup;
     // x 1000 26, 35; x 2000 48, 45; 1 x 256 4.7, 8.3 with a wavefront a row; 1 x
@@ -432,13 +440,16 @@ struct LpRows {
     // From four shards on a wavefront takes a shard at a time: shards rarely
     // fill the vectors that a whole workgroup has in flight (8192 rows x 8 x 5000
     // bf16 115 us, 139 with 256 threads together, 191 with 512; 8000 158, 162,
-    // 205; 16000 317, 315, 308).  Fewer shards: rows of a few vectors go to a
-    // wavefront each (20000 x 2000 19 us, 43 with a workgroup; 4096 x 8000 15.3,
-    // 15.5), others to workgroups as wide as their vectors fill (4096 x 50257 70
-    // us with 512, 75 with 256).
+    // 205; 16000 317, 315, 308).  With fewer shards, rows of a few vectors that
+    // are many enough go to a wavefront each (20000 x 2000 19 us, 43 with a
+    // workgroup; 4096 x 8000 15.3, 15.5; 500 x 4000 5.2, 4.9; 1 x 8000 5.7, 4.2);
+    // others to workgroups as wide as their vectors fill (4096 x 50257 70 us with
+    // 512, 75 with 256; 50 rows x 3 x 6000 5.8 us with a wavefront a shard, 6.2
+    // together; 500 x 2 x 30000 20, 14).
     if (a.nranks > 4) return launch<512, 512, kWave>(a, stream, st);
     if (a.nranks == 4) return launch<kLpBlock, kLpBlock, kWave>(a, stream, st);
-    if (a.vocabulary <= 16 * kWave * V) return launch<kLpBlock, kWave, kWave>(a, stream, st);
+    if (all <= (int64_t)V * (a.rows < 1024 ? a.rows : 1024)) return launch<kLpBlock, kWave, kWave>(a, stream, st);
+    if (a.nranks > 1 && columns <= 1024 * V) return launch<kLpBlock, kLpBlock, kWave>(a, stream, st);
     if (columns < 3 * 512 * V) return launch<kLpBlock, kLpBlock, kLpBlock>(a, stream, st);
     return launch<512, 512, 512>(a, stream, st);
   }
@@ -495,7 +506,8 @@ arResult_t lpForward(const void* const* logits, const size_t* cols, const size_t
     if (cols[r] > 0)
       ok = ok && addRows(v, logits[r], rows, cols[r], strides ? strides[r] : cols[r], elemSize(dtype), false, -1);
   if (!ok) return arInvalidArgument;
-  if (!k.whole) {
+  const bool joined = !k.whole || k.parts > 1;
+  if (joined) {
     size_t need = 0;
     const arResult_t r = lpWorkspace(rows, cols, nranks, &need);
     if (r != arSuccess) return r;
@@ -512,23 +524,24 @@ arResult_t lpForward(const void* const* logits, const size_t* cols, const size_t
   a.scale = scale;
   a.scaleLog2e = (float)((double)scale * 1.44269504088896340736);
   a.vocabulary = vocabulary;
-  a.pieces = (int)k.pieces;
-  if (k.whole) {
-    const size_t bytes = rows * (size_t)vocabulary * (size_t)elemSize(dtype);
-    fillShards(&a, logits, cols, strides, nranks, 0, k.pieceCols);
-    return byType<LpRows, const LpArgs&, bool, hipStream_t>(dtype, a, bytes > kLpStream, st) == hipSuccess ? arSuccess : arHipError;
-  }
-  int piece = 0;
+  a.parts = (int)k.parts;
+  const bool stream = rows * (size_t)vocabulary * (size_t)elemSize(dtype) > kLpStream;
+  int part = 0;
   for (int first = 0; first < nranks; first += kOpRanks) {
     fillShards(&a, logits, cols, strides, nranks, first, k.pieceCols);
-    a.partial = (float2*)workspace + piece;
-    piece += a.pieceStart[a.nranks];
-    if (a.pieceStart[a.nranks] > 0 && byType<LpPieces, const LpArgs&, hipStream_t>(dtype, a, st) != hipSuccess)
-      return arHipError;
+    const int pieces = a.pieceStart[a.nranks];
+    if (joined) a.partial = (float2*)workspace + part;
+    hipError_t e = hipSuccess;
+    if (k.whole) e = byType<LpRows, const LpArgs&, bool, hipStream_t>(dtype, a, stream, st);
+    else if (pieces > 0) e = byType<LpPieces, const LpArgs&, hipStream_t>(dtype, a, st);
+    if (e != hipSuccess) return arHipError;
+    part += k.whole ? 1 : pieces;
   }
-  const LpJoinArgs j = {targets, logp, top, logSum, (const float2*)workspace, vocabulary, a.pieces, a.rows, scale,
+  if (!joined) return arSuccess;
+  const LpJoinArgs j = {targets, logp, top, logSum, (const float2*)workspace, vocabulary, a.parts, a.rows, scale,
                         a.scaleLog2e};
-  return launchKernel(tokenLogprobJoin, dim3(gridOf(a.rows, kWave)), dim3(kWave), j, st) == hipSuccess ? arSuccess : arHipError;
+  return launchKernel(tokenLogprobJoin, dim3(gridOf(a.rows, kWave)), dim3(kWave), j, st) == hipSuccess ? arSuccess
+                                                                                                      : arHipError;
 }
 
 arResult_t lpBackward(const float* dlogp, const void* const* logits, const size_t* cols, const size_t* strides,

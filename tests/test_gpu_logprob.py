@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 DTYPES = [torch.float32, torch.float16, torch.bfloat16]
 INF, NAN = float("inf"), float("nan")
-EMPTY = [0]   # shards without columns that calls get at their end: past 16 ranks rows are taken in pieces
+MORE = [0, 0]   # shards that calls get at their end: without columns, and of 33000 columns that are masked out
 SHARDS = [[40000, 3], [12345] * 4, [1], [7], [64, 65], [1000], [3, 0, 2049, 1], [4096, 4096], [8191, 8193], [20000, 1, 9], [16000] * 8, [33] * 40]
 
 
@@ -39,16 +39,19 @@ def inputs(rows, shards, dt, seed, ignored=0.2, std=3.0):
     return xs, t
 
 
-@pytest.fixture(params=[0, 15], ids=["rows", "pieces"])
+@pytest.fixture(params=[(0, 0), (15, 0), (0, 1)], ids=["rows", "launches", "pieces"])
 def form(request):
-    """Both forms of a call with few rows, whatever its vocabulary."""
-    EMPTY[0] = request.param
+    """The forms a call can take: one launch, several for more than 16 ranks, and for few rows of a long vocabulary
+    pieces of them."""
+    MORE[:] = request.param
     yield request.param
-    EMPTY[0] = 0
+    MORE[:] = 0, 0
 
 
 def on_device(xs, pad, offs):
-    return [dev(x, pad + r % 3, offs) for r, x in enumerate(xs)] + [torch.empty(len(xs[0]), 0, dtype=xs[0].dtype, device="cuda")] * EMPTY[0]
+    more = [torch.empty(len(xs[0]), 0, dtype=xs[0].dtype, device="cuda")] * MORE[0]
+    more += [torch.full((len(xs[0]), 33000), -INF, dtype=xs[0].dtype, device="cuda") for _ in range(MORE[1])]
+    return [dev(x, pad + r % 3, offs) for r, x in enumerate(xs)] + more
 
 
 def run_forward(B, xs, targets, scale=1.0, pad=0, offs=0, stats=True, stream=None, workspace=None):
@@ -167,7 +170,7 @@ def test_masks(B, form, rows, dt):
     d, (top, log_sum) = gradients(rows, 8), statistics(xs, t, 1.0)
     out = run_backward(B, d, xs, t, top, log_sum)
     check_backward(out, d, xs, t, top, log_sum)
-    got = torch.cat([o.cpu() for o in out], 1)
+    got = torch.cat([o.cpu() for o in out[:3]], 1)
     masked = whole == -INF
     assert (got[masked] == 0).all()
 
@@ -202,7 +205,7 @@ def test_rows_without_a_distribution(B, form, rows):
     rest = [x[5:] for x in xs]
     check_forward((logp[5:], top[5:], log_sum[5:]), rest, t[5:])
     out = run_backward(B, torch.ones(rows), xs, t, top.cpu(), log_sum.cpu())
-    got = torch.cat([o.float().cpu() for o in out], 1)
+    got = torch.cat([o.float().cpu() for o in out[:2]], 1)
     assert torch.isnan(got[0]).all() and torch.isnan(got[1, 640 + 330]) and torch.isnan(got[2]).all()
     assert (got[3:5] == 0).all() and torch.isfinite(got[5:]).all()
     zero = run_backward(B, torch.zeros(rows), xs, t, top.cpu(), log_sum.cpu())
@@ -212,13 +215,13 @@ def test_rows_without_a_distribution(B, form, rows):
 @pytest.mark.parametrize("rows", [4, 1100])
 def test_a_target_past_the_vocabulary(B, form, rows):
     xs, t = inputs(rows, [50, 70], torch.float32, 12, ignored=0.0)
-    t[0], t[1] = 120, (1 << 62)
+    t[0], t[1] = 120 + 33000 * MORE[1], (1 << 62)
     t[2] = 119
     logp, top, log_sum = run_forward(B, xs, t)
     assert torch.isnan(logp[:2]).all() and torch.isfinite(logp[2:]).all()
     d = torch.ones(rows)
     d[1] = 0.0
-    out = torch.cat([o.cpu() for o in run_backward(B, d, xs, t, top.cpu(), log_sum.cpu())], 1)
+    out = torch.cat([o.cpu() for o in run_backward(B, d, xs, t, top.cpu(), log_sum.cpu())[:2]], 1)
     assert torch.isnan(out[0]).all() and (out[1] == 0).all() and torch.isfinite(out[2:]).all()
 
 
