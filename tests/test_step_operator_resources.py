@@ -1,0 +1,24 @@
+"""The kernels of dropout, token log-probabilities and the policy loss in the built code object: none spills or uses
+scratch memory, and the wide ones keep the wavefronts their launches count on.  CPU only."""
+import pytest
+from test_kernel_resources import kernels  # noqa: F401  (a fixture)
+
+FAMILIES = {"dropoutAddI": 10, "dropoutAddBackwardI": 12, "dropoutAddBackwardFewI": 5, "dropoutBiasGradsI": 3,
+            "tokenLogprobRowsI": 42, "tokenLogprobPiecesI": 3, "tokenLogprobJoinE": 1, "tokenLogprobBackwardI": 18,
+            "policySumsE": 1, "policyGradE": 1, "policyFewE": 1}
+
+
+@pytest.mark.parametrize("family", FAMILIES)
+def test_kernels_do_not_spill(kernels, family):  # noqa: F811
+    hits = {n: k for n, k in kernels.items() if "%d%s" % (len(family) - 1, family) in n}
+    assert len(hits) == FAMILIES[family], sorted(hits)
+    bad = {n: k for n, k in hits.items() if k["private_segment_fixed_size"] or k["vgpr_spill_count"]}
+    assert not bad, bad
+
+
+def test_registers_leave_eight_wavefronts_a_simd(kernels):  # noqa: F811
+    """Memory-bound kernels with one step a wavefront in flight: 64 registers at most."""
+    for name in ("dropoutAddI", "dropoutAddBackwardI", "tokenLogprobRowsI", "tokenLogprobBackwardI"):
+        for n, k in kernels.items():
+            if "%d%s" % (len(name) - 1, name) in n:
+                assert k["vgpr_count"] <= 64, (n, k)
