@@ -16,9 +16,10 @@ def test_kernels_do_not_spill(kernels, family):  # noqa: F811
     assert not bad, bad
 
 
-def test_registers_leave_eight_wavefronts_a_simd(kernels):  # noqa: F811
-    """Memory-bound kernels with one step a wavefront in flight: 64 registers at most."""
-    for name in ("dropoutAddI", "dropoutAddBackwardI", "tokenLogprobRowsI", "tokenLogprobBackwardI"):
+def test_registers_leave_wavefronts_enough(kernels):  # noqa: F811
+    """Memory-bound kernels with one step a wavefront in flight: 8 wavefronts a SIMD (64 registers), 7 for rows of
+    narrow shards, whose threads look their shards up one by one."""
+    for name, most in (("dropoutAddI", 64), ("dropoutAddBackwardI", 64), ("tokenLogprobRowsI", 72), ("tokenLogprobBackwardI", 64)):
         for n, k in kernels.items():
             if "%d%s" % (len(name) - 1, name) in n:
-                assert k["vgpr_count"] <= 64, (n, k)
+                assert k["vgpr_count"] <= (64 if "ELi512E" in n else most), (n, k)
