@@ -752,7 +752,7 @@ arResult_t arDropoutAddBackwardWorkspace(const size_t* rows, int nranks, size_t 
  *  targets   (device) `rows` indices into the vocabulary.  A negative one marks
  *            a row that is ignored: its logits are not read, its logp, top and
  *            logSum are 0.  One past the vocabulary gives NaN.
- *  scale     finite, > 0: one over the sampling temperature.
+ *  scale     > 0, at most 2^127: one over the sampling temperature.
  *  logp      (device) `rows` floats.
  *  top, logSum  (device, each may be NULL) `rows` floats for
  *            arTokenLogprobBackward; scale * top + logSum is the logarithm of the
@@ -761,7 +761,8 @@ arResult_t arDropoutAddBackwardWorkspace(const size_t* rows, int nranks, size_t 
  *            arTokenLogprobWorkspace reports 0.
  * Masks: a logit of -inf, or of the type's lowest value beside ordinary ones,
  * has probability 0; logits that all have the lowest value are equally likely.
- * logp is -inf for such a target, and NaN where a row has a NaN or +inf
+ * Logits whose difference passes 3.4e38 are infinitely far apart.  logp is -inf
+ * for a target of probability 0 by its mask, and NaN where a row has a NaN or +inf
  * logit or nothing but -inf: then there is no distribution.
  * Outputs must not overlap any other buffer.
  * Errors: arInvalidArgument (nothing enqueued), arInvalidUsage in an open

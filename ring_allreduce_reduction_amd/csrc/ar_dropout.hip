@@ -154,9 +154,10 @@ __device__ __forceinline__ DropPlace placeOf(const DropArgs& a) {
 // Calls f(load, settle, store), how a thread's elements of a row come and go.
 // The 8 elements, or the fewer before a row's end, come with one load: at the
 // end it moves back to end with the row, so that all threads' loads go out
-// alike, and `settle` brings the elements to their places once they are there.
-// 2537 rows of 2047 fp16 backward 15.5 us with the last elements loaded one by
-// one, 12.2 so.  Rows of less than 8 elements are loaded one by one.
+// alike, and `settle` brings the elements to their places once they are there;
+// what it reads of its neighbour's, who may be writing them in place, is not
+// used.  2537 rows of 2047 fp16 backward 15.5 us with the last elements loaded
+// one by one, 12.2 so.  Rows of less than 8 elements are loaded one by one.
 template <typename E, typename F>
 __device__ __forceinline__ void withAccess(const DropPlace& at, int cols, F f) {
   typedef typename E::T T;
@@ -482,10 +483,15 @@ void fillDraw(DropArgs* a, double p, uint64_t seed, uint64_t offset, const uint6
   a->step = step;
 }
 
+// Ranks of a launch: its workgroups, one at least to a tile of each rank's
+// columns, have fewer than 2^32 threads.
+int dropRanks(size_t cols) { return cols <= (size_t)1 << 26 ? kOpRanks : 1; }
+
 // This launch's rows and their slices; returns the grid's slices.
 int fillDropRows(DropArgs* a, const size_t* rows, const uint64_t* firstRow, int nranks, int first, size_t cols,
                  bool sums) {
-  a->nranks = nranks - first < kOpRanks ? nranks - first : kOpRanks;
+  const int most = dropRanks(cols);
+  a->nranks = nranks - first < most ? nranks - first : most;
   uint64_t next = 0;
   for (int r = 0; r < first; ++r) next += rows[r];
   a->rowStart[0] = 0;
@@ -532,8 +538,7 @@ arResult_t dropForward(const void* const* x, const void* const* bias, const void
   DropArgs a{};
   fillDraw(&a, p, seed, offset, step);
   const size_t bytes = (size_t)s.total * cols * (size_t)esz * (residual ? 3 : 2);
-  for (int l = 0; l < s.launches; ++l) {
-    const int first = l * kOpRanks;
+  for (int first = 0; first < nranks; first += dropRanks(cols)) {
     const int slices = fillDropRows(&a, rows, firstRow, nranks, first, cols, false);
     if (slices == 0) continue;
     for (int r = 0; r < a.nranks; ++r) {
@@ -559,10 +564,11 @@ arResult_t dropWorkspace(const size_t* rows, int nranks, size_t cols, size_t* by
   if (bytes == nullptr || !shapeOk(rows, nranks, cols, &s)) return arInvalidArgument;
   const DropCut k = dropCut((int)cols, kDropBackBlock);
   size_t slices = 0;
-  for (int l = 0; l < s.launches; ++l) {
-    const int64_t n = rowsOfLaunch(rows, nranks, l * kOpRanks);
+  const int ranks = dropRanks(cols);
+  for (int first = 0; first < nranks; first += ranks) {
+    const int64_t n = rowsOfLaunch(rows, nranks, first, ranks);
     const int most = n > 0 ? dropSlices(n, k, true) : 0;
-    slices += (size_t)(most > 0 && most < kOpRanks ? kOpRanks : most);   // one at least for each rank with rows
+    slices += (size_t)(most > 0 && most < ranks ? ranks : most);   // one at least for each rank with rows
   }
   *bytes = (slices > 0 ? slices : 1) * ((cols + 7) / 8 * 8) * sizeof(float);
   return arSuccess;
@@ -606,8 +612,7 @@ arResult_t dropBackward(const void* const* dy, void* const* dx, void* const* dbi
   fillDraw(&a, p, seed, offset, step);
   int partials = 0;
   const size_t bytes = (size_t)s.total * cols * (size_t)esz * (dx ? 2 : 1);
-  for (int l = 0; l < s.launches; ++l) {
-    const int first = l * kOpRanks;
+  for (int first = 0; first < nranks; first += dropRanks(cols)) {
     const int slices = fillDropRows(&a, rows, firstRow, nranks, first, cols, true);
     if (slices == 0) continue;
     for (int r = 0; r < a.nranks; ++r) {
@@ -618,7 +623,7 @@ arResult_t dropBackward(const void* const* dy, void* const* dx, void* const* dbi
     a.xStride = (int64_t)dyStride;
     a.yStride = (int64_t)dxStride;
     a.stream = bytes > kDropStream;
-    if (dbias != nullptr && s.launches == 1 && s.total <= kFewRows) {
+    if (dbias != nullptr && nranks <= dropRanks(cols) && s.total <= kFewRows) {
       for (int r = 0; r < nranks; ++r) w.dbias[r] = dbias[r];
       return byTypes<DropBackwardFew, const DropFewArgs&, hipStream_t>(dtype, wtype, w, st) == hipSuccess ? arSuccess
                                                                                                           : arHipError;

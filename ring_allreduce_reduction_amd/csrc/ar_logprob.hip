@@ -63,9 +63,10 @@ __device__ __forceinline__ Running join(const Running& a, const Running& b, floa
 }
 
 // N more logits.  The exponents are scaleLog2e x less the largest's, `ref`, in
-// one rounding each; what ref itself was rounded by is taken off the sum.
-// Where ref would overflow (rows of nothing but the lowest value) differences
-// come first.
+// one rounding each; what ref itself was rounded by is taken off the sum to
+// first order, which up to 2^12 leaves 2^-26 of it.  Past that (large offsets,
+// rows of nothing but the lowest value) differences come first, an operation
+// more a logit.
 template <int N>
 __device__ __forceinline__ void meet(Running* run, const float (&f)[N], float c) {
   float top = run->top;
@@ -73,7 +74,7 @@ __device__ __forceinline__ void meet(Running* run, const float (&f)[N], float c)
   for (int e = 0; e < N; ++e) top = fmaxf(top, f[e]);
   const float base = baseOf(top), ref = base * c;
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (fabsf(ref) < 0x1p125f) {
+  if (fabsf(ref) <= 0x1p12f) {
 #pragma unroll
     for (int e = 0; e < N; ++e) s[e % 4] += __builtin_amdgcn_exp2f(fmaf(f[e], c, -ref));
     const float off = fmaf(base, c, -ref) * -kLn2;
@@ -243,7 +244,8 @@ __device__ __forceinline__ PieceAt pieceAt(const LpArgs& a) {
   return p;
 }
 
-// Few rows of a long vocabulary: a workgroup a piece of a row leaves the piece's running values; tokenLogprobJoin joins them.
+// Few rows of a long vocabulary: a workgroup a piece of a row leaves the
+// piece's running values; tokenLogprobJoin joins them.
 template <int DT>
 __global__ void __launch_bounds__(kLpBlock) tokenLogprobPieces(const LpArgs a) {
   typedef typename Elem<DT>::type T;
@@ -448,7 +450,8 @@ struct LpRows {
     // together; 500 x 2 x 30000 20, 14).
     if (a.nranks > 4) return launch<512, 512, kWave>(a, stream, st);
     if (a.nranks == 4) return launch<kLpBlock, kLpBlock, kWave>(a, stream, st);
-    if (all <= (int64_t)V * (a.rows < 1024 ? a.rows : 1024)) return launch<kLpBlock, kWave, kWave>(a, stream, st);
+    const int many = a.rows < 1024 ? a.rows : 1024;
+    if (all <= (int64_t)V * many) return launch<kLpBlock, kWave, kWave>(a, stream, st);
     if (a.nranks > 1 && columns <= 1024 * V) return launch<kLpBlock, kLpBlock, kWave>(a, stream, st);
     if (columns < 3 * 512 * V) return launch<kLpBlock, kLpBlock, kLpBlock>(a, stream, st);
     return launch<512, 512, 512>(a, stream, st);
@@ -485,7 +488,8 @@ struct LpBackward {
   }
 };
 
-bool scaleOk(float scale) { return scale > 0.0f && std::isfinite(scale); }
+// Up to where scale log2(e) is finite.
+bool scaleOk(float scale) { return scale > 0.0f && scale <= 0x1p127f; }
 
 arResult_t lpForward(const void* const* logits, const size_t* cols, const size_t* strides, int nranks, size_t rows,
                      const int64_t* targets, float scale, float* logp, float* top, float* logSum, int dtype,
@@ -581,7 +585,8 @@ arResult_t lpBackward(const float* dlogp, const void* const* logits, const size_
       a.dx[r] = cols[first + r] > 0 ? dlogits[first + r] : nullptr;
       a.dxStride[r] = (int64_t)(dstrides ? dstrides[first + r] : cols[first + r]);
     }
-    if (a.pieceStart[a.nranks] > 0 && byType<LpBackward, const LpArgs&, bool, hipStream_t>(dtype, a, bytes > kLpStream, st) != hipSuccess)
+    if (a.pieceStart[a.nranks] == 0) continue;
+    if (byType<LpBackward, const LpArgs&, bool, hipStream_t>(dtype, a, bytes > kLpStream, st) != hipSuccess)
       return arHipError;
   }
   return arSuccess;

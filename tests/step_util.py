@@ -24,11 +24,11 @@ def threshold(p):
     return int(math.floor(p * 65536.0 + 0.5))
 
 
-def drawn(rows, first, cols, seed, offset):
-    """The 16-bit numbers of rows first .. first + rows - 1, (rows, cols)."""
+def drawn(rows, first, cols, seed, offset, start=0):
+    """The 16-bit numbers of rows first .. first + rows - 1, columns start (a multiple of 8) and following."""
     groups = (cols + 7) // 8
     offset %= 1 << 64
-    g, r = np.meshgrid(np.arange(groups, dtype=np.uint64), np.arange(first, first + rows, dtype=np.uint64))
+    g, r = np.meshgrid(np.arange(start // 8, start // 8 + groups, dtype=np.uint64), np.arange(first, first + rows, dtype=np.uint64))
     words = philox([g, r, np.full_like(g, offset & 0xFFFFFFFF), np.full_like(g, offset >> 32)],
                    (seed & 0xFFFFFFFF, seed >> 32))
     out = np.stack([(w >> np.uint64(16 * h)) & np.uint64(0xFFFF) for w in words for h in (0, 1)], axis=2)
@@ -66,6 +66,7 @@ def logprob(x, targets, scale, ranks=1):
     logp = at - log_sum
     d_sum = ds * 1.01 + 3 * U * log_sum.abs() + U * U
     d_logp = d_sum + 3 * U * at.abs() + U * logp.abs()
+    logp = torch.where(logp.abs() >= 2.0 ** 128 * (1 - 2.0 ** -25), logp * float("inf"), logp)   # rounds to an infinity
     live = (targets >= 0)
     out = [torch.where(live, v[:, 0], 0.0) for v in (logp, top, log_sum, d_logp, d_sum)]
     return out

@@ -317,3 +317,29 @@ def test_wide_rows(B):
     kept = masks([1], cols, p, SEED, OFFSET)
     check_forward(run_forward(B, [x], None, None, p), [x], None, None, kept, p)
     check_backward(*run_backward(B, [x], torch.float32, p), [x], kept, p)
+
+
+@pytest.mark.parametrize("cols", [1 << 30, (1 << 26) + 5])
+def test_the_widest_rows_of_several_ranks(B, cols):
+    """Eight ranks' rows of 2^30 columns (more than 2^32 threads at 8 columns each), in place, and their sums; windows
+    at the ends and across 2^29."""
+    n, p, wide = 8, 0.5, 4096
+    xs = [torch.full((1, cols), r + 1.0, dtype=torch.bfloat16, device="cuda") for r in range(n)]
+    starts = [0, min(1 << 29, cols // 2 // 8 * 8), (cols - wide) // 8 * 8]
+    B.arDropoutAdd(xs, xs, p, SEED, OFFSET)
+    torch.cuda.synchronize()
+    for r in range(n):
+        for s in starts:
+            kept = su.drawn(1, r, min(wide, cols - s), SEED, OFFSET, s) >= su.threshold(p)
+            assert torch.equal(xs[r][:, s:s + wide].float().cpu(), torch.where(kept, 2.0 * (r + 1), 0.0)), (r, s)
+    few = xs[:2] if cols > 1 << 28 else xs
+    for x in xs:
+        x.fill_(1.0)
+    db = [torch.empty(cols, dtype=torch.bfloat16, device="cuda") for _ in few]
+    B.arDropoutAddBackward(few, few, p, SEED, OFFSET, None, db)
+    torch.cuda.synchronize()
+    for s in starts:
+        kept = [su.drawn(1, r, min(wide, cols - s), SEED, OFFSET, s) >= su.threshold(p) for r in range(len(few))]
+        want = torch.cat(kept).float().mul(2.0)
+        assert torch.equal(torch.cat([x[:, s:s + wide] for x in few]).float().cpu(), want)
+        assert torch.equal(db[0][s:s + wide].float().cpu(), want.sum(0)) and torch.equal(db[-1][s:s + wide], db[0][s:s + wide])

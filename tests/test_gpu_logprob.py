@@ -232,14 +232,15 @@ def test_far_logits(B, form, rows):
     for scale, shift in ((1.0, 1000.0), (1.0, -30000.0), (64.0, 0.0), (2.0 ** -10, 0.0)):
         far = [x + shift for x in xs]
         check_forward(run_forward(B, far, t, scale), far, t, scale)
-    big = [x * 1e37 for x in xs]
-    check_forward(run_forward(B, big, t, 1e-37), big, t, 1e-37)
+    for scale, size in ((1e-37, 1e37), (1.0, 1e30), (2.0 ** 127, 1.0)):
+        big = [x * size for x in xs]
+        check_forward(run_forward(B, big, t, scale), big, t, scale)
 
 
 @pytest.mark.parametrize("rows", [2, 1100])
 def test_equal_logits(B, form, rows):
     """Every token equally likely: logSum is ln n."""
-    for v in (0.0, 5.5, -65000.0):
+    for v in (0.0, 5.5, -65000.0, 2900.0, 1e30, -3e38, torch.finfo(torch.float32).max):
         xs = [torch.full((rows, c), v) for c in (1000, 24)]
         t = torch.arange(rows) % 1024
         logp, top, log_sum = run_forward(B, xs, t)
@@ -341,3 +342,19 @@ def test_no_rows(B):
     B.arTokenLogprob(x, t, e, e, e)
     B.arTokenLogprobBackward(e, x, t, e, e, x)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rows", [7, 1300])
+def test_column_slices_of_one_buffer(B, rows):
+    """The shards as slices of one wide logits tensor, the gradient in place."""
+    shards = [100, 37, 3, 250]
+    xs, t = inputs(rows, shards, torch.float16, 21)
+    wide = torch.cat(xs, 1).cuda()
+    views = list(wide.split(shards, 1))
+    logp, top, log_sum = (torch.full((rows,), NAN, device="cuda") for _ in range(3))
+    B.arTokenLogprob(views, t.cuda(), logp, top, log_sum)
+    d = gradients(rows, 22)
+    B.arTokenLogprobBackward(d.cuda(), views, t.cuda(), top, log_sum, views)
+    torch.cuda.synchronize()
+    check_forward((logp, top, log_sum), xs, t)
+    check_backward([v.contiguous() for v in views], d, xs, t, top.cpu(), log_sum.cpu())

@@ -39,7 +39,8 @@ def drop_back(B, **kw):
 
 
 def logprob(B, **kw):
-    a = dict(x=P(BASE), cols=N(16), strides=None, nranks=1, rows=4, t=2 * BASE, scale=1.0, logp=3 * BASE, top=4 * BASE,
+    """Few rows of a vocabulary long enough to need the workspace."""
+    a = dict(x=P(BASE), cols=N(40000), strides=None, nranks=1, rows=4, t=2 * BASE, scale=1.0, logp=3 * BASE, top=4 * BASE,
              ls=5 * BASE, dtype=B.arFloat32, ws=8 * BASE, wb=1 << 20)
     a.update(kw)
     return B.lib().arTokenLogprob(a["x"], a["cols"], a["strides"], a["nranks"], a["rows"], a["t"], a["scale"], a["logp"],
@@ -91,7 +92,7 @@ def test_dropout_refusals(B):
 def test_logprob_refusals(B):
     common = [dict(cols=None), dict(nranks=0), dict(nranks=129), dict(cols=N(0)), dict(cols=N((1 << 30) + 1)),
               dict(strides=N(15)), dict(strides=N((1 << 48) + 1)), dict(strides=N(1 << 47)), dict(rows=1 << 31),
-              dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(dtype=B.arInt32),
+              dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(scale=1.8e38), dict(dtype=B.arInt32),
               dict(dtype=7), dict(x=None), dict(x=P(0)), dict(x=P(BASE + 2)), dict(t=None), dict(t=2 * BASE + 4)]
     refused(logprob, B, common + [
         dict(logp=None), dict(logp=3 * BASE + 2), dict(top=4 * BASE + 1), dict(ls=5 * BASE + 3), dict(ws=None),
@@ -127,7 +128,7 @@ def test_workspaces(B):
     for args in ((None, 1, r), (N(4), 1, None), (N(4), 0, r), (N(1 << 31), 1, r)):
         assert L.arPolicyLossWorkspace(*args) == B.arInvalidArgument
     for rows in ([0], [1], [100], [1 << 30], [5] * 72):
-        for cols in (1, 33, 4096, 1 << 20):
+        for cols in (1, 33, 4096, 1 << 20, (1 << 26) + 1):
             n = B.arDropoutAddBackwardWorkspace(rows, cols)
             # at most 512 partial sums a column, or 16 a launch
             assert n % 16 == 0 and 4 * cols <= n <= 4 * (cols + 8) * max(512, 5 * 16)
