@@ -23,8 +23,7 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417
 
 struct LpArgs {
   const void* x[kOpRanks];
-  void* dx[kOpRanks];               // backward
-  int64_t xStride[kOpRanks], dxStride[kOpRanks];
+  int64_t xStride[kOpRanks];
   int64_t colStart[kOpRanks + 1];   // shard r holds columns [colStart[r], colStart[r + 1]) of the vocabulary
   int pieceStart[kOpRanks + 1];     // and pieces [pieceStart[r], pieceStart[r + 1]) of the launch
   int64_t vocabulary;               // the columns of every launch's shards
@@ -37,6 +36,12 @@ struct LpArgs {
   int parts;
   int rows, nranks;
   float scale, scaleLog2e;
+};
+
+struct LpBackArgs {
+  LpArgs call;
+  void* dx[kOpRanks];
+  int64_t dxStride[kOpRanks];
 };
 
 // A largest value and the sum of exp(scale (x - it)) of what was met.  Of
@@ -295,8 +300,9 @@ __global__ void __launch_bounds__(kWave) tokenLogprobJoin(const LpJoinArgs a) {
 
 // A workgroup takes a piece of kLpBlock / THREADS rows at a time.
 template <int DT, int THREADS, bool STREAM>
-__global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpArgs a) {
+__global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpBackArgs b) {
   typedef typename Elem<DT>::type T;
+  const LpArgs& a = b.call;
   constexpr int V = kVec<DT>, ROWS = kLpBlock / THREADS;
   typedef typename VecOf<T, V>::type Vec;
   const PieceAt p = pieceAt(a);
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpArgs a)
     const float d = a.dlogp[row] * a.scale, base = baseOf(a.top[row]), logSum = a.logSum[row] * kLog2e;
     const float g = t < 0 ? 0.0f : t < a.vocabulary || d == 0.0f ? d : NAN;
     const T* x = (const T*)a.x[p.rank] + row * a.xStride[p.rank];
-    T* dx = (T*)a.dx[p.rank] + row * a.dxStride[p.rank];
+    T* dx = (T*)b.dx[p.rank] + row * b.dxStride[p.rank];
     const Part part = partOf<T, V>(dx, p.from, p.to);
     const auto element = [&](float v, int64_t c) {
       const float q = __builtin_amdgcn_exp2f(fmaf(v - base, a.scaleLog2e, -logSum));
@@ -468,12 +474,13 @@ struct LpPieces {
 template <int DT>
 struct LpBackward {
   template <int THREADS>
-  static hipError_t launch(const LpArgs& a, bool stream, hipStream_t st) {
+  static hipError_t launch(const LpBackArgs& b, bool stream, hipStream_t st) {
     return launchKernel(stream ? tokenLogprobBackward<DT, THREADS, true> : tokenLogprobBackward<DT, THREADS, false>,
-                        pieceGrid(a, kLpBlock / THREADS), dim3(kLpBlock), a, st);
+                        pieceGrid(b.call, kLpBlock / THREADS), dim3(kLpBlock), b, st);
   }
-  static hipError_t run(const LpArgs& a, bool stream, hipStream_t st) {
+  static hipError_t run(const LpBackArgs& b, bool stream, hipStream_t st) {
     constexpr int V = kVec<DT>;
+    const LpArgs& a = b.call;
     int64_t widest = 0;   // of the launch's shards
     for (int r = 0; r < a.nranks; ++r) {
       const int64_t c = a.colStart[r + 1] - a.colStart[r];
@@ -482,9 +489,9 @@ struct LpBackward {
     // 8192 rows x 8 x 250 bf16: 15 us with 16 threads a row, 29 with 64, 92 with
     // 256; x 500 23, 30, 92; x 1000 43, 38, 93; x 2000 154, 100, 125; x 4000 243,
     // 188, 183.
-    if (widest <= 64 * V) return launch<16>(a, stream, st);
-    if (widest <= 256 * V) return launch<64>(a, stream, st);
-    return launch<kLpBlock>(a, stream, st);
+    if (widest <= 64 * V) return launch<16>(b, stream, st);
+    if (widest <= 256 * V) return launch<64>(b, stream, st);
+    return launch<kLpBlock>(b, stream, st);
   }
 };
 
@@ -568,7 +575,8 @@ arResult_t lpBackward(const float* dlogp, const void* const* logits, const size_
       ok = ok && addRows(v, logits[r], rows, cols[r], strides ? strides[r] : cols[r], esz, false, r) &&
            addRows(v, dlogits[r], rows, cols[r], dstrides ? dstrides[r] : cols[r], esz, true, r);
   if (!ok || outputsOverlap(v)) return arInvalidArgument;
-  LpArgs a{};
+  LpBackArgs b{};
+  LpArgs& a = b.call;
   a.targets = targets;
   a.dlogp = dlogp;
   a.top = const_cast<float*>(top);
@@ -582,11 +590,11 @@ arResult_t lpBackward(const float* dlogp, const void* const* logits, const size_
   for (int first = 0; first < nranks; first += kOpRanks) {
     fillShards(&a, logits, cols, strides, nranks, first, k.pieceCols);
     for (int r = 0; r < a.nranks; ++r) {
-      a.dx[r] = cols[first + r] > 0 ? dlogits[first + r] : nullptr;
-      a.dxStride[r] = (int64_t)(dstrides ? dstrides[first + r] : cols[first + r]);
+      b.dx[r] = cols[first + r] > 0 ? dlogits[first + r] : nullptr;
+      b.dxStride[r] = (int64_t)(dstrides ? dstrides[first + r] : cols[first + r]);
     }
     if (a.pieceStart[a.nranks] == 0) continue;
-    if (byType<LpBackward, const LpArgs&, bool, hipStream_t>(dtype, a, bytes > kLpStream, st) != hipSuccess)
+    if (byType<LpBackward, const LpBackArgs&, bool, hipStream_t>(dtype, b, bytes > kLpStream, st) != hipSuccess)
       return arHipError;
   }
   return arSuccess;

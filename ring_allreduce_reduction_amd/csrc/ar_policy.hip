@@ -37,12 +37,8 @@ constexpr int kPolFewEach = 5;
 // ranks leave of their last ones.
 constexpr int kPolFew = kPolFewBlock * kPolFewEach - kOpRanks * kWave;
 
-struct PolArgs {
-  const float* logp[kOpRanks];
-  const float* old[kOpRanks];
-  const float* ref[kOpRanks];          // null pointers: no KL term
-  const float* advantage[kOpRanks];
-  const float* weight[kOpRanks];       // null pointers: 1
+// What both passes need; the second one no more.
+struct PolCall {
   float* dlogp[kOpRanks];              // null pointers: not wanted
   int start[kOpRanks + 1];             // rank r has tokens [start[r], start[r + 1]) of the launch
   int blockStart[kOpRanks + 1];        // and workgroups [blockStart[r], blockStart[r + 1])
@@ -50,10 +46,18 @@ struct PolArgs {
   int partials;                        // of all launches
   double* partial;                     // kPolSums rows of `partials`; the first pass: from this launch's first
   float* stats;                        // where the launch writes them, or null
-  double logLow, logHigh;              // log(1 - low), log(1 + high)
-  float low, high;                     // 1 - low, 1 + high
   double klCoef, denominator, gradScale;
   double over;                         // what the sums are divided by, where the host knows it; else 0
+};
+
+struct PolArgs : PolCall {
+  const float* logp[kOpRanks];
+  const float* old[kOpRanks];
+  const float* ref[kOpRanks];          // null pointers: no KL term
+  const float* advantage[kOpRanks];
+  const float* weight[kOpRanks];       // null pointers: 1
+  double logLow, logHigh;              // log(1 - low), log(1 + high)
+  float low, high;                     // 1 - low, 1 + high
 };
 
 struct Token {
@@ -140,12 +144,12 @@ __device__ __forceinline__ float addToken(const PolArgs& a, float logp, float ol
   return counts ? weight * t.dlogp : 0.0f;
 }
 
-__device__ __forceinline__ double partOf(const PolArgs& a, double weights) {
+__device__ __forceinline__ double partOf(const PolCall& a, double weights) {
   const double over = a.denominator > 0.0 ? a.denominator : weights;
   return over != 0.0 ? 1.0 / over : 0.0;
 }
 
-__device__ __forceinline__ void putStats(const PolArgs& a, const double (&s)[kPolSums]) {
+__device__ __forceinline__ void putStats(const PolCall& a, const double (&s)[kPolSums]) {
   const double part = partOf(a, s[0]), policy = s[1] * part, kl = s[2] * part;
   a.stats[0] = (float)(policy + a.klCoef * kl);
   a.stats[1] = (float)policy;
@@ -167,7 +171,7 @@ struct PolPlace {
   int64_t first, step;
 };
 
-__device__ __forceinline__ PolPlace polPlace(const PolArgs& a) {
+__device__ __forceinline__ PolPlace polPlace(const PolCall& a) {
   PolPlace p;
   p.rank = 0;
   while ((int)blockIdx.x >= a.blockStart[p.rank + 1]) ++p.rank;
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(kPolBlock) policySums(const PolArgs a) {
 
 // The sums of the first pass in one order for every workgroup, and what they
 // are needed for: the stats, and each gradient's factor.
-__global__ void __launch_bounds__(kPolBlock) policyGrad(const PolArgs a) {
+__global__ void __launch_bounds__(kPolBlock) policyGrad(const PolCall a) {
   __shared__ double lds[kPolBlock / kWave], ldsAll[kPolBlock / kWave][kPolSums];
   typedef FloatVec<kPolVec> Vec;
   // a thread's first gradients are on their way while the sums are joined
@@ -411,7 +415,7 @@ arResult_t policyLoss(const float* const* logp, const float* const* old, const f
     a.stats = l == 0 ? stats : nullptr;
     const int grid = unscaled != nullptr ? a.blockStart[a.nranks] : 0;
     if (grid == 0 && l > 0) continue;
-    if (launchKernel(policyGrad, dim3(grid > 0 ? grid : 1), dim3(kPolBlock), a, st) != hipSuccess) return arHipError;
+    if (launchKernel<PolCall>(policyGrad, dim3(grid > 0 ? grid : 1), dim3(kPolBlock), a, st) != hipSuccess) return arHipError;
   }
   return arSuccess;
 }
