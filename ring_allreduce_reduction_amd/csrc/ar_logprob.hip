@@ -82,14 +82,14 @@ __device__ __forceinline__ void meet(Running* run, const float (&f)[N], float c)
   if (fabsf(ref) <= 0x1p12f) {
 #pragma unroll
     for (int e = 0; e < N; ++e) s[e % 4] += __builtin_amdgcn_exp2f(fmaf(f[e], c, -ref));
-    const float off = fmaf(base, c, -ref) * -kLn2;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) s[k] = fmaf(s[k], off, s[k]);
+    s[0] = (s[0] + s[1]) + (s[2] + s[3]);
+    s[0] = fmaf(s[0], fmaf(base, c, -ref) * -kLn2, s[0]);
   } else {
 #pragma unroll
     for (int e = 0; e < N; ++e) s[e % 4] += expOf(f[e], base, c);
+    s[0] = (s[0] + s[1]) + (s[2] + s[3]);
   }
-  run->sum = fmaf(run->sum, expOf(run->top, base, c), (s[0] + s[1]) + (s[2] + s[3]));
+  run->sum = fmaf(run->sum, expOf(run->top, base, c), s[0]);
   run->top = top;
 }
 
@@ -103,12 +103,12 @@ __device__ __forceinline__ typename VecOf<T, V>::type loadAs(const T* p) {
 // start at 16 bytes of `p`, the row, and the few elements around them one a
 // thread.
 struct Part {
-  int64_t from, first, last, to;
+  int from, first, last, to;
 };
 
 template <typename T, int V>
-__device__ __forceinline__ Part partOf(const T* p, int64_t from, int64_t to) {
-  const int64_t first = from + (int64_t)((0 - (uintptr_t)(p + from)) % 16 / sizeof(T));
+__device__ __forceinline__ Part partOf(const T* p, int from, int to) {
+  const int first = from + (int)((0 - (uintptr_t)(p + from)) % 16 / sizeof(T));
   if (first >= to) return Part{from, to, to, to};
   return Part{from, first, first + (to - first) / V * V, to};
 }
@@ -117,23 +117,23 @@ __device__ __forceinline__ Part partOf(const T* p, int64_t from, int64_t to) {
 // for its one of the rest.  `thread` counts from 0 among those that share p.
 template <int V, int STEP, typename F, typename G>
 __device__ __forceinline__ void forPart(const Part& p, int thread, F f, G g) {
-  for (int64_t c = p.first + thread * V; c < p.last; c += STEP) f(c);
-  const int64_t head = p.first - p.from, rest = head + (p.to - p.last);   // at most 2 (V - 1)
+  for (int c = p.first + thread * V; c < p.last; c += STEP) f(c);
+  const int head = p.first - p.from, rest = head + (p.to - p.last);   // at most 2 (V - 1)
   if (thread < rest) g(thread < head ? p.from + thread : p.last + (thread - head));
 }
 
 // THREADS threads' part of a shard's row: four vectors a thread in flight, -inf
 // past the last one.
 template <int DT, int THREADS, bool STREAM>
-__device__ __forceinline__ void meetColumns(Running* run, int thread, const typename Elem<DT>::type* x, int64_t from,
-                                            int64_t to, float c) {
+__device__ __forceinline__ void meetColumns(Running* run, int thread, const typename Elem<DT>::type* x, int from, int to,
+                                            float c) {
   typedef typename Elem<DT>::type T;
   constexpr int V = kVec<DT>;
   typedef typename VecOf<T, V>::type Vec;
   const Part part = partOf<T, V>(x, from, to);
   forPart<V, THREADS * V * kLpVecs>(
       part, thread,
-      [&](int64_t i) {
+      [&](int i) {
         Vec v[kLpVecs];
 #pragma unroll
         for (int k = 0; k < kLpVecs; ++k) {
@@ -145,7 +145,7 @@ __device__ __forceinline__ void meetColumns(Running* run, int thread, const type
         for (int e = 0; e < V * kLpVecs; ++e) f[e] = (float)v[e / V][e % V];
         meet(run, f, c);
       },
-      [&](int64_t i) {
+      [&](int i) {
         const float f[1] = {(float)x[i]};
         meet(run, f, c);
       });
@@ -154,11 +154,10 @@ __device__ __forceinline__ void meetColumns(Running* run, int thread, const type
 // Over THREADS threads of a workgroup side by side; the first one receives it.
 template <int THREADS>
 __device__ __forceinline__ Running joinThreads(Running run, float c, Running* lds) {
-#pragma unroll
-  for (int m = 1; m < kWave && m < THREADS; m *= 2) {
-    const Running other = {__shfl_xor(run.top, m), __shfl_xor(run.sum, m)};
-    run = join(run, other, c);
-  }
+  constexpr int LANES = THREADS < kWave ? THREADS : kWave;
+  const float top = laneMax<LANES>(run.top);
+  run.sum = laneSum<LANES>(run.sum * expOf(run.top, baseOf(top), c));
+  run.top = top;
   if (THREADS <= kWave) return run;
   __syncthreads();   // lds may still be read from the row before
   if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = run;
@@ -223,7 +222,7 @@ __global__ void __launch_bounds__(BLOCK) tokenLogprobRows(const LpArgs a) {
     Running run = nothing();
     for (int r = shard; r < a.nranks; r += ROW / SHARD)
       meetColumns<DT, SHARD, STREAM>(&run, thread, (const T*)a.x[r] + row * a.xStride[r], 0,
-                                     a.colStart[r + 1] - a.colStart[r], a.scaleLog2e);
+                                     (int)(a.colStart[r + 1] - a.colStart[r]), a.scaleLog2e);
     run = joinThreads<ROW>(run, a.scaleLog2e, lds);
     if (first && a.partial) putPart(a, row, t, run, logit);
     else if (first) putRow(a, row, run, logit);
@@ -233,8 +232,7 @@ __global__ void __launch_bounds__(BLOCK) tokenLogprobRows(const LpArgs a) {
 // A workgroup's piece of its shard: shard r's columns cut into as many equal
 // parts (but for 16 columns) as it has pieces.
 struct PieceAt {
-  int rank;
-  int64_t from, to;
+  int rank, from, to;
 };
 
 __device__ __forceinline__ PieceAt pieceAt(const LpArgs& a) {
@@ -244,8 +242,8 @@ __device__ __forceinline__ PieceAt pieceAt(const LpArgs& a) {
   const unsigned pieces = a.pieceStart[p.rank + 1] - a.pieceStart[p.rank], piece = blockIdx.x - a.pieceStart[p.rank];
   const unsigned cols = (unsigned)(a.colStart[p.rank + 1] - a.colStart[p.rank]);
   const unsigned each = ((cols + pieces - 1) / pieces + 15) / 16 * 16;
-  p.from = (int64_t)each * piece < cols ? (int64_t)each * piece : cols;
-  p.to = p.from + each < cols ? p.from + each : cols;
+  p.from = (int)((uint64_t)each * piece < cols ? each * piece : cols);
+  p.to = (int)(p.from + each < cols ? p.from + each : cols);
   return p;
 }
 
@@ -313,30 +311,31 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpBackArg
   };
   for (int64_t row = (int64_t)blockIdx.y * ROWS + (ROWS > 1 ? threadIdx.x / THREADS : 0); row < a.rows;
        row += (int64_t)gridDim.y * ROWS) {
-    const int64_t t = a.targets[row], at = t - a.colStart[p.rank];
+    const int64_t t = a.targets[row], place = t - a.colStart[p.rank];
+    const int at = place >= 0 && place < p.to ? (int)place : -1;   // the target's column here
     const float d = a.dlogp[row] * a.scale, base = baseOf(a.top[row]), logSum = a.logSum[row] * kLog2e;
     const float g = t < 0 ? 0.0f : t < a.vocabulary || d == 0.0f ? d : NAN;
     const T* x = (const T*)a.x[p.rank] + row * a.xStride[p.rank];
     T* dx = (T*)b.dx[p.rank] + row * b.dxStride[p.rank];
     const Part part = partOf<T, V>(dx, p.from, p.to);
-    const auto element = [&](float v, int64_t c) {
+    const auto element = [&](float v, int c) {
       const float q = __builtin_amdgcn_exp2f(fmaf(v - base, a.scaleLog2e, -logSum));
       return (T)(g * ((c == at ? 1.0f : 0.0f) - q));
     };
     if (g == 0.0f)
       forPart<V, THREADS * V>(
-          part, thread, [&](int64_t c) { store(dx + c, (Vec)(T)0.0f); }, [&](int64_t c) { dx[c] = (T)0.0f; });
+          part, thread, [&](int c) { store(dx + c, (Vec)(T)0.0f); }, [&](int c) { dx[c] = (T)0.0f; });
     else
       forPart<V, THREADS * V>(
           part, thread,
-          [&](int64_t c) {
+          [&](int c) {
             const Vec v = loadAs<T, V, STREAM>(x + c);
             Vec out;
 #pragma unroll
             for (int e = 0; e < V; ++e) out[e] = element((float)v[e], c + e);
             store(dx + c, out);
           },
-          [&](int64_t c) { dx[c] = element((float)x[c], c); });
+          [&](int c) { dx[c] = element((float)x[c], c); });
   }
 }
 

@@ -107,6 +107,29 @@ __device__ __forceinline__ float laneSum(float v) {
 
 __device__ __forceinline__ float waveSum(float v) { return laneSum<64>(v); }
 
+// The larger of v and what lane permutation CTRL brings, in the rows of ROWS;
+// lanes that it brings nothing keep v.
+template <int CTRL, int ROWS = 0xf>
+__device__ __forceinline__ float maxDpp(float v) {
+  const int bits = __builtin_bit_cast(int, v);
+  return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(bits, bits, CTRL, ROWS, 0xf, false)));
+}
+
+// Largest value of a wavefront or its parts of 16; every lane receives its own
+// part's.  A NaN is passed over.
+template <int LANES>
+__device__ __forceinline__ float laneMax(float v) {
+  static_assert(LANES == 16 || LANES == 64, "parts of a wavefront");
+  v = maxDpp<0xb1>(v);
+  v = maxDpp<0x4e>(v);
+  v = maxDpp<0x141>(v);
+  v = maxDpp<0x140>(v);
+  if (LANES == 16) return v;
+  v = maxDpp<0x142, 0xa>(v);
+  v = maxDpp<0x143, 0xc>(v);
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
 // The sum of N slices' values in eight chains, joined in pairs: an eighth of the
 // roundings of one chain.
 template <int N, typename F>
