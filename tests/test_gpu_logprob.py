@@ -138,9 +138,15 @@ def test_padded_rows_odd_addresses_in_place(B, form, rows, dt):
 
 
 @pytest.mark.parametrize("rows", [5, 1100])
-def test_logp_alone(B, form, rows):
+def test_logp_alone_and_with_one_statistic(B, form, rows):
     xs, t = inputs(rows, [300, 20], torch.bfloat16, 4)
     check_forward(run_forward(B, xs, t, stats=False), xs, t)
+    whole = run_forward(B, xs, t)
+    for k in (1, 2):
+        out = [torch.full((rows,), NAN, device="cuda") for _ in range(2)]
+        B.arTokenLogprob(on_device(xs, 0, 0), t.cuda(), out[0], *[out[1] if i == k else None for i in (1, 2)])
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], whole[0]) and torch.equal(out[1], whole[k])
 
 
 @pytest.mark.parametrize("rows", [8, 1104])

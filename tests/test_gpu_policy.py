@@ -217,3 +217,17 @@ def test_two_streams(B):
     torch.cuda.synchronize()
     for data, _, out, stats, _, _ in sets:
         check((stats, out), data)
+
+
+def test_as_many_tokens_as_there_may_be(B):
+    """2^31 - 1 tokens of one rank: every token alike, so that the sums are exact."""
+    n = (1 << 31) - 1
+    zeros, ones = torch.zeros(n, device="cuda"), torch.ones(n, device="cuda")
+    out, stats = torch.full((n,), NAN, device="cuda"), torch.empty(5, device="cuda")
+    for weights in (None, [ones]):
+        out.fill_(NAN)
+        B.arPolicyLoss([zeros], [zeros], [ones], stats, weights=weights, dlogps=[out])
+        torch.cuda.synchronize()
+        assert stats.tolist() == [-1.0, -1.0, 0.0, 0.0, float(torch.tensor(float(n)))]
+        want = torch.tensor(-1.0 / n, dtype=torch.float64).float().item()
+        assert out.min().item() == want and out.max().item() == want
