@@ -1,5 +1,5 @@
 // ar_ops.h -- element types and small reductions shared by the operator
-// kernels (layer norm, gradient norm and clipping).
+// kernels.
 #pragma once
 
 #include <hip/hip_runtime.h>
