@@ -411,12 +411,19 @@ DropCut dropCut(int cols, int block) {
 // and read, so it has 32 rows at least (2537 rows of 2047 11.8 us; 16 rows 11.7,
 // 64 13.2; of 2048 11.0, 11.3, 11.3) and there are at most two a CU (160000 rows
 // of 100 21 us, 23 with four, 28 with eight, 44 with 20; of 512 66, 69, 68, 78).
+// Where up to half of the CUs would have a workgroup more than the others, its
+// rows are shared out among them all (312 workgroups 11.9 us, as 256 11.1; 580
+// 14.3, as 512 13.1; but 453 13.4, as 256 14.1), with tiles few enough to come near.
 int dropSlices(int64_t rows, const DropCut& k, bool sums) {
   const int64_t once = (int64_t)1 << k.rowsLog, each = sums && once < 32 ? 32 : once;
   int64_t most = (sums ? 32 : 256) * kOpsCUs / k.tiles;
   const int64_t full = (rows + each - 1) / each;
   if (sums && most > 2 * kOpsCUs) most = 2 * kOpsCUs;
-  return (int)(full < most ? full : most < 1 ? 1 : most);
+  int64_t n = full < most ? full : most < 1 ? 1 : most;
+  const int64_t grid = n * k.tiles;
+  if (sums && k.tiles <= kOpsCUs / 8 && grid > kOpsCUs && grid % kOpsCUs <= kOpsCUs / 2)
+    n = grid / kOpsCUs * kOpsCUs / k.tiles;
+  return (int)n;
 }
 
 // Calls that move more than the caches hold load and store past them: 8 x 4096
