@@ -25,16 +25,20 @@ namespace {
 
 constexpr int kPolBlock = 256;
 constexpr int kPolSums = 4;            // weights, weighted loss, kl, clipped tokens
-// Workgroups, and partial sums, of a launch's first pass at most: 8 x 262144
-// tokens 18.2 us with 2 a CU, 18.3 with 4, 21.9 with 8, whose sums cost as much
-// as their tokens; 8 x 100000 10.8, 11.2, 12.0.  Two vectors a thread in flight
-// 19.6; the second pass, which takes as many, gained nothing from 4 or 8.
-constexpr int kPolGrid = 2 * kOpsCUs;
+// Workgroups, and partial sums, of a launch at most, and where they do with a
+// vector a thread: 8 x 262144 tokens 16.9 us with 2 a CU, 20.2 with 1, 17.7 with
+// 4, 20.9 with 8, whose sums cost as much as their tokens; 8 x 100000 10.2, 11.4,
+// 9.4 and 9.4.  Two vectors a thread in flight in the first pass cost a tenth.
+constexpr int kPolGrid = 2 * kOpsCUs, kPolOnce = 4 * kOpsCUs;
 constexpr int kPolVec = 4;             // tokens of a thread at a time
+// Vectors of a thread that the second pass has on their way while it joins the
+// sums: with one 17.7 us, with two 17.1, with eight 17.0.
+constexpr int kPolAhead = 4;
 constexpr int kPolFewBlock = 1024;
 constexpr int kPolFewEach = 5;
 // Tokens of one workgroup's launch: its wavefronts' parts of 64, less what the
-// ranks leave of their last ones.
+// ranks leave of their last ones.  8 x 64 tokens 3.8 us (6.6 in two launches), x
+// 256 5.0 (6.4), x 512 6.3 (6.6); 6000 of one rank 7.6 (6.2).
 constexpr int kPolFew = kPolFewBlock * kPolFewEach - kOpRanks * kWave;
 
 // What both passes need; the second one no more.
@@ -56,9 +60,12 @@ struct PolArgs : PolCall {
   const float* ref[kOpRanks];          // null pointers: no KL term
   const float* advantage[kOpRanks];
   const float* weight[kOpRanks];       // null pointers: 1
+  bool hasRef;
   double logLow, logHigh;              // log(1 - low), log(1 + high)
   float low, high;                     // 1 - low, 1 + high
 };
+
+typedef int Halves __attribute__((ext_vector_type(2)));   // of 64 bits
 
 struct Token {
   float loss, kl, dlogp;
@@ -99,35 +106,72 @@ __device__ __forceinline__ Token tokenOf(const PolArgs& a, float logp, float old
   return t;
 }
 
-// Sums over a workgroup; every thread receives them.
-template <int BLOCK>
-__device__ __forceinline__ double blockSum64(double s, double* lds) {
-#pragma unroll
-  for (int m = 1; m < kWave; m *= 2) s += __shfl_xor(s, m);
-  if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = s;
-  __syncthreads();
-  s = lds[0];
-  for (int w = 1; w < BLOCK / kWave; ++w) s += lds[w];
-  return s;
+// What lane permutation CTRL brings.
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v) {
+  const auto b = __builtin_bit_cast(Halves, v);
+  return __builtin_bit_cast(double, Halves{__builtin_amdgcn_update_dpp(0, b[0], CTRL, 0xf, 0xf, true),
+                                           __builtin_amdgcn_update_dpp(0, b[1], CTRL, 0xf, 0xf, true)});
 }
 
-// Four sums at once: neighbours hand each other the halves they do not keep, so
-// that after two steps a lane holds one of the four and 7 exchanges do for 24.
-template <int BLOCK>
-__device__ __forceinline__ void blockSums(double (&s)[kPolSums], double (*lds)[kPolSums]) {
-  const bool odd = threadIdx.x & 1, second = threadIdx.x & 2;
-  const double a = (odd ? s[2] : s[0]) + __shfl_xor(odd ? s[0] : s[2], 1);
-  const double b = (odd ? s[3] : s[1]) + __shfl_xor(odd ? s[1] : s[3], 1);
-  double v = (second ? b : a) + __shfl_xor(second ? a : b, 2);
-#pragma unroll
-  for (int m = 4; m < kWave; m *= 2) v += __shfl_xor(v, m);
-  if (threadIdx.x % kWave < kPolSums) lds[threadIdx.x / kWave][(odd ? 2 : 0) + (second ? 1 : 0)] = v;
+// v plus that of the lane 16 (ROWS) or 32 further on, modulo twice as much.
+template <bool ROWS>
+__device__ __forceinline__ double addHalves(double v) {
+  const auto b = __builtin_bit_cast(Halves, v);
+  const auto swap = [](int h) {
+    return ROWS ? __builtin_amdgcn_permlane16_swap(h, h, false, false)
+                : __builtin_amdgcn_permlane32_swap(h, h, false, false);
+  };
+  const auto low = swap(b[0]), high = swap(b[1]);
+  return __builtin_bit_cast(double, Halves{(int)low[0], (int)high[0]}) +
+         __builtin_bit_cast(double, Halves{(int)low[1], (int)high[1]});
+}
+
+// Sum over those of LANES lanes side by side whose index agrees modulo 4; each
+// receives its own, the same in all of them.
+template <int LANES>
+__device__ __forceinline__ double sumFourths(double v) {
+  static_assert(LANES == 16 || LANES == 64, "a row or a wavefront");
+  v += dpp64<0x128>(v);   // row_ror 8
+  v += dpp64<0x124>(v);   // row_ror 4
+  return LANES == 16 ? v : addHalves<false>(addHalves<true>(v));
+}
+
+// Sum over quads; each of their lanes receives it.
+__device__ __forceinline__ double sumQuad(double v) {
+  v += dpp64<0xb1>(v);          // quad_perm 1,0,3,2
+  return v + dpp64<0x4e>(v);    // quad_perm 2,3,0,1
+}
+
+// Sum over a workgroup of four wavefronts; every thread receives it.
+__device__ __forceinline__ double blockSum64(double s, double (&lds)[4]) {
+  s = sumFourths<kWave>(sumQuad(s));
+  if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = s;
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kPolSums; ++k) {
-    s[k] = lds[0][k];
-    for (int w = 1; w < BLOCK / kWave; ++w) s[k] += lds[w][k];
-  }
+  return sumQuad(lds[threadIdx.x % 4]);
+}
+
+// Four sums over a workgroup of 4 or 16 wavefronts; thread i receives number
+// i % 4.  Neighbours hand each other what they do not keep, so that after two
+// steps a lane holds one of the four; the wavefronts' are read one a lane.
+template <int BLOCK>
+__device__ __forceinline__ double blockSums(const double (&s)[kPolSums], double (&lds)[BLOCK / kWave * kPolSums]) {
+  static_assert(kPolSums == 4, "one a lane of a quad");
+  const bool odd = threadIdx.x & 1, second = threadIdx.x & 2;
+  const double a = (odd ? s[1] : s[0]) + dpp64<0xb1>(odd ? s[0] : s[1]);
+  const double b = (odd ? s[3] : s[2]) + dpp64<0xb1>(odd ? s[2] : s[3]);
+  const double v = sumFourths<kWave>((second ? b : a) + dpp64<0x4e>(second ? a : b));
+  const int lane = (int)threadIdx.x % kWave;
+  if (lane < kPolSums) lds[threadIdx.x / kWave * kPolSums + lane] = v;
+  __syncthreads();
+  constexpr int ALL = BLOCK / kWave * kPolSums;
+  return sumFourths<ALL>(lds[threadIdx.x % ALL]);
+}
+
+// What lane `lane` of the wavefront holds.
+__device__ __forceinline__ double laneOf(double v, int lane) {
+  const auto b = __builtin_bit_cast(Halves, v);
+  return __builtin_bit_cast(double, Halves{__builtin_amdgcn_readlane(b[0], lane), __builtin_amdgcn_readlane(b[1], lane)});
 }
 
 // Adds a token up and returns its gradient short of the common factor.  One of
@@ -149,13 +193,16 @@ __device__ __forceinline__ double partOf(const PolCall& a, double weights) {
   return over != 0.0 ? 1.0 / over : 0.0;
 }
 
-__device__ __forceinline__ void putStats(const PolCall& a, const double (&s)[kPolSums]) {
-  const double part = partOf(a, s[0]), policy = s[1] * part, kl = s[2] * part;
+// Called by the workgroup's threads with what blockSums gave them.
+__device__ __forceinline__ void putStats(const PolCall& a, double sums) {
+  const double weights = laneOf(sums, 0), loss = laneOf(sums, 1), klSum = laneOf(sums, 2), clipped = laneOf(sums, 3);
+  if (threadIdx.x > 0) return;
+  const double part = partOf(a, weights), policy = loss * part, kl = klSum * part;
   a.stats[0] = (float)(policy + a.klCoef * kl);
   a.stats[1] = (float)policy;
   a.stats[2] = (float)kl;
-  a.stats[3] = (float)(s[3] * part);
-  a.stats[4] = (float)s[0];
+  a.stats[3] = (float)(clipped * part);
+  a.stats[4] = (float)weights;
 }
 
 // A gradient and the factor it was short of; 0 where nothing counts, whatever
@@ -183,18 +230,18 @@ __device__ __forceinline__ PolPlace polPlace(const PolCall& a) {
   return p;
 }
 
-// Calls f(first token) for a thread's vectors, then g(token) for its part of
+// Calls f(first token) for a thread's vectors but the first `done`, then g(token) for its part of
 // the rest, which the rank's first workgroup takes.
 template <typename F, typename G>
-__device__ __forceinline__ void forTokens(const PolPlace& p, F f, G g) {
-  int64_t i = p.first;
+__device__ __forceinline__ void forTokens(const PolPlace& p, int done, F f, G g) {
+  int64_t i = p.first + done * p.step;
   for (; i < p.whole; i += p.step) f(i);
   i = p.whole + p.first / kPolVec;
   if (i < p.count) g(i);
 }
 
 __global__ void __launch_bounds__(kPolBlock) policySums(const PolArgs a) {
-  __shared__ double lds[kPolBlock / kWave][kPolSums];
+  __shared__ double lds[kPolBlock / kWave * kPolSums];
   const PolPlace at = polPlace(a);
   const float *logp = a.logp[at.rank], *old = a.old[at.rank], *ref = a.ref[at.rank];
   const float *advantage = a.advantage[at.rank], *weight = a.weight[at.rank];
@@ -204,7 +251,7 @@ __global__ void __launch_bounds__(kPolBlock) policySums(const PolArgs a) {
   const bool known = a.over > 0.0;
   const double factor = known ? a.gradScale / a.over : 1.0;
   forTokens(
-      at,
+      at, 0,
       [&](int64_t i) {
         const Vec l = loadVec<float, kPolVec>(logp + i), o = loadVec<float, kPolVec>(old + i);
         const Vec v = loadVec<float, kPolVec>(advantage + i);
@@ -223,45 +270,48 @@ __global__ void __launch_bounds__(kPolBlock) policySums(const PolArgs a) {
                                  weight ? weight[i] : 1.0f, s);
         if (dlogp) dlogp[i] = known ? timesFactor(d, factor) : d;
       });
-  blockSums<kPolBlock>(s, lds);
-  if (threadIdx.x == 0)
-#pragma unroll
-    for (int k = 0; k < kPolSums; ++k) a.partial[(size_t)k * a.partials + blockIdx.x] = s[k];
+  const double sums = blockSums<kPolBlock>(s, lds);
+  if (threadIdx.x < kPolSums) a.partial[(size_t)threadIdx.x * a.partials + blockIdx.x] = sums;
 }
 
-// The sums of the first pass in one order for every workgroup, and what they
-// are needed for: the stats, and each gradient's factor.
+// The sums of the first pass in one order for every workgroup: what each
+// gradient's factor needs of them, and, where the launch writes the stats, all
+// of them in its last workgroup, which has no tokens.
 __global__ void __launch_bounds__(kPolBlock) policyGrad(const PolCall a) {
-  __shared__ double lds[kPolBlock / kWave], ldsAll[kPolBlock / kWave][kPolSums];
   typedef FloatVec<kPolVec> Vec;
-  // a thread's first gradients are on their way while the sums are joined
-  const bool any = a.start[a.nranks] > 0;   // else a launch for the stats alone
-  PolPlace at{};
-  if (any) at = polPlace(a);
-  float* dlogp = any ? a.dlogp[at.rank] : nullptr;
-  Vec ahead = (Vec)0.0f;
-  if (dlogp && at.first < at.whole) ahead = loadVec<float, kPolVec>(dlogp + at.first);
-  double weights = 0.0;
-  for (int i = threadIdx.x; i < a.partials; i += kPolBlock) weights += a.partial[i];
-  weights = blockSum64<kPolBlock>(weights, lds);
-  if (a.stats && blockIdx.x == 0) {
+  if (a.stats && blockIdx.x == gridDim.x - 1) {
+    __shared__ double lds[kPolBlock / kWave * kPolSums];
     double s[kPolSums] = {0.0, 0.0, 0.0, 0.0};
     for (int i = threadIdx.x; i < a.partials; i += kPolBlock)
 #pragma unroll
       for (int k = 0; k < kPolSums; ++k) s[k] += a.partial[(size_t)k * a.partials + i];
-    blockSums<kPolBlock>(s, ldsAll);
-    if (threadIdx.x == 0) putStats(a, s);
+    putStats(a, blockSums<kPolBlock>(s, lds));
+    return;
   }
-  if (dlogp == nullptr) return;
-  const double factor = a.gradScale * partOf(a, weights);
-  forTokens(
-      at,
-      [&](int64_t i) {
-        Vec d = i == at.first ? ahead : loadVec<float, kPolVec>(dlogp + i);
+  __shared__ double lds[kPolBlock / kWave];
+  const PolPlace at = polPlace(a);
+  float* dlogp = a.dlogp[at.rank];
+  // a thread's first gradients are on their way while the sums are joined
+  Vec ahead[kPolAhead];
 #pragma unroll
-        for (int e = 0; e < kPolVec; ++e) d[e] = timesFactor(d[e], factor);
-        storeVec<float, kPolVec>(dlogp + i, d);
-      },
+  for (int k = 0; k < kPolAhead; ++k) {
+    ahead[k] = (Vec)0.0f;
+    if (at.first + k * at.step < at.whole) ahead[k] = loadVec<float, kPolVec>(dlogp + at.first + k * at.step);
+  }
+  double weights = 0.0;
+  for (int i = threadIdx.x; i < a.partials; i += kPolBlock) weights += a.partial[i];
+  weights = blockSum64(weights, lds);
+  const double factor = a.gradScale * partOf(a, weights);
+  const auto put = [&](int64_t i, Vec d) {
+#pragma unroll
+    for (int e = 0; e < kPolVec; ++e) d[e] = timesFactor(d[e], factor);
+    storeVec<float, kPolVec>(dlogp + i, d);
+  };
+#pragma unroll
+  for (int k = 0; k < kPolAhead; ++k)
+    if (at.first + k * at.step < at.whole) put(at.first + k * at.step, ahead[k]);
+  forTokens(
+      at, kPolAhead, [&](int64_t i) { put(i, loadVec<float, kPolVec>(dlogp + i)); },
       [&](int64_t i) { dlogp[i] = timesFactor(dlogp[i], factor); });
 }
 
@@ -269,40 +319,46 @@ __global__ void __launch_bounds__(kPolBlock) policyGrad(const PolCall a) {
 // their factor is known.  A wavefront takes 64 tokens of a rank at a time.
 __global__ void __launch_bounds__(kPolFewBlock) policyFew(const PolArgs a) {
   constexpr int WAVES = kPolFewBlock / kWave;
-  __shared__ double lds[WAVES][kPolSums];
+  __shared__ double lds[WAVES * kPolSums];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave), lane = (int)threadIdx.x % kWave;
+  // all of a thread's tokens are on their way before the first is looked at
+  float logp[kPolFewEach], old[kPolFewEach], advantage[kPolFewEach], ref[kPolFewEach], weight[kPolFewEach];
+  float *dlogp[kPolFewEach], d[kPolFewEach];
+  bool any[kPolFewEach];
+  const bool hasRef = a.hasRef;
+  int r = 0;
+#pragma unroll
+  for (int k = 0; k < kPolFewEach; ++k) {
+    const int piece = wave + k * WAVES;
+    any[k] = piece < a.blockStart[a.nranks];
+    if (!any[k]) continue;
+    while (piece >= a.blockStart[r + 1]) ++r;
+    const int i = (piece - a.blockStart[r]) * kWave + lane;
+    any[k] = i < a.start[r + 1] - a.start[r];
+    dlogp[k] = a.dlogp[r] ? a.dlogp[r] + i : nullptr;
+    if (!any[k]) continue;
+    logp[k] = a.logp[r][i];
+    old[k] = a.old[r][i];
+    advantage[k] = a.advantage[r][i];
+    ref[k] = hasRef ? a.ref[r][i] : 0.0f;
+    weight[k] = a.weight[r] ? a.weight[r][i] : 1.0f;
+  }
   double s[kPolSums] = {0.0, 0.0, 0.0, 0.0};
-  float d[kPolFewEach];
 #pragma unroll
-  for (int k = 0; k < kPolFewEach; ++k) {
-    const int piece = wave + k * WAVES;
-    d[k] = 0.0f;
-    if (piece >= a.blockStart[a.nranks]) continue;
-    int r = 0;
-    while (piece >= a.blockStart[r + 1]) ++r;
-    const int i = (piece - a.blockStart[r]) * kWave + lane;
-    if (i < a.start[r + 1] - a.start[r])
-      d[k] = addToken(a, a.logp[r][i], a.old[r][i], a.advantage[r][i], a.ref[r] != nullptr,
-                      a.ref[r] ? a.ref[r][i] : 0.0f, a.weight[r] ? a.weight[r][i] : 1.0f, s);
-  }
-  blockSums<kPolFewBlock>(s, lds);
-  if (threadIdx.x == 0) putStats(a, s);
-  const double factor = a.gradScale * partOf(a, s[0]);
+  for (int k = 0; k < kPolFewEach; ++k)
+    if (any[k]) d[k] = addToken(a, logp[k], old[k], advantage[k], hasRef, ref[k], weight[k], s);
+  const double sums = blockSums<kPolFewBlock>(s, lds);
+  putStats(a, sums);
+  const double factor = a.gradScale * partOf(a, laneOf(sums, 0));
 #pragma unroll
-  for (int k = 0; k < kPolFewEach; ++k) {
-    const int piece = wave + k * WAVES;
-    if (piece >= a.blockStart[a.nranks]) continue;
-    int r = 0;
-    while (piece >= a.blockStart[r + 1]) ++r;
-    const int i = (piece - a.blockStart[r]) * kWave + lane;
-    if (a.dlogp[r] && i < a.start[r + 1] - a.start[r]) a.dlogp[r][i] = timesFactor(d[k], factor);
-  }
+  for (int k = 0; k < kPolFewEach; ++k)
+    if (any[k] && dlogp[k]) *dlogp[k] = timesFactor(d[k], factor);
 }
 
 // Workgroups, and partial sums, of a launch of `tokens` tokens.
 int polBlocks(int64_t tokens) {
   const int64_t full = (tokens + kPolBlock * kPolVec - 1) / (kPolBlock * kPolVec);
-  return (int)(full < kPolGrid ? full : kPolGrid);
+  return (int)(full <= kPolOnce ? full : kPolGrid);
 }
 
 bool polFew(const Shape& s) { return s.total == 0 || (s.launches == 1 && s.total <= kPolFew); }
@@ -380,6 +436,7 @@ arResult_t policyLoss(const float* const* logp, const float* const* old, const f
   }
   if (outputsOverlap(v)) return arInvalidArgument;
   PolArgs a{};
+  a.hasRef = ref != nullptr;
   a.low = (float)(1.0 - clipLow);
   a.high = (float)(1.0 + clipHigh);
   a.logLow = std::log1p(-clipLow);
@@ -413,9 +470,9 @@ arResult_t policyLoss(const float* const* logp, const float* const* old, const f
   for (int l = 0; l < s.launches; ++l) {
     fillTokens(&a, logp, old, ref, advantage, weight, unscaled, tokens, nranks, l * kOpRanks, false);
     a.stats = l == 0 ? stats : nullptr;
-    const int grid = unscaled != nullptr ? a.blockStart[a.nranks] : 0;
-    if (grid == 0 && l > 0) continue;
-    if (launchKernel<PolCall>(policyGrad, dim3(grid > 0 ? grid : 1), dim3(kPolBlock), a, st) != hipSuccess) return arHipError;
+    const int grid = (unscaled != nullptr ? a.blockStart[a.nranks] : 0) + (l == 0 ? 1 : 0);
+    if (grid == 0) continue;
+    if (launchKernel<PolCall>(policyGrad, dim3(grid), dim3(kPolBlock), a, st) != hipSuccess) return arHipError;
   }
   return arSuccess;
 }
