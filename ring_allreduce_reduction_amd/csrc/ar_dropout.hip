@@ -25,6 +25,14 @@ constexpr int kDropBlock = 256;
 constexpr int kDropBackBlock = 512;
 constexpr int kDropCols = 8;    // of a thread: one block of 128 bits
 
+// How a launch is cut.  A slice of the rows is taken `together` rows at a time
+// by `tiles` workgroups: each has `across` threads side by side on every one of
+// these rows, or, `flat`, they follow each other through them (across: a row's).
+struct DropCut {
+  int across, together, tiles;
+  bool flat;
+};
+
 struct DropArgs {
   const void* x[kOpRanks];          // forward: x, backward: dy
   const void* bias[kOpRanks];
@@ -35,8 +43,10 @@ struct DropArgs {
   int sliceStart[kOpRanks + 1];     // and slices of rows [sliceStart[r], sliceStart[r + 1])
   int64_t xStride, residualStride, yStride;
   int cols, nranks;
-  int rowsLog;                      // a workgroup takes 2^rowsLog rows at a time
-  int tiles;                        // workgroups across the columns
+  DropCut cut;
+  unsigned nearBlocks;              // so many workgroups have a slice's on one XCD
+  uint32_t overTiles;               // 2^32 / tiles, rounded down, at most 2^32 - 1
+  float overAcross;                 // 1 / cut.across; 0 where there is one row at a time
   uint32_t threshold;               // T in the upper half; with no element kept 1,
   uint32_t mask;                    // and 0 here: what is drawn is taken for 0
   bool stream;                      // host: past the caches
@@ -131,6 +141,7 @@ struct Eight {
 // the first.  Threads past the columns have n <= 0.
 struct DropPlace {
   int rank, column, n;
+  int tile, slice, line, place;     // its line and place among the workgroup's rows
   int row, rows, step;
   uint32_t group;
 };
@@ -138,16 +149,28 @@ struct DropPlace {
 template <int BLOCK>
 __device__ __forceinline__ DropPlace placeOf(const DropArgs& a) {
   DropPlace p;
-  const int across = BLOCK >> a.rowsLog;
-  const int tile = (int)(blockIdx.x % (unsigned)a.tiles), slice = (int)(blockIdx.x / (unsigned)a.tiles);
-  p.rank = 0;
-  while (slice >= a.sliceStart[p.rank + 1]) ++p.rank;
-  p.group = (uint32_t)(tile * across) + (threadIdx.x & (unsigned)(across - 1));
+  // eight slices at a time, one an XCD (workgroups go to them in turn)
+  const bool near = blockIdx.x < a.nearBlocks;
+  const unsigned block = near ? blockIdx.x / 8 : blockIdx.x;
+  p.slice = (int)__umulhi(block, a.overTiles);   // block / tiles, or 1 less
+  p.tile = (int)block - p.slice * a.cut.tiles;
+  if (p.tile >= a.cut.tiles) {
+    ++p.slice;
+    p.tile -= a.cut.tiles;
+  }
+  if (near) p.slice = p.slice * 8 + (int)(blockIdx.x % 8);
+  const int item = (a.cut.flat ? p.tile * BLOCK : 0) + (int)threadIdx.x;
+  p.line = (int)fmaf((float)item, a.overAcross, 0.5f * a.overAcross);   // item / across
+  p.place = item - __mul24(p.line, a.cut.across);
+  p.group = (uint32_t)((a.cut.flat ? 0 : p.tile * a.cut.across) + p.place);
   p.column = (int)p.group * kDropCols;
-  p.n = a.cols - p.column;
-  p.row = ((slice - a.sliceStart[p.rank]) << a.rowsLog) + (int)(threadIdx.x / (unsigned)across);
+  p.rank = 0;
+  while (p.slice >= a.sliceStart[p.rank + 1]) ++p.rank;
+  p.n = p.line < a.cut.together ? a.cols - p.column : 0;
+  const int first = a.sliceStart[p.rank];
+  p.row = (p.slice - first) * a.cut.together + p.line;
   p.rows = a.rowStart[p.rank + 1] - a.rowStart[p.rank];
-  p.step = (a.sliceStart[p.rank + 1] - a.sliceStart[p.rank]) << a.rowsLog;
+  p.step = (a.sliceStart[p.rank + 1] - first) * a.cut.together;
   return p;
 }
 
@@ -225,7 +248,7 @@ template <int DT, bool SUMS, bool STREAM>
 __global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackward(const DropArgs a) {
   typedef typename Elem<DT>::type T;
   typedef Eight<DT, STREAM> E;
-  __shared__ float lds[SUMS ? kDropBackBlock / kWave : 1][kWave * kDropCols];
+  __shared__ float lds[SUMS ? kDropBackBlock * kDropCols : 1];
   const DropPlace at = placeOf<kDropBackBlock>(a);
   FloatVec<8> sum = (FloatVec<8>)0.0f;
   if (at.n > 0) {
@@ -250,21 +273,32 @@ __global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackward(const DropA
     });
   }
   if constexpr (SUMS) {
-    // the rows of a wavefront, then the wavefronts
-    const int across = kDropBackBlock >> a.rowsLog;
-    for (int m = across; m < kWave; m *= 2)
+    // a column's lines are shared out among the threads that there are to it
+    const int columns = a.cut.across * kDropCols;
+    int lines = a.cut.together;
+    if (at.line < lines)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor(sum[e], m);
-    const int wave = (int)threadIdx.x / kWave, lane = (int)threadIdx.x % kWave;
-    if (lane < across)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) lds[wave][lane * kDropCols + e] = sum[e];
+      for (int e = 0; e < 8; ++e) lds[at.line * columns + at.place * kDropCols + e] = sum[e];
     __syncthreads();
-    const int tile = (int)(blockIdx.x % (unsigned)a.tiles), slice = (int)(blockIdx.x / (unsigned)a.tiles);
-    const int64_t first = (int64_t)tile * across * kDropCols, c = first + threadIdx.x;
-    if ((int)threadIdx.x < across * kDropCols && c < a.cols) {
-      const float all = joinSlices<kDropBackBlock / kWave>([&](int w) { return lds[w][threadIdx.x]; });
-      a.partial[(size_t)slice * a.partialCols + c] = all;
+    const int parts = kDropBackBlock / columns;
+    if (parts > 1) {
+      const int part = (int)threadIdx.x / columns;
+      float all = 0.0f;
+      if (part < parts)
+        for (int k = part; k < lines; k += parts) all += lds[k * columns + (int)threadIdx.x % columns];
+      __syncthreads();
+      if (part < parts) lds[threadIdx.x] = all;
+      __syncthreads();
+      lines = lines < parts ? lines : parts;
+    }
+    for (int c = threadIdx.x; c < columns; c += kDropBackBlock) {
+      const int64_t column = (int64_t)at.tile * columns + c;
+      if (column >= a.cols) continue;
+      float all = 0.0f;
+      int k = 0;
+      for (; k + 8 <= lines; k += 8) all += joinSlices<8>([&](int w) { return lds[(k + w) * columns + c]; });
+      for (; k < lines; ++k) all += lds[k * columns + c];
+      a.partial[(size_t)at.slice * a.partialCols + column] = all;
     }
   }
 }
@@ -384,23 +418,51 @@ __global__ void __launch_bounds__(kJoinBlock) dropoutBiasGrads(const DropSumArgs
   }
 }
 
-// How a launch is cut: `tiles` workgroups across the columns, each of
-// block / 2^rowsLog threads side by side and 2^rowsLog rows at a time.
-struct DropCut {
-  int rowsLog, tiles;
-};
+// The share of threads that have columns.
+double dropUsed(const DropCut& k, int groups, int block) {
+  return (double)groups * k.together / ((double)k.tiles * block);
+}
 
-// At most 64 threads side by side (8 x 4096 x 8192 backward 180 us, 187 with 32,
-// 190-204 with 128), as many as leave less than an eighth of them past the
-// columns: 8191 columns backward 262 us with 64 and 335 with 32.
-DropCut dropCut(int cols, int block) {
+// What costs most is lines of 128 bytes that two workgroups share, then threads
+// without columns.  Rows of whole lines are cut at lines, 64 threads wide where
+// that comes out even (8 x 4096 x 8192 backward 180 us, 187 with 32, 190-204 with
+// 128).  Others forward are not cut at all: the workgroups follow each other
+// through so many rows that few threads are left over (of 8 x 32768 x 1032 bf16
+// 269 us, 509 in tiles of 16 threads; x 520 x 65536 262, 518; 6500 x 5000 249,
+// 300 in tiles of 64).  Backward, where a thread stays with its columns, they are
+// one tile up to 256 threads (x 1032 245, 299 in two of 65 threads, 423 in nine
+// of 16), else even ones of 64 to 256.
+DropCut dropCut(int cols, int block, bool sums) {
   const int groups = (cols + kDropCols - 1) / kDropCols;
-  for (int across = kWave; across > 1; across /= 2) {
-    const int tiles = (groups + across - 1) / across;
-    if (across <= 16 ? across < 2 * groups : (int64_t)tiles * across <= groups + groups / 8)
-      return {__builtin_ctz(block / across), tiles};
+  if (groups % 32 == 0) {
+    const int across = groups % 64 == 0 ? 64 : 32;
+    return {across, block / across, groups / across, false};
   }
-  return {__builtin_ctz(block), groups};
+  DropCut best{};
+  double used = 0.0;
+  const auto offer = [&](const DropCut& k, double more) {
+    const double u = dropUsed(k, groups, block);
+    if (u <= used + more) return;
+    used = u;
+    best = k;
+  };
+  if (!sums) {
+    const int most = groups < block / 32 ? block / groups : 32;
+    for (int rows = 1; rows <= most && used < 0.97; ++rows)
+      offer({groups, rows, (int)(((int64_t)rows * groups + block - 1) / block), true}, 0.0);
+    return best;
+  }
+  if (groups % 8 == 0 && groups > 64) {   // 20000 x 1600: five tiles of 40 185 us, seven of 32 189, one of 200 202
+    for (int across = 64; across >= 24; across -= 8)
+      offer({across, block / across, (groups + across - 1) / across, false}, 0.02);
+    return best;
+  }
+  if (groups <= block / 2) return {groups, block / groups, 1, false};
+  for (int together = 2; together <= block / 64; ++together) {
+    const int tiles = (groups + block / together - 1) / (block / together), across = (groups + tiles - 1) / tiles;
+    offer({across, block / across, tiles, false}, 0.02);
+  }
+  return best;
 }
 
 // Slices of the rows of a launch, at most (but one to each rank with rows).
@@ -415,7 +477,7 @@ DropCut dropCut(int cols, int block) {
 // rows are shared out among them all (312 workgroups 11.9 us, as 256 11.1; 580
 // 14.3, as 512 13.1; but 453 13.4, as 256 14.1), with tiles few enough to come near.
 int dropSlices(int64_t rows, const DropCut& k, bool sums) {
-  const int64_t once = (int64_t)1 << k.rowsLog, each = sums && once < 32 ? 32 : once;
+  const int64_t once = k.together, each = sums && once < 32 ? (32 + once - 1) / once * once : once;
   int64_t most = (sums ? 32 : 256) * kOpsCUs / k.tiles;
   const int64_t full = (rows + each - 1) / each;
   if (sums && most > 2 * kOpsCUs) most = 2 * kOpsCUs;
@@ -509,11 +571,25 @@ int fillDropRows(DropArgs* a, const size_t* rows, const uint64_t* firstRow, int 
   }
   a->cols = (int)cols;
   a->partialCols = (int)((cols + 7) / 8 * 8);
-  const DropCut k = dropCut((int)cols, sums ? kDropBackBlock : kDropBlock);
-  a->rowsLog = k.rowsLog;
-  a->tiles = k.tiles;
+  const DropCut k = dropCut((int)cols, sums ? kDropBackBlock : kDropBlock, sums);
+  a->cut = k;
+  a->overAcross = k.together > 1 ? 1.0f / (float)k.across : 0.0f;
   const int64_t n = a->rowStart[a->nranks];
-  return n == 0 ? 0 : shareOut(a->rowStart, a->nranks, 1 << k.rowsLog, dropSlices(n, k, sums), a->sliceStart);
+  return n == 0 ? 0 : shareOut(a->rowStart, a->nranks, k.together, dropSlices(n, k, sums), a->sliceStart);
+}
+
+// The grid.  Tiles whose ends are not those of 128-byte lines share lines with
+// their neighbours, and go to the same XCD with them, whose cache puts the lines
+// together (8 x 4096 x 8191 bf16 forward 273 us, 335 without; backward 219, 264;
+// of whole lines, 8192, 247, 247 and 184, 181).
+dim3 dropGrid(DropArgs* a, int slices, int esz) {
+  const unsigned tiles = (unsigned)a->cut.tiles, grid = (unsigned)slices * tiles;
+  uintptr_t bits = (uintptr_t)(a->xStride | a->yStride | a->residualStride | a->cut.across * kDropCols) * (uintptr_t)esz;
+  for (int r = 0; r < a->nranks; ++r) bits |= (uintptr_t)a->x[r] | (uintptr_t)a->y[r] | (uintptr_t)a->residual[r];
+  const bool near = !a->cut.flat && tiles > 1 && bits % 128 != 0;
+  a->nearBlocks = near ? grid / (8 * tiles) * (8 * tiles) : 0;
+  a->overTiles = tiles == 1 ? ~0u : (uint32_t)(((uint64_t)1 << 32) / tiles);
+  return dim3(grid);
 }
 
 arResult_t dropForward(const void* const* x, const void* const* bias, const void* const* residual, void* const* y,
@@ -559,7 +635,7 @@ arResult_t dropForward(const void* const* x, const void* const* bias, const void
     a.yStride = (int64_t)yStride;
     a.residualStride = (int64_t)residualStride;
     a.stream = bytes > kDropStream;
-    const dim3 grid((unsigned)slices * (unsigned)a.tiles);
+    const dim3 grid = dropGrid(&a, slices, esz);
     if (byTypes<DropForward, const DropArgs&, dim3, hipStream_t>(dtype, wtype, a, grid, st) != hipSuccess)
       return arHipError;
   }
@@ -569,7 +645,7 @@ arResult_t dropForward(const void* const* x, const void* const* bias, const void
 arResult_t dropWorkspace(const size_t* rows, int nranks, size_t cols, size_t* bytes) {
   Shape s;
   if (bytes == nullptr || !shapeOk(rows, nranks, cols, &s)) return arInvalidArgument;
-  const DropCut k = dropCut((int)cols, kDropBackBlock);
+  const DropCut k = dropCut((int)cols, kDropBackBlock, true);
   size_t slices = 0;
   const int ranks = dropRanks(cols);
   for (int first = 0; first < nranks; first += ranks) {
@@ -636,7 +712,7 @@ arResult_t dropBackward(const void* const* dy, void* const* dx, void* const* dbi
                                                                                                           : arHipError;
     }
     if (dbias != nullptr) a.partial = (float*)workspace + (size_t)partials * a.partialCols;
-    const dim3 grid((unsigned)slices * (unsigned)a.tiles);
+    const dim3 grid = dropGrid(&a, slices, esz);
     if (byType<DropBackward, const DropArgs&, dim3, hipStream_t>(dtype, a, grid, st) != hipSuccess) return arHipError;
     partials += slices;
   }

@@ -118,6 +118,21 @@ def test_many_rows(B, cols, dt):
     check_forward(run_forward(B, dys, zs, bs, 0.1), dys, zs, bs, kept, 0.1)
 
 
+# workgroups that follow each other through the rows, one tile of all columns, tiles of whole lines, even tiles
+@pytest.mark.parametrize("cols", [40, 264, 515, 576, 768, 1032, 1368, 1600, 2041, 2056, 5000, 8191])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=str)
+def test_ways_to_cut_rows(B, cols, dt):
+    """Enough rows for each way to cut them; padded to odd strides, eight slices' tiles lie on one XCD, but for the
+    last slices."""
+    most = 2000000 // cols
+    rows = [most // 2 + 1, 3, 0, most // 3]
+    dys, zs, bs = inputs(rows, cols, dt, torch.float32, cols + 4)
+    kept = masks(rows, cols, 0.1, SEED, OFFSET)
+    for pad, offs in ((0, 0), (3, 1)):
+        check_backward(*run_backward(B, dys, torch.float32, 0.1, pad=pad, offs=offs), dys, kept, 0.1)
+        check_forward(run_forward(B, dys, zs, bs, 0.1, pad=pad, offs=offs), dys, zs, bs, kept, 0.1)
+
+
 @pytest.mark.parametrize("into", [None, "x", "z"])
 @pytest.mark.parametrize("cols", [3, 64, 770, 2049])
 @pytest.mark.parametrize("dt", [torch.float32, torch.float16], ids=str)
