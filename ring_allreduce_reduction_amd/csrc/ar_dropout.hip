@@ -425,13 +425,14 @@ double dropUsed(const DropCut& k, int groups, int block) {
 
 // What costs most is lines of 128 bytes that two workgroups share, then threads
 // without columns.  Rows of whole lines are cut at lines, 64 threads wide where
-// that comes out even (8 x 4096 x 8192 backward 180 us, 187 with 32, 190-204 with
-// 128).  Others forward are not cut at all: the workgroups follow each other
-// through so many rows that few threads are left over (of 8 x 32768 x 1032 bf16
-// 269 us, 509 in tiles of 16 threads; x 520 x 65536 262, 518; 6500 x 5000 249,
-// 300 in tiles of 64).  Backward, where a thread stays with its columns, they are
-// one tile up to 256 threads (x 1032 245, 299 in two of 65 threads, 423 in nine
-// of 16), else even ones of 64 to 256.
+// that comes out even (8 x 4096 x 8192 bf16 backward 180 us, 187 with 32, 190-204
+// with 128).  Others forward are not cut at all: the workgroups follow each other
+// through so many rows that few threads are left over (8 x 32768 x 1032 269 us,
+// 509 in tiles of 16 threads; 8 x 65536 x 520 268, 518; 8 x 6500 x 5000 247, 300
+// in tiles of 64).  Backward, where a thread stays with its columns, they are one
+// tile up to 256 threads (x 1032 245, 299 in two of 65 threads, 423 in nine of
+// 16), else even ones of 64 to 256 (8 x 16384 x 2056 in four of 65 244, in five
+// of 52 263).
 DropCut dropCut(int cols, int block, bool sums) {
   const int groups = (cols + kDropCols - 1) / kDropCols;
   if (groups % 32 == 0) {
@@ -452,7 +453,7 @@ DropCut dropCut(int cols, int block, bool sums) {
       offer({groups, rows, (int)(((int64_t)rows * groups + block - 1) / block), true}, 0.0);
     return best;
   }
-  if (groups % 8 == 0 && groups > 64) {   // 20000 x 1600: five tiles of 40 185 us, seven of 32 189, one of 200 202
+  if (groups % 8 == 0 && groups > 64) {   // 8 x 20000 x 1600: five tiles of 40 185 us, seven of 32 189, one of 200 202
     for (int across = 64; across >= 24; across -= 8)
       offer({across, block / across, (groups + across - 1) / across, false}, 0.02);
     return best;
@@ -460,7 +461,7 @@ DropCut dropCut(int cols, int block, bool sums) {
   if (groups <= block / 2) return {groups, block / groups, 1, false};
   for (int together = 2; together <= block / 64; ++together) {
     const int tiles = (groups + block / together - 1) / (block / together), across = (groups + tiles - 1) / tiles;
-    offer({across, block / across, tiles, false}, 0.02);
+    if (across >= kWave) offer({across, block / across, tiles, false}, 0.02);
   }
   return best;
 }
