@@ -10,6 +10,7 @@
 // largest value it has met and the sum relative to it.
 #include <cmath>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "ar_rows.h"
@@ -114,10 +115,13 @@ __device__ __forceinline__ Part partOf(const T* p, int from, int to) {
 }
 
 // Calls f(column) for a thread's vectors, STEP columns apart, then g(column)
-// for its one of the rest.  `thread` counts from 0 among those that share p.
+// for its one of the rest.  `thread` counts from 0 among those that share p;
+// the vectors begin with thread `skip`.
 template <int V, int STEP, typename F, typename G>
-__device__ __forceinline__ void forPart(const Part& p, int thread, F f, G g) {
-  for (int c = p.first + thread * V; c < p.last; c += STEP) f(c);
+__device__ __forceinline__ void forPart(const Part& p, int thread, F f, G g, int skip = 0) {
+  int c = p.first + (thread - skip) * V;
+  if (thread < skip) c += STEP;
+  for (; c < p.last; c += STEP) f(c);
   const int head = p.first - p.from, rest = head + (p.to - p.last);   // at most 2 (V - 1)
   if (thread < rest) g(thread < head ? p.from + thread : p.last + (thread - head));
 }
@@ -131,19 +135,27 @@ __device__ __forceinline__ void meetColumns(Running* run, int thread, const type
   constexpr int V = kVec<DT>;
   typedef typename VecOf<T, V>::type Vec;
   const Part part = partOf<T, V>(x, from, to);
+  const auto some = [&](auto count, int i) {
+    constexpr int N = decltype(count)::value;
+    Vec v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      v[k] = (Vec)(T)-INFINITY;
+      if (i + k * THREADS * V < part.last) v[k] = loadAs<T, V, STREAM>(x + i + k * THREADS * V);
+    }
+    float f[V * N];
+#pragma unroll
+    for (int e = 0; e < V * N; ++e) f[e] = (float)v[e / V][e % V];
+    meet(run, f, c);
+  };
   forPart<V, THREADS * V * kLpVecs>(
       part, thread,
       [&](int i) {
-        Vec v[kLpVecs];
-#pragma unroll
-        for (int k = 0; k < kLpVecs; ++k) {
-          v[k] = (Vec)(T)-INFINITY;
-          if (i + k * THREADS * V < part.last) v[k] = loadAs<T, V, STREAM>(x + i + k * THREADS * V);
-        }
-        float f[V * kLpVecs];
-#pragma unroll
-        for (int e = 0; e < V * kLpVecs; ++e) f[e] = (float)v[e / V][e % V];
-        meet(run, f, c);
+        // how many of the four any thread of the wavefront has
+        const int left = part.last - i + thread * V;
+        if (__ballot(left > 2 * THREADS * V)) some(std::integral_constant<int, kLpVecs>(), i);
+        else if (__ballot(left > THREADS * V)) some(std::integral_constant<int, 2>(), i);
+        else some(std::integral_constant<int, 1>(), i);
       },
       [&](int i) {
         const float f[1] = {(float)x[i]};
@@ -318,13 +330,16 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpBackArg
     const T* x = (const T*)a.x[p.rank] + row * a.xStride[p.rank];
     T* dx = (T*)b.dx[p.rank] + row * b.dxStride[p.rank];
     const Part part = partOf<T, V>(dx, p.from, p.to);
+    // wavefronts store whole lines of 128 bytes (8192 rows x 8 x 16008 bf16 710 us,
+    // 740 without)
+    const int skip = THREADS >= kWave ? (int)((uintptr_t)(dx + part.first) % 128 / 16) : 0;
     const auto element = [&](float v, int c) {
       const float q = __builtin_amdgcn_exp2f(fmaf(v - base, a.scaleLog2e, -logSum));
       return (T)(g * ((c == at ? 1.0f : 0.0f) - q));
     };
     if (g == 0.0f)
       forPart<V, THREADS * V>(
-          part, thread, [&](int c) { store(dx + c, (Vec)(T)0.0f); }, [&](int c) { dx[c] = (T)0.0f; });
+          part, thread, [&](int c) { store(dx + c, (Vec)(T)0.0f); }, [&](int c) { dx[c] = (T)0.0f; }, skip);
     else
       forPart<V, THREADS * V>(
           part, thread,
@@ -335,7 +350,7 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpBackArg
             for (int e = 0; e < V; ++e) out[e] = element((float)v[e], c + e);
             store(dx + c, out);
           },
-          [&](int c) { dx[c] = element((float)x[c], c); });
+          [&](int c) { dx[c] = element((float)x[c], c); }, skip);
   }
 }
 
@@ -437,10 +452,13 @@ struct LpRows {
     const int64_t all = a.colStart[a.nranks] - a.colStart[0], columns = all / a.nranks;   // of a shard
     // Narrow shards: 16 threads take one, alone on a row or four of them (8192
     // rows x 8 x 250 bf16 16 us, 37 with a wavefront a shard, 62 with a workgroup;
-    // x 1000 26, 35; x 2000 48, 45; 1 x 256 4.7, 8.3 with a wavefront a row; 1 x
-    // 2000 8.6, 10.3), where there are many rows: of 300 x 8 x 1000 7.2 us and 5.9
-    // with a wavefront a shard, 1 x 2000 6.3 and 4.6.
-    if (columns <= 128 * V && a.rows >= 4 * kOpsCUs) {
+    // x 1000 26, 35; 1 x 256 4.7, 8.3 with a wavefront a row; 1 x 2000 8.6, 10.3),
+    // where there are many rows: of 300 x 8 x 1000 7.2 us and 5.9 with a wavefront a
+    // shard, 1 x 2000 6.3 and 4.6.  Wider ones leave a wavefront threads without a
+    // vector (110000 x 8 x 1200 352 us, 587 with a wavefront a shard; 65536 x 8 x
+    // 2056 383, 450; 50000 x 8 x 2600 354, 379; 40000 x 8 x 3000 327, 321) and ask for
+    // more rows (1200 x 8 x 2000 13.5, 11.6; 8192 46.6, 47.3).
+    if ((columns <= 128 * V && a.rows >= 4 * kOpsCUs) || (columns <= 352 * V && a.rows >= 16 * kOpsCUs)) {
       if (a.nranks < 4) return launch<kLpBlock, 16, 16>(a, stream, st);
       return launch<kLpBlock, kWave, 16>(a, stream, st);
     }
@@ -485,11 +503,14 @@ struct LpBackward {
       const int64_t c = a.colStart[r + 1] - a.colStart[r];
       widest = c > widest ? c : widest;
     }
-    // 8192 rows x 8 x 250 bf16: 15 us with 16 threads a row, 29 with 64, 92 with
-    // 256; x 500 23, 30, 92; x 1000 43, 38, 93; x 2000 154, 100, 125; x 4000 243,
-    // 188, 183.
-    if (widest <= 64 * V) return launch<16>(b, stream, st);
-    if (widest <= 256 * V) return launch<64>(b, stream, st);
+    // 2.1 GB of logits in 8 shards, bf16: of 100 columns 1290 us with 16 threads a
+    // row, 2017 with 32; 250 1174, 1116, 1667 with 64; 520 1310, 1003, 1177; 800 813,
+    // 740, 773; 1032 1001 with 32, 862, 1079 with 128; 1600 676 with 64, 763; 2000 775,
+    // 723, 911 with 256; 3000 697 with 128, 725; 5000 763, 731.
+    if (widest <= 24 * V) return launch<16>(b, stream, st);
+    if (widest <= 112 * V) return launch<32>(b, stream, st);
+    if (widest <= 240 * V) return launch<64>(b, stream, st);
+    if (widest <= 400 * V) return launch<128>(b, stream, st);
     return launch<kLpBlock>(b, stream, st);
   }
 };

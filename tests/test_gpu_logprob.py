@@ -126,6 +126,26 @@ def test_many_rows(B, rows, shards, dt):
     check_backward(run_backward(B, d, xs, t, top, log_sum), d, xs, t, top, log_sum)
 
 
+@pytest.mark.parametrize("dt", DTYPES, ids=str)
+@pytest.mark.parametrize("rows,shards", [(4096, [1100, 1409]), (4097, [1501, 1, 900, 2300, 703]), (4099, [2000])], ids=str)
+def test_narrow_shards_of_very_many_rows(B, rows, shards, dt):
+    """16 threads a shard, of few to all vectors they have in flight at a time."""
+    xs, t = inputs(rows, shards, dt, rows)
+    check_forward(run_forward(B, xs, t, offs=1), xs, t)
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("dt", DTYPES, ids=str)
+@pytest.mark.parametrize("widest", [1, 95, 97, 192, 193, 447, 449, 896, 897, 959, 961, 1599, 1601, 1920, 1921, 3200, 3201])
+def test_gradients_of_each_width(B, widest, dt, inplace):
+    """16 to 256 threads a row, their vectors from the row's first whole line on."""
+    rows, shards = 37, [widest, widest // 2, 3]
+    xs, t = inputs(rows, shards, dt, widest)
+    d, (top, log_sum) = gradients(rows, 11), statistics(xs, t, 1.0)
+    for pad, offs in ((0, 0), (3, 1), (8, 24)):
+        check_backward(run_backward(B, d, xs, t, top, log_sum, pad=pad, offs=offs, inplace=inplace), d, xs, t, top, log_sum)
+
+
 @pytest.mark.parametrize("rows", [1, 1200])
 @pytest.mark.parametrize("dt", DTYPES, ids=str)
 def test_padded_rows_odd_addresses_in_place(B, form, rows, dt):
