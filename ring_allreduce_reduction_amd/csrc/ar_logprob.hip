@@ -116,11 +116,12 @@ __device__ __forceinline__ Part partOf(const T* p, int from, int to) {
 
 // Calls f(column) for a thread's vectors, STEP columns apart, then g(column)
 // for its one of the rest.  `thread` counts from 0 among those that share p;
-// the vectors begin with thread `skip`.
+// the vectors begin with thread `skip`, the threads before it come in behind the
+// last of them, `behind` columns on.
 template <int V, int STEP, typename F, typename G>
-__device__ __forceinline__ void forPart(const Part& p, int thread, F f, G g, int skip = 0) {
+__device__ __forceinline__ void forPart(const Part& p, int thread, F f, G g, int skip = 0, int behind = 0) {
   int c = p.first + (thread - skip) * V;
-  if (thread < skip) c += STEP;
+  if (thread < skip) c += behind;
   for (; c < p.last; c += STEP) f(c);
   const int head = p.first - p.from, rest = head + (p.to - p.last);   // at most 2 (V - 1)
   if (thread < rest) g(thread < head ? p.from + thread : p.last + (thread - head));
@@ -313,7 +314,9 @@ template <int DT, int THREADS, bool STREAM>
 __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpBackArgs b) {
   typedef typename Elem<DT>::type T;
   const LpArgs& a = b.call;
-  constexpr int V = kVec<DT>, ROWS = kLpBlock / THREADS;
+  // vectors of a thread in flight, where it has more than a few (8192 rows x 8 x
+  // 16008 bf16 689 us, 707 with one, 681 with four; 65536 x 8 x 2056 735, 780, 760)
+  constexpr int V = kVec<DT>, ROWS = kLpBlock / THREADS, U = THREADS > 16 ? 2 : 1;
   typedef typename VecOf<T, V>::type Vec;
   const PieceAt p = pieceAt(a);
   const int thread = (int)threadIdx.x % THREADS;
@@ -339,18 +342,26 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpBackArg
     };
     if (g == 0.0f)
       forPart<V, THREADS * V>(
-          part, thread, [&](int c) { store(dx + c, (Vec)(T)0.0f); }, [&](int c) { dx[c] = (T)0.0f; }, skip);
+          part, thread, [&](int c) { store(dx + c, (Vec)(T)0.0f); }, [&](int c) { dx[c] = (T)0.0f; }, skip, THREADS * V);
     else
-      forPart<V, THREADS * V>(
+      forPart<V, U * THREADS * V>(
           part, thread,
           [&](int c) {
-            const Vec v = loadAs<T, V, STREAM>(x + c);
-            Vec out;
+            Vec v[U];
 #pragma unroll
-            for (int e = 0; e < V; ++e) out[e] = element((float)v[e], c + e);
-            store(dx + c, out);
+            for (int k = 0; k < U; ++k)
+              if (k == 0 || c + k * THREADS * V < part.last) v[k] = loadAs<T, V, STREAM>(x + c + k * THREADS * V);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+              const int first = c + k * THREADS * V;
+              if (k > 0 && first >= part.last) break;
+              Vec out;
+#pragma unroll
+              for (int e = 0; e < V; ++e) out[e] = element((float)v[k][e], first + e);
+              store(dx + first, out);
+            }
           },
-          [&](int c) { dx[c] = element((float)x[c], c); }, skip);
+          [&](int c) { dx[c] = element((float)x[c], c); }, skip, THREADS * V);
   }
 }
 
@@ -504,9 +515,9 @@ struct LpBackward {
       widest = c > widest ? c : widest;
     }
     // 2.1 GB of logits in 8 shards, bf16: of 100 columns 1290 us with 16 threads a
-    // row, 2017 with 32; 250 1174, 1116, 1667 with 64; 520 1310, 1003, 1177; 800 813,
-    // 740, 773; 1032 1001 with 32, 862, 1079 with 128; 1600 676 with 64, 763; 2000 775,
-    // 723, 911 with 256; 3000 697 with 128, 725; 5000 763, 731.
+    // row, 2026 with 32; 250 1174, 1124, 1707 with 64; 520 1310, 897, 1031; 800 697
+    // with 32, 687; 1032 903, 787, 1002 with 128; 1600 663 with 64, 686; 2000 738, 671,
+    // 1037 with 256; 3000 652 with 128, 708; 4000 685, 666; 5000 726, 691.
     if (widest <= 24 * V) return launch<16>(b, stream, st);
     if (widest <= 112 * V) return launch<32>(b, stream, st);
     if (widest <= 240 * V) return launch<64>(b, stream, st);
