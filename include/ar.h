@@ -672,7 +672,7 @@ arResult_t arGradClip(arTensorList_t list, arNormKind_t kind, float scale, float
 
 /*
  * arDropoutAdd -- what follows the AllReduce of a row-parallel layer, on every
- * rank's rows in one launch (ranks beyond 16 in further launches of 16):
+ * rank's rows in one launch (ranks beyond 32 in further launches of 32):
  *   y = residual + k * s * (x + bias),
  * where k is 1 for the elements that stay and 0 for the others, which are
  * dropped with probability p, and s = 1 / (1 - p).  A dropped element is the

@@ -33,14 +33,12 @@ struct DropCut {
   bool flat;
 };
 
-struct DropArgs {
-  const void* x[kOpRanks];          // forward: x, backward: dy
-  const void* bias[kOpRanks];
-  const void* residual[kOpRanks];
-  void* y[kOpRanks];                // forward: y, backward: dx or null
-  uint32_t firstRow[kOpRanks];
-  int rowStart[kOpRanks + 1];       // rank r has rows [rowStart[r], rowStart[r + 1]) of the launch
-  int sliceStart[kOpRanks + 1];     // and slices of rows [sliceStart[r], sliceStart[r + 1])
+// Ranks of a launch at most.  Up to kOpRanks of them travel in arguments of
+// that size, which take less time to hand over (4 ranks' 64 rows of 768 fp32 4.1
+// us, 4.6 with twice the size; 20 ranks' 6.0, 8.2 in two launches).
+constexpr int kDropRanks = 2 * kOpRanks;
+
+struct DropCall {
   int64_t xStride, residualStride, yStride;
   int cols, nranks;
   DropCut cut;
@@ -56,6 +54,36 @@ struct DropArgs {
   const uint64_t* step;
   float* partial;                   // backward: this launch's first row of partial sums, or null
   int partialCols;                  // cols up to a multiple of 8
+};
+
+template <int RANKS>
+struct DropArgs : DropCall {
+  const void* x[RANKS];             // forward: x, backward: dy
+  const void* bias[RANKS];
+  const void* residual[RANKS];
+  void* y[RANKS];                   // forward: y, backward: dx or null
+  uint32_t firstRow[RANKS];
+  int rowStart[RANKS + 1];          // rank r has rows [rowStart[r], rowStart[r + 1]) of the launch
+  int sliceStart[RANKS + 1];        // and slices of rows [sliceStart[r], sliceStart[r + 1])
+
+  // Those of another size, whose ranks fit.
+  template <int OTHER>
+  static DropArgs of(const DropArgs<OTHER>& a) {
+    DropArgs to{};
+    (DropCall&)to = a;
+    for (int r = 0; r < a.nranks; ++r) {
+      to.x[r] = a.x[r];
+      to.bias[r] = a.bias[r];
+      to.residual[r] = a.residual[r];
+      to.y[r] = a.y[r];
+      to.firstRow[r] = a.firstRow[r];
+    }
+    for (int r = 0; r <= a.nranks; ++r) {
+      to.rowStart[r] = a.rowStart[r];
+      to.sliceStart[r] = a.sliceStart[r];
+    }
+    return to;
+  }
 };
 
 typedef uint32_t Words __attribute__((ext_vector_type(4)));
@@ -81,7 +109,7 @@ __device__ __forceinline__ bool kept(const Words& w, int e, uint32_t threshold) 
   return (e % 2 ? w[e / 2] : w[e / 2] << 16) >= threshold;
 }
 
-__device__ __forceinline__ Words wordsOf(const DropArgs& a, uint64_t offset, uint32_t row, uint32_t group) {
+__device__ __forceinline__ Words wordsOf(const DropCall& a, uint64_t offset, uint32_t row, uint32_t group) {
   return philox(Words{group, row, (uint32_t)offset, (uint32_t)(offset >> 32)}, a.key0, a.key1) & a.mask;
 }
 
@@ -146,8 +174,8 @@ struct DropPlace {
   uint32_t group;
 };
 
-template <int BLOCK>
-__device__ __forceinline__ DropPlace placeOf(const DropArgs& a) {
+template <int BLOCK, int RANKS>
+__device__ __forceinline__ DropPlace placeOf(const DropArgs<RANKS>& a) {
   DropPlace p;
   // eight slices at a time, one an XCD (workgroups go to them in turn)
   const bool near = blockIdx.x < a.nearBlocks;
@@ -201,8 +229,8 @@ __device__ __forceinline__ void withAccess(const DropPlace& at, int cols, F f) {
     store);
 }
 
-template <int DT, int WT, bool STREAM, bool RESIDUAL>
-__device__ __forceinline__ void forwardRows(const DropArgs& a, const DropPlace& at) {
+template <int DT, int WT, bool STREAM, bool RESIDUAL, int RANKS>
+__device__ __forceinline__ void forwardRows(const DropArgs<RANKS>& a, const DropPlace& at) {
   typedef typename Elem<DT>::type T;
   typedef typename Elem<WT>::type W;
   typedef Eight<DT, STREAM> E;
@@ -236,16 +264,16 @@ __device__ __forceinline__ void forwardRows(const DropArgs& a, const DropPlace& 
   });
 }
 
-template <int DT, int WT, bool STREAM>
-__global__ void __launch_bounds__(kDropBlock) dropoutAdd(const DropArgs a) {
+template <int DT, int WT, int RANKS, bool STREAM>
+__global__ void __launch_bounds__(kDropBlock) dropoutAdd(const DropArgs<RANKS> a) {
   const DropPlace at = placeOf<kDropBlock>(a);
   if (at.n <= 0) return;
   if (a.residual[at.rank]) forwardRows<DT, WT, STREAM, true>(a, at);
   else forwardRows<DT, WT, STREAM, false>(a, at);
 }
 
-template <int DT, bool SUMS, bool STREAM>
-__global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackward(const DropArgs a) {
+template <int DT, int RANKS, bool SUMS, bool STREAM>
+__global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackward(const DropArgs<RANKS> a) {
   typedef typename Elem<DT>::type T;
   typedef Eight<DT, STREAM> E;
   __shared__ float lds[SUMS ? kDropBackBlock * kDropCols : 1];
@@ -310,13 +338,14 @@ __global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackward(const DropA
 // four rows' loads ahead gained nothing).
 constexpr int kFewAcross = 8, kFewRows = 256;
 
+template <int RANKS>
 struct DropFewArgs {
-  DropArgs rows;
-  void* dbias[kOpRanks];
+  DropArgs<RANKS> rows;
+  void* dbias[RANKS];
 };
 
-template <int DT, int WT>
-__global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackwardFew(const DropFewArgs w) {
+template <int DT, int WT, int RANKS>
+__global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackwardFew(const DropFewArgs<RANKS> w) {
   typedef typename Elem<DT>::type T;
   typedef typename Elem<WT>::type W;
   typedef Eight<DT, false> E;
@@ -328,7 +357,7 @@ __global__ void __launch_bounds__(kDropBackBlock) dropoutAddBackwardFew(const Dr
     uint32_t index;
   };
   __shared__ RowAt rows[kFewRows];
-  const DropArgs& a = w.rows;
+  const DropArgs<RANKS>& a = w.rows;
   for (int r = 0; r < a.nranks; ++r) {
     const int from = a.rowStart[r], n = a.rowStart[r + 1] - from;
     for (int i = threadIdx.x; i < n; i += kDropBackBlock)
@@ -497,27 +526,42 @@ constexpr size_t kDropStream = (size_t)256 << 20;
 
 template <int DT, int WT>
 struct DropForward {
-  static hipError_t run(const DropArgs& a, dim3 grid, hipStream_t st) {
-    return launchKernel(a.stream ? dropoutAdd<DT, WT, true> : dropoutAdd<DT, WT, false>, grid, dim3(kDropBlock), a, st);
+  template <int RANKS>
+  static hipError_t launch(const DropArgs<RANKS>& a, dim3 grid, hipStream_t st) {
+    return launchKernel(a.stream ? dropoutAdd<DT, WT, RANKS, true> : dropoutAdd<DT, WT, RANKS, false>, grid,
+                        dim3(kDropBlock), a, st);
+  }
+  static hipError_t run(const DropArgs<kDropRanks>& a, dim3 grid, hipStream_t st) {
+    return a.nranks > kOpRanks ? launch(a, grid, st) : launch(DropArgs<kOpRanks>::of(a), grid, st);
   }
 };
 
 template <int DT>
 struct DropBackward {
-  static hipError_t run(const DropArgs& a, dim3 grid, hipStream_t st) {
-    const auto kernel = a.partial ? (a.stream ? dropoutAddBackward<DT, true, true> : dropoutAddBackward<DT, true, false>)
-                                  : (a.stream ? dropoutAddBackward<DT, false, true> : dropoutAddBackward<DT, false, false>);
-    return launchKernel(kernel, grid, dim3(kDropBackBlock), a, st);
+  template <int RANKS>
+  static hipError_t launch(const DropArgs<RANKS>& a, dim3 grid, hipStream_t st) {
+    const auto sums = a.stream ? dropoutAddBackward<DT, RANKS, true, true> : dropoutAddBackward<DT, RANKS, true, false>;
+    const auto none = a.stream ? dropoutAddBackward<DT, RANKS, false, true> : dropoutAddBackward<DT, RANKS, false, false>;
+    return launchKernel(a.partial ? sums : none, grid, dim3(kDropBackBlock), a, st);
+  }
+  static hipError_t run(const DropArgs<kDropRanks>& a, dim3 grid, hipStream_t st) {
+    return a.nranks > kOpRanks ? launch(a, grid, st) : launch(DropArgs<kOpRanks>::of(a), grid, st);
   }
 };
 
 template <int DT, int WT>
 struct DropBackwardFew {
-  static hipError_t run(const DropFewArgs& w, hipStream_t st) {
+  template <int RANKS>
+  static hipError_t launch(const DropArgs<RANKS>& a, void* const* dbias, hipStream_t st) {
     constexpr int COLS = kFewAcross * kDropCols;
-    return launchKernel(dropoutAddBackwardFew<DT, WT>,
-                        dim3(gridOf(((int64_t)w.rows.cols + COLS - 1) / COLS, kDropBackBlock)), dim3(kDropBackBlock), w,
-                        st);
+    DropFewArgs<RANKS> w;
+    w.rows = a;
+    for (int r = 0; r < RANKS; ++r) w.dbias[r] = r < a.nranks ? dbias[r] : nullptr;
+    return launchKernel(dropoutAddBackwardFew<DT, WT, RANKS>,
+                        dim3(gridOf(((int64_t)a.cols + COLS - 1) / COLS, kDropBackBlock)), dim3(kDropBackBlock), w, st);
+  }
+  static hipError_t run(const DropArgs<kDropRanks>& a, void* const* dbias, hipStream_t st) {
+    return a.nranks > kOpRanks ? launch(a, dbias, st) : launch(DropArgs<kOpRanks>::of(a), dbias, st);
   }
 };
 
@@ -542,7 +586,7 @@ bool drawOk(const size_t* rows, const uint64_t* firstRow, int nranks, double p, 
   return true;
 }
 
-void fillDraw(DropArgs* a, double p, uint64_t seed, uint64_t offset, const uint64_t* step) {
+void fillDraw(DropCall* a, double p, uint64_t seed, uint64_t offset, const uint64_t* step) {
   const int t = (int)std::floor(p * 65536.0 + 0.5);
   a->threshold = (uint32_t)(t >= 65536 ? 1 : t) << 16;
   a->mask = t >= 65536 ? 0u : ~0u;
@@ -555,10 +599,10 @@ void fillDraw(DropArgs* a, double p, uint64_t seed, uint64_t offset, const uint6
 
 // Ranks of a launch: its workgroups, one at least to a tile of each rank's
 // columns, have fewer than 2^32 threads.
-int dropRanks(size_t cols) { return cols <= (size_t)1 << 26 ? kOpRanks : 1; }
+int dropRanks(size_t cols) { return cols <= (size_t)1 << 26 ? kDropRanks : 1; }
 
 // This launch's rows and their slices; returns the grid's slices.
-int fillDropRows(DropArgs* a, const size_t* rows, const uint64_t* firstRow, int nranks, int first, size_t cols,
+int fillDropRows(DropArgs<kDropRanks>* a, const size_t* rows, const uint64_t* firstRow, int nranks, int first, size_t cols,
                  bool sums) {
   const int most = dropRanks(cols);
   a->nranks = nranks - first < most ? nranks - first : most;
@@ -583,7 +627,7 @@ int fillDropRows(DropArgs* a, const size_t* rows, const uint64_t* firstRow, int 
 // their neighbours, and go to the same XCD with them, whose cache puts the lines
 // together (8 x 4096 x 8191 bf16 forward 273 us, 335 without; backward 219, 264;
 // of whole lines, 8192, 247, 247 and 184, 181).
-dim3 dropGrid(DropArgs* a, int slices, int esz) {
+dim3 dropGrid(DropArgs<kDropRanks>* a, int slices, int esz) {
   const unsigned tiles = (unsigned)a->cut.tiles, grid = (unsigned)slices * tiles;
   uintptr_t bits = (uintptr_t)(a->xStride | a->yStride | a->residualStride | a->cut.across * kDropCols) * (uintptr_t)esz;
   for (int r = 0; r < a->nranks; ++r) bits |= (uintptr_t)a->x[r] | (uintptr_t)a->y[r] | (uintptr_t)a->residual[r];
@@ -619,7 +663,7 @@ arResult_t dropForward(const void* const* x, const void* const* bias, const void
     if (!ok) return arInvalidArgument;
   }
   if (outputsOverlap(v)) return arInvalidArgument;
-  DropArgs a{};
+  DropArgs<kDropRanks> a{};
   fillDraw(&a, p, seed, offset, step);
   const size_t bytes = (size_t)s.total * cols * (size_t)esz * (residual ? 3 : 2);
   for (int first = 0; first < nranks; first += dropRanks(cols)) {
@@ -637,7 +681,7 @@ arResult_t dropForward(const void* const* x, const void* const* bias, const void
     a.residualStride = (int64_t)residualStride;
     a.stream = bytes > kDropStream;
     const dim3 grid = dropGrid(&a, slices, esz);
-    if (byTypes<DropForward, const DropArgs&, dim3, hipStream_t>(dtype, wtype, a, grid, st) != hipSuccess)
+    if (byTypes<DropForward, const DropArgs<kDropRanks>&, dim3, hipStream_t>(dtype, wtype, a, grid, st) != hipSuccess)
       return arHipError;
   }
   return arSuccess;
@@ -691,8 +735,7 @@ arResult_t dropBackward(const void* const* dy, void* const* dx, void* const* dbi
     if (!ok) return arInvalidArgument;
   }
   if (outputsOverlap(v)) return arInvalidArgument;
-  DropFewArgs w{};
-  DropArgs& a = w.rows;
+  DropArgs<kDropRanks> a{};
   fillDraw(&a, p, seed, offset, step);
   int partials = 0;
   const size_t bytes = (size_t)s.total * cols * (size_t)esz * (dx ? 2 : 1);
@@ -708,13 +751,14 @@ arResult_t dropBackward(const void* const* dy, void* const* dx, void* const* dbi
     a.yStride = (int64_t)dxStride;
     a.stream = bytes > kDropStream;
     if (dbias != nullptr && nranks <= dropRanks(cols) && s.total <= kFewRows) {
-      for (int r = 0; r < nranks; ++r) w.dbias[r] = dbias[r];
-      return byTypes<DropBackwardFew, const DropFewArgs&, hipStream_t>(dtype, wtype, w, st) == hipSuccess ? arSuccess
-                                                                                                          : arHipError;
+      const hipError_t e = byTypes<DropBackwardFew, const DropArgs<kDropRanks>&, void* const*, hipStream_t>(
+          dtype, wtype, a, dbias, st);
+      return e == hipSuccess ? arSuccess : arHipError;
     }
     if (dbias != nullptr) a.partial = (float*)workspace + (size_t)partials * a.partialCols;
     const dim3 grid = dropGrid(&a, slices, esz);
-    if (byType<DropBackward, const DropArgs&, dim3, hipStream_t>(dtype, a, grid, st) != hipSuccess) return arHipError;
+    if (byType<DropBackward, const DropArgs<kDropRanks>&, dim3, hipStream_t>(dtype, a, grid, st) != hipSuccess)
+      return arHipError;
     partials += slices;
   }
   if (dbias == nullptr) return arSuccess;

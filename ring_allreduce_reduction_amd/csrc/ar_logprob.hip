@@ -22,11 +22,12 @@ constexpr int kLpBlock = 256;
 constexpr int kLpVecs = 4;       // of a thread in flight
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
-struct LpArgs {
-  const void* x[kOpRanks];
-  int64_t xStride[kOpRanks];
-  int64_t colStart[kOpRanks + 1];   // shard r holds columns [colStart[r], colStart[r + 1]) of the vocabulary
-  int pieceStart[kOpRanks + 1];     // and pieces [pieceStart[r], pieceStart[r + 1]) of the launch
+// Ranks of a launch at most.  Up to kOpRanks of them travel in arguments of
+// that size, which take less time to hand over (one token, 8 ranks: 6.3 us, 6.8
+// with twice the size; 20 ranks 7.6, 10.4 in two launches and a join).
+constexpr int kLpRanks = 2 * kOpRanks;
+
+struct LpCall {
   int64_t vocabulary;               // the columns of every launch's shards
   const int64_t* targets;
   const float* dlogp;
@@ -39,10 +40,46 @@ struct LpArgs {
   float scale, scaleLog2e;
 };
 
+template <int RANKS>
+struct LpArgs : LpCall {
+  const void* x[RANKS];
+  int64_t xStride[RANKS];
+  int64_t colStart[RANKS + 1];      // shard r holds columns [colStart[r], colStart[r + 1]) of the vocabulary
+  int pieceStart[RANKS + 1];        // and pieces [pieceStart[r], pieceStart[r + 1]) of the launch
+
+  // Those of another size, whose ranks fit.
+  template <int OTHER>
+  static LpArgs of(const LpArgs<OTHER>& a) {
+    LpArgs to{};
+    (LpCall&)to = a;
+    for (int r = 0; r < a.nranks; ++r) {
+      to.x[r] = a.x[r];
+      to.xStride[r] = a.xStride[r];
+    }
+    for (int r = 0; r <= a.nranks; ++r) {
+      to.colStart[r] = a.colStart[r];
+      to.pieceStart[r] = a.pieceStart[r];
+    }
+    return to;
+  }
+};
+
+template <int RANKS>
 struct LpBackArgs {
-  LpArgs call;
-  void* dx[kOpRanks];
-  int64_t dxStride[kOpRanks];
+  LpArgs<RANKS> call;
+  void* dx[RANKS];
+  int64_t dxStride[RANKS];
+
+  template <int OTHER>
+  static LpBackArgs of(const LpBackArgs<OTHER>& b) {
+    LpBackArgs to{};
+    to.call = LpArgs<RANKS>::of(b.call);
+    for (int r = 0; r < b.call.nranks; ++r) {
+      to.dx[r] = b.dx[r];
+      to.dxStride[r] = b.dxStride[r];
+    }
+    return to;
+  }
 };
 
 // A largest value and the sum of exp(scale (x - it)) of what was met.  Of
@@ -181,8 +218,8 @@ __device__ __forceinline__ Running joinThreads(Running run, float c, Running* ld
 }
 
 // The target's logit, read early; NaN where the launch's shards have none.
-template <int DT>
-__device__ __forceinline__ float targetLogit(const LpArgs& a, int64_t row, int64_t t) {
+template <int DT, int RANKS>
+__device__ __forceinline__ float targetLogit(const LpArgs<RANKS>& a, int64_t row, int64_t t) {
   for (int r = 0; r < a.nranks; ++r)
     if (t >= a.colStart[r] && t < a.colStart[r + 1])
       return (float)((const typename Elem<DT>::type*)a.x[r])[row * a.xStride[r] + (t - a.colStart[r])];
@@ -191,7 +228,8 @@ __device__ __forceinline__ float targetLogit(const LpArgs& a, int64_t row, int64
 
 // Of several launches each leaves the running values of its shards, and the one
 // with the target its logit, for tokenLogprobJoin.
-__device__ __forceinline__ void putPart(const LpArgs& a, int64_t row, int64_t t, const Running& run, float logit) {
+template <int RANKS>
+__device__ __forceinline__ void putPart(const LpArgs<RANKS>& a, int64_t row, int64_t t, const Running& run, float logit) {
   a.partial[row * a.parts] = make_float2(run.top, run.sum);
   if (t >= a.colStart[0] && t < a.colStart[a.nranks]) a.logp[row] = logit;
 }
@@ -212,8 +250,8 @@ __device__ __forceinline__ void putIgnored(const A& a, int64_t row) {
 }
 
 // ROW threads take a row, SHARD of them a shard at a time.
-template <int DT, int BLOCK, int ROW, int SHARD, bool STREAM>
-__global__ void __launch_bounds__(BLOCK) tokenLogprobRows(const LpArgs a) {
+template <int DT, int RANKS, int BLOCK, int ROW, int SHARD, bool STREAM>
+__global__ void __launch_bounds__(BLOCK) tokenLogprobRows(const LpArgs<RANKS> a) {
   typedef typename Elem<DT>::type T;
   static_assert(ROW == BLOCK || ROW <= kWave, "rows of a wavefront's parts meet no barrier");
   constexpr int ROWS = BLOCK / ROW;
@@ -248,7 +286,8 @@ struct PieceAt {
   int rank, from, to;
 };
 
-__device__ __forceinline__ PieceAt pieceAt(const LpArgs& a) {
+template <int RANKS>
+__device__ __forceinline__ PieceAt pieceAt(const LpArgs<RANKS>& a) {
   PieceAt p;
   p.rank = 0;
   while ((int)blockIdx.x >= a.pieceStart[p.rank + 1]) ++p.rank;
@@ -262,8 +301,8 @@ __device__ __forceinline__ PieceAt pieceAt(const LpArgs& a) {
 
 // Few rows of a long vocabulary: a workgroup a piece of a row leaves the
 // piece's running values; tokenLogprobJoin joins them.
-template <int DT>
-__global__ void __launch_bounds__(kLpBlock) tokenLogprobPieces(const LpArgs a) {
+template <int DT, int RANKS>
+__global__ void __launch_bounds__(kLpBlock) tokenLogprobPieces(const LpArgs<RANKS> a) {
   typedef typename Elem<DT>::type T;
   __shared__ Running lds[kLpBlock / kWave];
   const PieceAt p = pieceAt(a);
@@ -310,10 +349,10 @@ __global__ void __launch_bounds__(kWave) tokenLogprobJoin(const LpJoinArgs a) {
 }
 
 // A workgroup takes a piece of kLpBlock / THREADS rows at a time.
-template <int DT, int THREADS, bool STREAM>
-__global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpBackArgs b) {
+template <int DT, int RANKS, int THREADS, bool STREAM>
+__global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpBackArgs<RANKS> b) {
   typedef typename Elem<DT>::type T;
-  const LpArgs& a = b.call;
+  const LpArgs<RANKS>& a = b.call;
   // vectors of a thread in flight, where it has more than a few (8192 rows x 8 x
   // 16008 bf16 689 us, 707 with one, 681 with four; 65536 x 8 x 2056 735, 780, 760)
   constexpr int V = kVec<DT>, ROWS = kLpBlock / THREADS, U = THREADS > 16 ? 2 : 1;
@@ -397,7 +436,7 @@ LpCut lpCut(const size_t* cols, int nranks, size_t rows) {
     k.pieceCols *= 2;
     count();
   }
-  if (k.whole) k.parts = (nranks + kOpRanks - 1) / kOpRanks;
+  if (k.whole) k.parts = (nranks + kLpRanks - 1) / kLpRanks;
   return k;
 }
 
@@ -427,9 +466,9 @@ arResult_t lpWorkspace(size_t rows, const size_t* cols, int nranks, size_t* byte
   return arSuccess;
 }
 
-void fillShards(LpArgs* a, const void* const* x, const size_t* cols, const size_t* strides, int nranks, int first,
+void fillShards(LpArgs<kLpRanks>* a, const void* const* x, const size_t* cols, const size_t* strides, int nranks, int first,
                 int pieceCols) {
-  a->nranks = nranks - first < kOpRanks ? nranks - first : kOpRanks;
+  a->nranks = nranks - first < kLpRanks ? nranks - first : kLpRanks;
   int64_t at = 0;
   for (int r = 0; r < first; ++r) at += (int64_t)cols[r];
   a->colStart[0] = at;
@@ -444,34 +483,45 @@ void fillShards(LpArgs* a, const void* const* x, const size_t* cols, const size_
 }
 
 // Workgroups of `each` rows at a time.
-dim3 pieceGrid(const LpArgs& a, int each) {
+template <int RANKS>
+dim3 pieceGrid(const LpArgs<RANKS>& a, int each) {
   const int64_t groups = ((int64_t)a.rows + each - 1) / each, rows = groups < 65535 ? groups : 65535;
   return dim3((unsigned)a.pieceStart[a.nranks], (unsigned)rows);
 }
 
 template <int DT>
 struct LpRows {
-  template <int BLOCK, int ROW, int SHARD>
-  static hipError_t launch(const LpArgs& a, bool stream, hipStream_t st) {
+  template <int RANKS, int BLOCK, int ROW, int SHARD>
+  static hipError_t launch(const LpArgs<RANKS>& a, bool stream, hipStream_t st) {
     constexpr int ROWS = BLOCK / ROW;
-    return launchKernel(stream ? tokenLogprobRows<DT, BLOCK, ROW, SHARD, true>
-                               : tokenLogprobRows<DT, BLOCK, ROW, SHARD, false>,
+    return launchKernel(stream ? tokenLogprobRows<DT, RANKS, BLOCK, ROW, SHARD, true>
+                               : tokenLogprobRows<DT, RANKS, BLOCK, ROW, SHARD, false>,
                         dim3(gridOf(((int64_t)a.rows + ROWS - 1) / ROWS, BLOCK)), dim3(BLOCK), a, st);
   }
-  static hipError_t run(const LpArgs& a, bool stream, hipStream_t st) {
+  // Narrow shards: 16 threads take one, alone on a row or four of them (8192
+  // rows x 8 x 250 bf16 16 us, 37 with a wavefront a shard, 62 with a workgroup;
+  // x 1000 26, 35; 1 x 256 4.7, 8.3 with a wavefront a row; 1 x 2000 8.6, 10.3),
+  // where there are many rows: of 300 x 8 x 1000 7.2 us and 5.9 with a wavefront a
+  // shard, 1 x 2000 6.3 and 4.6.  Wider ones leave a wavefront threads without a
+  // vector (110000 x 8 x 1200 352 us, 587 with a wavefront a shard; 65536 x 8 x
+  // 2056 383, 450; 50000 x 8 x 2600 354, 379; 40000 x 8 x 3000 327, 321) and ask for
+  // more rows (1200 x 8 x 2000 13.5, 11.6; 8192 46.6, 47.3).
+  static bool narrow(const LpArgs<kLpRanks>& a) {
     constexpr int V = kVec<DT>;
-    const int64_t all = a.colStart[a.nranks] - a.colStart[0], columns = all / a.nranks;   // of a shard
-    // Narrow shards: 16 threads take one, alone on a row or four of them (8192
-    // rows x 8 x 250 bf16 16 us, 37 with a wavefront a shard, 62 with a workgroup;
-    // x 1000 26, 35; 1 x 256 4.7, 8.3 with a wavefront a row; 1 x 2000 8.6, 10.3),
-    // where there are many rows: of 300 x 8 x 1000 7.2 us and 5.9 with a wavefront a
-    // shard, 1 x 2000 6.3 and 4.6.  Wider ones leave a wavefront threads without a
-    // vector (110000 x 8 x 1200 352 us, 587 with a wavefront a shard; 65536 x 8 x
-    // 2056 383, 450; 50000 x 8 x 2600 354, 379; 40000 x 8 x 3000 327, 321) and ask for
-    // more rows (1200 x 8 x 2000 13.5, 11.6; 8192 46.6, 47.3).
-    if ((columns <= 128 * V && a.rows >= 4 * kOpsCUs) || (columns <= 352 * V && a.rows >= 16 * kOpsCUs)) {
-      if (a.nranks < 4) return launch<kLpBlock, 16, 16>(a, stream, st);
-      return launch<kLpBlock, kWave, 16>(a, stream, st);
+    const int64_t columns = (a.colStart[a.nranks] - a.colStart[0]) / a.nranks;
+    return (columns <= 128 * V && a.rows >= 4 * kOpsCUs) || (columns <= 352 * V && a.rows >= 16 * kOpsCUs);
+  }
+  static hipError_t run(const LpArgs<kLpRanks>& all, bool stream, hipStream_t st) {
+    constexpr int V = kVec<DT>;
+    if (all.nranks > kOpRanks) {
+      if (narrow(all)) return launch<kLpRanks, kLpBlock, kWave, 16>(all, stream, st);
+      return launch<kLpRanks, 512, 512, kWave>(all, stream, st);
+    }
+    const LpArgs<kOpRanks> a = LpArgs<kOpRanks>::of(all);
+    const int64_t vocabulary = a.colStart[a.nranks] - a.colStart[0], columns = vocabulary / a.nranks;   // of a shard
+    if (narrow(all)) {
+      if (a.nranks < 4) return launch<kOpRanks, kLpBlock, 16, 16>(a, stream, st);
+      return launch<kOpRanks, kLpBlock, kWave, 16>(a, stream, st);
     }
     // From four shards on a wavefront takes a shard at a time: shards rarely
     // fill the vectors that a whole workgroup has in flight (8192 rows x 8 x 5000
@@ -482,33 +532,42 @@ struct LpRows {
     // others to workgroups as wide as their vectors fill (4096 x 50257 70 us with
     // 512, 75 with 256; 50 rows x 3 x 6000 5.8 us with a wavefront a shard, 6.2
     // together; 500 x 2 x 30000 20, 14).
-    if (a.nranks > 4) return launch<512, 512, kWave>(a, stream, st);
-    if (a.nranks == 4) return launch<kLpBlock, kLpBlock, kWave>(a, stream, st);
+    if (a.nranks > 4) return launch<kOpRanks, 512, 512, kWave>(a, stream, st);
+    if (a.nranks == 4) return launch<kOpRanks, kLpBlock, kLpBlock, kWave>(a, stream, st);
     const int many = a.rows < 1024 ? a.rows : 1024;
-    if (all <= (int64_t)V * many) return launch<kLpBlock, kWave, kWave>(a, stream, st);
-    if (a.nranks > 1 && columns <= 1024 * V) return launch<kLpBlock, kLpBlock, kWave>(a, stream, st);
-    if (columns < 3 * 512 * V) return launch<kLpBlock, kLpBlock, kLpBlock>(a, stream, st);
-    return launch<512, 512, 512>(a, stream, st);
+    if (vocabulary <= (int64_t)V * many) return launch<kOpRanks, kLpBlock, kWave, kWave>(a, stream, st);
+    if (a.nranks > 1 && columns <= 1024 * V) return launch<kOpRanks, kLpBlock, kLpBlock, kWave>(a, stream, st);
+    if (columns < 3 * 512 * V) return launch<kOpRanks, kLpBlock, kLpBlock, kLpBlock>(a, stream, st);
+    return launch<kOpRanks, 512, 512, 512>(a, stream, st);
   }
 };
 
 template <int DT>
 struct LpPieces {
-  static hipError_t run(const LpArgs& a, hipStream_t st) {
-    return launchKernel(tokenLogprobPieces<DT>, pieceGrid(a, 1), dim3(kLpBlock), a, st);
+  template <int RANKS>
+  static hipError_t launch(const LpArgs<RANKS>& a, hipStream_t st) {
+    return launchKernel(tokenLogprobPieces<DT, RANKS>, pieceGrid(a, 1), dim3(kLpBlock), a, st);
+  }
+  static hipError_t run(const LpArgs<kLpRanks>& a, hipStream_t st) {
+    return a.nranks > kOpRanks ? launch(a, st) : launch(LpArgs<kOpRanks>::of(a), st);
   }
 };
 
 template <int DT>
 struct LpBackward {
-  template <int THREADS>
-  static hipError_t launch(const LpBackArgs& b, bool stream, hipStream_t st) {
-    return launchKernel(stream ? tokenLogprobBackward<DT, THREADS, true> : tokenLogprobBackward<DT, THREADS, false>,
+  template <int THREADS, int RANKS>
+  static hipError_t launch(const LpBackArgs<RANKS>& b, bool stream, hipStream_t st) {
+    return launchKernel(stream ? tokenLogprobBackward<DT, RANKS, THREADS, true>
+                               : tokenLogprobBackward<DT, RANKS, THREADS, false>,
                         pieceGrid(b.call, kLpBlock / THREADS), dim3(kLpBlock), b, st);
   }
-  static hipError_t run(const LpBackArgs& b, bool stream, hipStream_t st) {
+  static hipError_t run(const LpBackArgs<kLpRanks>& b, bool stream, hipStream_t st) {
+    return b.call.nranks > kOpRanks ? byWidth(b, stream, st) : byWidth(LpBackArgs<kOpRanks>::of(b), stream, st);
+  }
+  template <int RANKS>
+  static hipError_t byWidth(const LpBackArgs<RANKS>& b, bool stream, hipStream_t st) {
     constexpr int V = kVec<DT>;
-    const LpArgs& a = b.call;
+    const LpArgs<RANKS>& a = b.call;
     int64_t widest = 0;   // of the launch's shards
     for (int r = 0; r < a.nranks; ++r) {
       const int64_t c = a.colStart[r + 1] - a.colStart[r];
@@ -557,7 +616,7 @@ arResult_t lpForward(const void* const* logits, const size_t* cols, const size_t
     v.push_back(Extent{(uintptr_t)workspace, need, 1, need, true, -1});
   }
   if (outputsOverlap(v)) return arInvalidArgument;
-  LpArgs a{};
+  LpArgs<kLpRanks> a{};
   a.targets = targets;
   a.logp = logp;
   a.top = top;
@@ -569,13 +628,13 @@ arResult_t lpForward(const void* const* logits, const size_t* cols, const size_t
   a.parts = (int)k.parts;
   const bool stream = rows * (size_t)vocabulary * (size_t)elemSize(dtype) > kLpStream;
   int part = 0;
-  for (int first = 0; first < nranks; first += kOpRanks) {
+  for (int first = 0; first < nranks; first += kLpRanks) {
     fillShards(&a, logits, cols, strides, nranks, first, k.pieceCols);
     const int pieces = a.pieceStart[a.nranks];
     if (joined) a.partial = (float2*)workspace + part;
     hipError_t e = hipSuccess;
-    if (k.whole) e = byType<LpRows, const LpArgs&, bool, hipStream_t>(dtype, a, stream, st);
-    else if (pieces > 0) e = byType<LpPieces, const LpArgs&, hipStream_t>(dtype, a, st);
+    if (k.whole) e = byType<LpRows, const LpArgs<kLpRanks>&, bool, hipStream_t>(dtype, a, stream, st);
+    else if (pieces > 0) e = byType<LpPieces, const LpArgs<kLpRanks>&, hipStream_t>(dtype, a, st);
     if (e != hipSuccess) return arHipError;
     part += k.whole ? 1 : pieces;
   }
@@ -606,8 +665,8 @@ arResult_t lpBackward(const float* dlogp, const void* const* logits, const size_
       ok = ok && addRows(v, logits[r], rows, cols[r], strides ? strides[r] : cols[r], esz, false, r) &&
            addRows(v, dlogits[r], rows, cols[r], dstrides ? dstrides[r] : cols[r], esz, true, r);
   if (!ok || outputsOverlap(v)) return arInvalidArgument;
-  LpBackArgs b{};
-  LpArgs& a = b.call;
+  LpBackArgs<kLpRanks> b{};
+  LpArgs<kLpRanks>& a = b.call;
   a.targets = targets;
   a.dlogp = dlogp;
   a.top = const_cast<float*>(top);
@@ -618,14 +677,14 @@ arResult_t lpBackward(const float* dlogp, const void* const* logits, const size_
   a.vocabulary = vocabulary;
   const LpCut k = lpCut(cols, nranks, rows);
   const size_t bytes = 2 * rows * (size_t)vocabulary * (size_t)esz;
-  for (int first = 0; first < nranks; first += kOpRanks) {
+  for (int first = 0; first < nranks; first += kLpRanks) {
     fillShards(&a, logits, cols, strides, nranks, first, k.pieceCols);
     for (int r = 0; r < a.nranks; ++r) {
       b.dx[r] = cols[first + r] > 0 ? dlogits[first + r] : nullptr;
       b.dxStride[r] = (int64_t)(dstrides ? dstrides[first + r] : cols[first + r]);
     }
     if (a.pieceStart[a.nranks] == 0) continue;
-    if (byType<LpBackward, const LpBackArgs&, bool, hipStream_t>(dtype, b, bytes > kLpStream, st) != hipSuccess)
+    if (byType<LpBackward, const LpBackArgs<kLpRanks>&, bool, hipStream_t>(dtype, b, bytes > kLpStream, st) != hipSuccess)
       return arHipError;
   }
   return arSuccess;

@@ -41,28 +41,58 @@ constexpr int kPolFewEach = 5;
 // 256 5.0 (6.4), x 512 6.3 (6.6); 6000 of one rank 7.6 (6.2).
 constexpr int kPolFew = kPolFewBlock * kPolFewEach - kOpRanks * kWave;
 
-// What both passes need; the second one no more.
+// Ranks of a launch at most.  Up to kOpRanks of them travel in arguments of
+// that size, which take less time to hand over (1250 tokens of 4 ranks 4.4 us,
+// 4.6 with twice the size; 20 ranks 6.5, 18 in two launches and a third).
+constexpr int kPolRanks = 2 * kOpRanks;
+
 struct PolCall {
-  float* dlogp[kOpRanks];              // null pointers: not wanted
-  int start[kOpRanks + 1];             // rank r has tokens [start[r], start[r + 1]) of the launch
-  int blockStart[kOpRanks + 1];        // and workgroups [blockStart[r], blockStart[r + 1])
   int nranks;
   int partials;                        // of all launches
   double* partial;                     // kPolSums rows of `partials`; the first pass: from this launch's first
   float* stats;                        // where the launch writes them, or null
   double klCoef, denominator, gradScale;
   double over;                         // what the sums are divided by, where the host knows it; else 0
-};
-
-struct PolArgs : PolCall {
-  const float* logp[kOpRanks];
-  const float* old[kOpRanks];
-  const float* ref[kOpRanks];          // null pointers: no KL term
-  const float* advantage[kOpRanks];
-  const float* weight[kOpRanks];       // null pointers: 1
-  bool hasRef;
   double logLow, logHigh;              // log(1 - low), log(1 + high)
   float low, high;                     // 1 - low, 1 + high
+  bool hasRef;
+};
+
+// What the second pass needs, and what the first needs besides.
+template <int RANKS>
+struct PolGradArgs : PolCall {
+  float* dlogp[RANKS];                 // null pointers: not wanted
+  int start[RANKS + 1];                // rank r has tokens [start[r], start[r + 1]) of the launch
+  int blockStart[RANKS + 1];           // and workgroups [blockStart[r], blockStart[r + 1])
+};
+
+template <int RANKS>
+struct PolArgs : PolGradArgs<RANKS> {
+  const float* logp[RANKS];
+  const float* old[RANKS];
+  const float* ref[RANKS];             // null pointers: no KL term
+  const float* advantage[RANKS];
+  const float* weight[RANKS];          // null pointers: 1
+
+  // Those of another size, whose ranks fit.
+  template <int OTHER>
+  static PolArgs of(const PolArgs<OTHER>& a) {
+    PolArgs to{};
+    (PolCall&)to = a;
+    for (int r = 0; r < a.nranks; ++r) {
+      to.dlogp[r] = a.dlogp[r];
+      to.logp[r] = a.logp[r];
+      to.old[r] = a.old[r];
+      to.ref[r] = a.ref[r];
+      to.advantage[r] = a.advantage[r];
+      to.weight[r] = a.weight[r];
+    }
+    for (int r = 0; r <= a.nranks; ++r) {
+      to.start[r] = a.start[r];
+      to.blockStart[r] = a.blockStart[r];
+    }
+    return to;
+  }
 };
 
 typedef int Halves __attribute__((ext_vector_type(2)));   // of 64 bits
@@ -88,7 +118,7 @@ __device__ __forceinline__ float2 expLess(float d) {
   return make_float2(small ? near + d : e, small ? near : e - d);
 }
 
-__device__ __forceinline__ Token tokenOf(const PolArgs& a, float logp, float old, float advantage, bool hasRef,
+__device__ __forceinline__ Token tokenOf(const PolCall& a, float logp, float old, float advantage, bool hasRef,
                                          float ref) {
   Token t;
   const double change = (double)logp - (double)old;
@@ -176,7 +206,7 @@ __device__ __forceinline__ double laneOf(double v, int lane) {
 
 // Adds a token up and returns its gradient short of the common factor.  One of
 // weight 0 is left out, whatever its other values are.
-__device__ __forceinline__ float addToken(const PolArgs& a, float logp, float old, float advantage, bool hasRef,
+__device__ __forceinline__ float addToken(const PolCall& a, float logp, float old, float advantage, bool hasRef,
                                           float ref, float weight, double (&s)[kPolSums]) {
   const Token t = tokenOf(a, logp, old, advantage, hasRef, ref);
   const bool counts = weight != 0.0f;
@@ -218,7 +248,8 @@ struct PolPlace {
   int64_t first, step;
 };
 
-__device__ __forceinline__ PolPlace polPlace(const PolCall& a) {
+template <int RANKS>
+__device__ __forceinline__ PolPlace polPlace(const PolGradArgs<RANKS>& a) {
   PolPlace p;
   p.rank = 0;
   while ((int)blockIdx.x >= a.blockStart[p.rank + 1]) ++p.rank;
@@ -240,9 +271,10 @@ __device__ __forceinline__ void forTokens(const PolPlace& p, int done, F f, G g)
   if (i < p.count) g(i);
 }
 
-__global__ void __launch_bounds__(kPolBlock) policySums(const PolArgs a) {
+template <int RANKS>
+__global__ void __launch_bounds__(kPolBlock) policySums(const PolArgs<RANKS> a) {
   __shared__ double lds[kPolBlock / kWave * kPolSums];
-  const PolPlace at = polPlace(a);
+  const PolPlace at = polPlace<RANKS>(a);
   const float *logp = a.logp[at.rank], *old = a.old[at.rank], *ref = a.ref[at.rank];
   const float *advantage = a.advantage[at.rank], *weight = a.weight[at.rank];
   float* dlogp = a.dlogp[at.rank];
@@ -277,7 +309,8 @@ __global__ void __launch_bounds__(kPolBlock) policySums(const PolArgs a) {
 // The sums of the first pass in one order for every workgroup: what each
 // gradient's factor needs of them, and, where the launch writes the stats, all
 // of them in its last workgroup, which has no tokens.
-__global__ void __launch_bounds__(kPolBlock) policyGrad(const PolCall a) {
+template <int RANKS>
+__global__ void __launch_bounds__(kPolBlock) policyGrad(const PolGradArgs<RANKS> a) {
   typedef FloatVec<kPolVec> Vec;
   if (a.stats && blockIdx.x == gridDim.x - 1) {
     __shared__ double lds[kPolBlock / kWave * kPolSums];
@@ -317,7 +350,8 @@ __global__ void __launch_bounds__(kPolBlock) policyGrad(const PolCall a) {
 
 // Few tokens: one workgroup, one launch, the gradients kept in registers until
 // their factor is known.  A wavefront takes 64 tokens of a rank at a time.
-__global__ void __launch_bounds__(kPolFewBlock) policyFew(const PolArgs a) {
+template <int RANKS>
+__global__ void __launch_bounds__(kPolFewBlock) policyFew(const PolArgs<RANKS> a) {
   constexpr int WAVES = kPolFewBlock / kWave;
   __shared__ double lds[WAVES * kPolSums];
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave), lane = (int)threadIdx.x % kWave;
@@ -361,26 +395,32 @@ int polBlocks(int64_t tokens) {
   return (int)(full <= kPolOnce ? full : kPolGrid);
 }
 
-bool polFew(const Shape& s) { return s.total == 0 || (s.launches == 1 && s.total <= kPolFew); }
+// Of more than kOpRanks ranks less, since each may leave 63 threads of a part.
+bool polFew(const Shape& s, int nranks) {
+  if (s.total == 0) return true;
+  return nranks <= kPolRanks && s.total <= kPolFew - (nranks > kOpRanks ? (kPolRanks - kOpRanks) * kWave : 0);
+}
+
+int polLaunches(int nranks) { return (nranks + kPolRanks - 1) / kPolRanks; }
 
 arResult_t polWorkspace(const size_t* tokens, int nranks, size_t* bytes) {
   Shape s;
   if (bytes == nullptr || !rowsOk(tokens, nranks, &s)) return arInvalidArgument;
   size_t partials = 0;
-  if (!polFew(s))
-    for (int l = 0; l < s.launches; ++l) {
-      const int64_t n = rowsOfLaunch(tokens, nranks, l * kOpRanks);
+  if (!polFew(s, nranks))
+    for (int l = 0; l < polLaunches(nranks); ++l) {
+      const int64_t n = rowsOfLaunch(tokens, nranks, l * kPolRanks, kPolRanks);
       const int most = n > 0 ? polBlocks(n) : 0;
-      partials += (size_t)(most > 0 && most < kOpRanks ? kOpRanks : most);   // one at least for each rank with tokens
+      partials += (size_t)(most > 0 && most < kPolRanks ? kPolRanks : most);   // one at least for each rank with tokens
     }
   *bytes = partials * kPolSums * sizeof(double);
   return arSuccess;
 }
 
-void fillTokens(PolArgs* a, const float* const* logp, const float* const* old, const float* const* ref,
+void fillTokens(PolArgs<kPolRanks>* a, const float* const* logp, const float* const* old, const float* const* ref,
                 const float* const* advantage, const float* const* weight, float* const* dlogp, const size_t* tokens,
                 int nranks, int first, bool few) {
-  a->nranks = nranks - first < kOpRanks ? nranks - first : kOpRanks;
+  a->nranks = nranks - first < kPolRanks ? nranks - first : kPolRanks;
   a->start[0] = 0;
   for (int r = 0; r < a->nranks; ++r) {
     const int k = first + r;
@@ -398,6 +438,13 @@ void fillTokens(PolArgs* a, const float* const* logp, const float* const* old, c
     for (int r = 0; r < a->nranks; ++r) a->blockStart[r + 1] = a->blockStart[r] + ((int)tokens[r] + kWave - 1) / kWave;
   else if (n > 0) shareOut(a->start, a->nranks, kPolBlock * kPolVec, polBlocks(n), a->blockStart);
   else a->blockStart[a->nranks] = 0;
+}
+
+// With arguments of the size that the ranks need.
+template <typename A, typename B>
+bool polLaunch(void (*kernel)(A), void (*larger)(B), int grid, int block, const PolArgs<kPolRanks>& a, hipStream_t st) {
+  if (a.nranks > kOpRanks) return launchKernel<B>(larger, dim3(grid), dim3(block), a, st) == hipSuccess;
+  return launchKernel<A>(kernel, dim3(grid), dim3(block), PolArgs<kOpRanks>::of(a), st) == hipSuccess;
 }
 
 arResult_t policyLoss(const float* const* logp, const float* const* old, const float* const* ref,
@@ -426,7 +473,7 @@ arResult_t policyLoss(const float* const* logp, const float* const* old, const f
     if (dlogp != nullptr) ok = ok && addRows(v, dlogp[r], 1, n, n, 4, true, r);
   }
   if (!ok) return arInvalidArgument;
-  const bool few = polFew(s);
+  const bool few = polFew(s, nranks);
   if (!few) {
     size_t need = 0;
     const arResult_t r = polWorkspace(tokens, nranks, &need);
@@ -435,7 +482,7 @@ arResult_t policyLoss(const float* const* logp, const float* const* old, const f
     v.push_back(Extent{(uintptr_t)workspace, need, 1, need, true, -1});
   }
   if (outputsOverlap(v)) return arInvalidArgument;
-  PolArgs a{};
+  PolArgs<kPolRanks> a{};
   a.hasRef = ref != nullptr;
   a.low = (float)(1.0 - clipLow);
   a.high = (float)(1.0 + clipHigh);
@@ -448,31 +495,31 @@ arResult_t policyLoss(const float* const* logp, const float* const* old, const f
   if (few) {
     fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, 0, true);
     a.stats = stats;
-    return launchKernel(policyFew, dim3(1), dim3(kPolFewBlock), a, st) == hipSuccess ? arSuccess : arHipError;
+    return polLaunch(policyFew<kOpRanks>, policyFew<kPolRanks>, 1, kPolFewBlock, a, st) ? arSuccess : arHipError;
   }
-  for (int l = 0; l < s.launches; ++l) {
-    fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, l * kOpRanks, false);
+  for (int l = 0; l < polLaunches(nranks); ++l) {
+    fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, l * kPolRanks, false);
     a.partials += a.blockStart[a.nranks];
   }
   int partials = 0;
-  for (int l = 0; l < s.launches; ++l) {
-    fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, l * kOpRanks, false);
+  for (int l = 0; l < polLaunches(nranks); ++l) {
+    fillTokens(&a, logp, old, ref, advantage, weight, dlogp, tokens, nranks, l * kPolRanks, false);
     const int grid = a.blockStart[a.nranks];
     if (grid == 0) continue;
     a.partial = (double*)workspace + partials;
-    if (launchKernel(policySums, dim3(grid), dim3(kPolBlock), a, st) != hipSuccess) return arHipError;
+    if (!polLaunch(policySums<kOpRanks>, policySums<kPolRanks>, grid, kPolBlock, a, st)) return arHipError;
     partials += grid;
   }
   a.partial = (double*)workspace;
   // with a factor known beforehand the gradients are whole, and the stats are
   // left (8 x 262144 tokens without weights 14.5 us, with them 18.5)
   float* const* unscaled = a.over > 0.0 ? nullptr : dlogp;
-  for (int l = 0; l < s.launches; ++l) {
-    fillTokens(&a, logp, old, ref, advantage, weight, unscaled, tokens, nranks, l * kOpRanks, false);
+  for (int l = 0; l < polLaunches(nranks); ++l) {
+    fillTokens(&a, logp, old, ref, advantage, weight, unscaled, tokens, nranks, l * kPolRanks, false);
     a.stats = l == 0 ? stats : nullptr;
     const int grid = (unscaled != nullptr ? a.blockStart[a.nranks] : 0) + (l == 0 ? 1 : 0);
     if (grid == 0) continue;
-    if (launchKernel<PolCall>(policyGrad, dim3(grid), dim3(kPolBlock), a, st) != hipSuccess) return arHipError;
+    if (!polLaunch(policyGrad<kOpRanks>, policyGrad<kPolRanks>, grid, kPolBlock, a, st)) return arHipError;
   }
   return arSuccess;
 }

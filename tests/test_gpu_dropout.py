@@ -188,7 +188,7 @@ def test_replicas_draw_alike_and_ranks_do_not(B):
     assert torch.equal(run_forward(B, [torch.ones(128, cols, dtype=torch.float16)], None, None, p)[0].float(), whole)
 
 
-@pytest.mark.parametrize("n", [17, 40, 128])
+@pytest.mark.parametrize("n", [17, 32, 33, 40, 128])
 def test_many_ranks(B, n):
     rows, cols = [3 * r % 5 for r in range(n)], 130
     xs, zs, bs = inputs(rows, cols, torch.bfloat16, torch.float32, n)

@@ -39,10 +39,10 @@ def inputs(rows, shards, dt, seed, ignored=0.2, std=3.0):
     return xs, t
 
 
-@pytest.fixture(params=[(0, 0), (15, 0), (0, 1)], ids=["rows", "launches", "pieces"])
+@pytest.fixture(params=[(0, 0), (15, 0), (33, 0), (0, 1)], ids=["rows", "ranks", "launches", "pieces"])
 def form(request):
-    """The forms a call can take: one launch, several for more than 16 ranks, and for few rows of a long vocabulary
-    pieces of them."""
+    """The forms a call can take: one launch, one of more than 16 ranks, several for more than 32, and for few rows of
+    a long vocabulary pieces of them."""
     MORE[:] = request.param
     yield request.param
     MORE[:] = 0, 0
@@ -118,7 +118,8 @@ def test_few_rows(B, shards, dt, scale):
 
 @pytest.mark.parametrize("dt", DTYPES, ids=str)
 @pytest.mark.parametrize("rows,shards", [(1023, [500, 533]), (1024, [500, 533]), (1025, [3, 0, 1001]), (5000, [65]),
-                                         (70001, [9]), (1100, [9] * 17), (66000, [1, 1]), (3000, [2050, 77])], ids=str)
+                                         (70001, [9]), (1100, [9] * 17), (1100, [9] * 33), (4100, [130] * 20), (200, [700] * 32),
+                                         (66000, [1, 1]), (3000, [2050, 77])], ids=str)
 def test_many_rows(B, rows, shards, dt):
     xs, t = inputs(rows, shards, dt, rows)
     check_forward(run_forward(B, xs, t), xs, t)

@@ -62,7 +62,7 @@ def check(got, data, low=0.2, high=0.28, kl=0.05, denominator=0.0, scale=1.0, re
 
 
 @pytest.mark.parametrize("tokens", [[1], [2, 0, 1], [500, 375, 250, 0], [4096], [4097], [1000] * 5, [70000, 0, 1], [300000, 17],
-                                    [200] * 17, [3000] * 40, [1] * 128, [0] * 20 + [9]], ids=lambda t: "%dx%d" % (len(t), max(t)))
+                                    [200] * 17, [95] * 32, [97] * 32, [90] * 33, [3000] * 40, [1] * 128, [0] * 20 + [9]], ids=lambda t: "%dx%d" % (len(t), max(t)))
 def test_policy_loss(B, tokens):
     data = inputs(tokens, len(tokens))
     check(run(B, data), data)
