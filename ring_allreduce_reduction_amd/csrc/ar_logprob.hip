@@ -505,11 +505,15 @@ struct LpRows {
   // shard, 1 x 2000 6.3 and 4.6.  Wider ones leave a wavefront threads without a
   // vector (110000 x 8 x 1200 352 us, 587 with a wavefront a shard; 65536 x 8 x
   // 2056 383, 450; 50000 x 8 x 2600 354, 379; 40000 x 8 x 3000 327, 321) and ask for
-  // more rows (1200 x 8 x 2000 13.5, 11.6; 8192 46.6, 47.3).
+  // more rows (1200 x 8 x 2000 13.5, 11.6; 8192 46.6, 47.3); one to three gain less
+  // (16500 x 1 x 1316 12.4, 14.9; 5000 x 3 x 1500 15.0, 12.9; 40000 x 2 x 2800 79.8,
+  // 71.8).
   static bool narrow(const LpArgs<kLpRanks>& a) {
     constexpr int V = kVec<DT>;
     const int64_t columns = (a.colStart[a.nranks] - a.colStart[0]) / a.nranks;
-    return (columns <= 128 * V && a.rows >= 4 * kOpsCUs) || (columns <= 352 * V && a.rows >= 16 * kOpsCUs);
+    const bool few = a.nranks < 4;
+    return (columns <= 128 * V && a.rows >= 4 * kOpsCUs) ||
+           (columns <= (few ? 192 : 352) * V && a.rows >= (few ? 32 : 16) * kOpsCUs);
   }
   static hipError_t run(const LpArgs<kLpRanks>& all, bool stream, hipStream_t st) {
     constexpr int V = kVec<DT>;

@@ -128,7 +128,7 @@ def test_many_rows(B, rows, shards, dt):
 
 
 @pytest.mark.parametrize("dt", DTYPES, ids=str)
-@pytest.mark.parametrize("rows,shards", [(4096, [1100, 1409]), (4097, [1501, 1, 900, 2300, 703]), (4099, [2000])], ids=str)
+@pytest.mark.parametrize("rows,shards", [(8192, [700, 790]), (4097, [1501, 1, 900, 2300, 703]), (8200, [1400])], ids=str)
 def test_narrow_shards_of_very_many_rows(B, rows, shards, dt):
     """16 threads a shard, of few to all vectors they have in flight at a time."""
     xs, t = inputs(rows, shards, dt, rows)
