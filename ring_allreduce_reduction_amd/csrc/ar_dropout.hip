@@ -495,7 +495,7 @@ DropCut dropCut(int cols, int block, bool sums) {
   return best;
 }
 
-// Slices of the rows of a launch, at most (but one to each rank with rows).
+// Cuts the rows of a launch's ranks into slices, and returns their number.
 // Workgroups that come and go keep a closer window over memory than ones that
 // last: forward 245 us with 256 workgroups a CU in all, 262 with 128, 280 with
 // 32, 267-271 with 512 and more; backward 181 with 32 a CU, 187 with 16, 190
@@ -506,16 +506,17 @@ DropCut dropCut(int cols, int block, bool sums) {
 // Where up to half of the CUs would have a workgroup more than the others, its
 // rows are shared out among them all (312 workgroups 11.9 us, as 256 11.1; 580
 // 14.3, as 512 13.1; but 453 13.4, as 256 14.1), with tiles few enough to come near.
-int dropSlices(int64_t rows, const DropCut& k, bool sums) {
-  const int64_t once = k.together, each = sums && once < 32 ? (32 + once - 1) / once * once : once;
+int sliceRows(const size_t* rows, int ranks, const DropCut& k, bool sums, int* rowStart, int* sliceStart) {
+  rowStart[0] = sliceStart[0] = 0;
+  for (int r = 0; r < ranks; ++r) rowStart[r + 1] = rowStart[r] + (int)rows[r];
+  const int each = sums && k.together < 32 ? (32 + k.together - 1) / k.together * k.together : k.together;
   int64_t most = (sums ? 32 : 256) * kOpsCUs / k.tiles;
-  const int64_t full = (rows + each - 1) / each;
   if (sums && most > 2 * kOpsCUs) most = 2 * kOpsCUs;
-  int64_t n = full < most ? full : most < 1 ? 1 : most;
-  const int64_t grid = n * k.tiles;
+  if (most < 1) most = 1;
+  const int64_t grid = (wholeGroups(rowStart, ranks, each) < most ? wholeGroups(rowStart, ranks, each) : most) * k.tiles;
   if (sums && k.tiles <= kOpsCUs / 8 && grid > kOpsCUs && grid % kOpsCUs <= kOpsCUs / 2)
-    n = grid / kOpsCUs * kOpsCUs / k.tiles;
-  return (int)n;
+    most = grid / kOpsCUs * kOpsCUs / k.tiles;
+  return giveOut(rowStart, ranks, each, k.together, (int)most, sliceStart);
 }
 
 // Calls that move more than the caches hold load and store past them: 8 x 4096
@@ -608,19 +609,15 @@ int fillDropRows(DropArgs<kDropRanks>* a, const size_t* rows, const uint64_t* fi
   a->nranks = nranks - first < most ? nranks - first : most;
   uint64_t next = 0;
   for (int r = 0; r < first; ++r) next += rows[r];
-  a->rowStart[0] = 0;
   for (int r = 0; r < a->nranks; ++r) {
-    a->rowStart[r + 1] = a->rowStart[r] + (int)rows[first + r];
     a->firstRow[r] = (uint32_t)(firstRow ? firstRow[first + r] : next);
     next += rows[first + r];
   }
   a->cols = (int)cols;
   a->partialCols = (int)((cols + 7) / 8 * 8);
-  const DropCut k = dropCut((int)cols, sums ? kDropBackBlock : kDropBlock, sums);
-  a->cut = k;
-  a->overAcross = k.together > 1 ? 1.0f / (float)k.across : 0.0f;
-  const int64_t n = a->rowStart[a->nranks];
-  return n == 0 ? 0 : shareOut(a->rowStart, a->nranks, k.together, dropSlices(n, k, sums), a->sliceStart);
+  a->cut = dropCut((int)cols, sums ? kDropBackBlock : kDropBlock, sums);
+  a->overAcross = a->cut.together > 1 ? 1.0f / (float)a->cut.across : 0.0f;
+  return sliceRows(rows + first, a->nranks, a->cut, sums, a->rowStart, a->sliceStart);
 }
 
 // The grid.  Tiles whose ends are not those of 128-byte lines share lines with
@@ -693,11 +690,9 @@ arResult_t dropWorkspace(const size_t* rows, int nranks, size_t cols, size_t* by
   const DropCut k = dropCut((int)cols, kDropBackBlock, true);
   size_t slices = 0;
   const int ranks = dropRanks(cols);
-  for (int first = 0; first < nranks; first += ranks) {
-    const int64_t n = rowsOfLaunch(rows, nranks, first, ranks);
-    const int most = n > 0 ? dropSlices(n, k, true) : 0;
-    slices += (size_t)(most > 0 && most < ranks ? ranks : most);   // one at least for each rank with rows
-  }
+  int rowStart[kDropRanks + 1], sliceStart[kDropRanks + 1];
+  for (int first = 0; first < nranks; first += ranks)
+    slices += (size_t)sliceRows(rows + first, nranks - first < ranks ? nranks - first : ranks, k, true, rowStart, sliceStart);
   *bytes = (slices > 0 ? slices : 1) * ((cols + 7) / 8 * 8) * sizeof(float);
   return arSuccess;
 }

@@ -389,10 +389,14 @@ __global__ void __launch_bounds__(kPolFewBlock) policyFew(const PolArgs<RANKS> a
     if (any[k] && dlogp[k]) *dlogp[k] = timesFactor(d[k], factor);
 }
 
-// Workgroups, and partial sums, of a launch of `tokens` tokens.
-int polBlocks(int64_t tokens) {
-  const int64_t full = (tokens + kPolBlock * kPolVec - 1) / (kPolBlock * kPolVec);
-  return (int)(full <= kPolOnce ? full : kPolGrid);
+// Shares a launch's tokens out among its workgroups, one partial sum each, or,
+// `few`, among a workgroup's wavefronts; returns their number.
+int cutTokens(const size_t* tokens, int ranks, bool few, int* start, int* blockStart) {
+  const int each = few ? kWave : kPolBlock * kPolVec;
+  start[0] = blockStart[0] = 0;
+  for (int r = 0; r < ranks; ++r) start[r + 1] = start[r] + (int)tokens[r];
+  const int most = wholeGroups(start, ranks, each) <= kPolOnce ? kPolOnce : kPolGrid;
+  return giveOut(start, ranks, each, each, most, blockStart);
 }
 
 // Of more than kOpRanks ranks less, since each may leave 63 threads of a part.
@@ -407,12 +411,11 @@ arResult_t polWorkspace(const size_t* tokens, int nranks, size_t* bytes) {
   Shape s;
   if (bytes == nullptr || !rowsOk(tokens, nranks, &s)) return arInvalidArgument;
   size_t partials = 0;
+  int start[kPolRanks + 1], blockStart[kPolRanks + 1];
   if (!polFew(s, nranks))
-    for (int l = 0; l < polLaunches(nranks); ++l) {
-      const int64_t n = rowsOfLaunch(tokens, nranks, l * kPolRanks, kPolRanks);
-      const int most = n > 0 ? polBlocks(n) : 0;
-      partials += (size_t)(most > 0 && most < kPolRanks ? kPolRanks : most);   // one at least for each rank with tokens
-    }
+    for (int first = 0; first < nranks; first += kPolRanks)
+      partials += (size_t)cutTokens(tokens + first, nranks - first < kPolRanks ? nranks - first : kPolRanks,
+                                    false, start, blockStart);
   *bytes = partials * kPolSums * sizeof(double);
   return arSuccess;
 }
@@ -421,11 +424,10 @@ void fillTokens(PolArgs<kPolRanks>* a, const float* const* logp, const float* co
                 const float* const* advantage, const float* const* weight, float* const* dlogp, const size_t* tokens,
                 int nranks, int first, bool few) {
   a->nranks = nranks - first < kPolRanks ? nranks - first : kPolRanks;
-  a->start[0] = 0;
+  cutTokens(tokens + first, a->nranks, few, a->start, a->blockStart);
   for (int r = 0; r < a->nranks; ++r) {
     const int k = first + r;
     const bool any = tokens[k] > 0;
-    a->start[r + 1] = a->start[r] + (int)tokens[k];
     a->logp[r] = any ? logp[k] : nullptr;
     a->old[r] = any ? old[k] : nullptr;
     a->ref[r] = any && ref ? ref[k] : nullptr;
@@ -433,11 +435,6 @@ void fillTokens(PolArgs<kPolRanks>* a, const float* const* logp, const float* co
     a->weight[r] = any && weight ? weight[k] : nullptr;
     a->dlogp[r] = any && dlogp ? dlogp[k] : nullptr;
   }
-  const int64_t n = a->start[a->nranks];
-  if (few)   // a wavefront's parts
-    for (int r = 0; r < a->nranks; ++r) a->blockStart[r + 1] = a->blockStart[r] + ((int)tokens[r] + kWave - 1) / kWave;
-  else if (n > 0) shareOut(a->start, a->nranks, kPolBlock * kPolVec, polBlocks(n), a->blockStart);
-  else a->blockStart[a->nranks] = 0;
 }
 
 // With arguments of the size that the ranks need.

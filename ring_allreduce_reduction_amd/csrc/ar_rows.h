@@ -89,6 +89,23 @@ inline int shareOut(const int* rowStart, int nranks, int groups, int most, int* 
   return blockStart[nranks];
 }
 
+// Groups of `groups` rows that all ranks' rows make, none of two ranks'.
+inline int64_t wholeGroups(const int* rowStart, int nranks, int groups) {
+  int64_t n = 0;
+  for (int r = 0; r < nranks; ++r) n += ((int64_t)rowStart[r + 1] - rowStart[r] + groups - 1) / groups;
+  return n;
+}
+
+// As shareOut, but where `most` are enough each rank has a workgroup for every
+// `each` of its rows.
+inline int giveOut(const int* rowStart, int nranks, int each, int groups, int most, int* blockStart) {
+  if (wholeGroups(rowStart, nranks, each) > most) return shareOut(rowStart, nranks, groups, most, blockStart);
+  blockStart[0] = 0;
+  for (int r = 0; r < nranks; ++r)
+    blockStart[r + 1] = blockStart[r] + (int)(((int64_t)rowStart[r + 1] - rowStart[r] + each - 1) / each);
+  return blockStart[nranks];
+}
+
 template <template <int, int> class F, typename... A>
 hipError_t byTypes(int dtype, int wtype, A... args) {
   if (wtype == arFloat32) {
