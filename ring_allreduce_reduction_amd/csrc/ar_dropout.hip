@@ -501,15 +501,19 @@ DropCut dropCut(int cols, int block, bool sums) {
 // 32, 267-271 with 512 and more; backward 181 with 32 a CU, 187 with 16, 190
 // with 8, 185 with 64.  Backward a slice costs a row of partial sums to write
 // and read, so it has 32 rows at least (2537 rows of 2047 11.8 us; 16 rows 11.7,
-// 64 13.2; of 2048 11.0, 11.3, 11.3) and there are at most two a CU (160000 rows
-// of 100 21 us, 23 with four, 28 with eight, 44 with 20; of 512 66, 69, 68, 78).
+// 64 13.2; of 2048 11.0, 11.3, 11.3), but 16 or 8 where a quarter of the CUs would
+// have none (3000 x 924 fp16 11.5 us, 9.2 so; 8 ranks' 84-0 x 12119 16.6, 10.7), and
+// there are at most two a CU (160000 rows of 100 21 us, 23 with four, 28 with
+// eight, 44 with 20; of 512 66, 69, 68, 78).
 // Where up to half of the CUs would have a workgroup more than the others, its
 // rows are shared out among them all (312 workgroups 11.9 us, as 256 11.1; 580
 // 14.3, as 512 13.1; but 453 13.4, as 256 14.1), with tiles few enough to come near.
 int sliceRows(const size_t* rows, int ranks, const DropCut& k, bool sums, int* rowStart, int* sliceStart) {
   rowStart[0] = sliceStart[0] = 0;
   for (int r = 0; r < ranks; ++r) rowStart[r + 1] = rowStart[r] + (int)rows[r];
-  const int each = sums && k.together < 32 ? (32 + k.together - 1) / k.together * k.together : k.together;
+  int least = 32;   // rows of a slice with sums
+  while (least > 8 && wholeGroups(rowStart, ranks, least) * k.tiles < 3 * kOpsCUs / 4) least /= 2;
+  const int each = sums && k.together < least ? (least + k.together - 1) / k.together * k.together : k.together;
   int64_t most = (sums ? 32 : 256) * kOpsCUs / k.tiles;
   if (sums && most > 2 * kOpsCUs) most = 2 * kOpsCUs;
   if (most < 1) most = 1;
