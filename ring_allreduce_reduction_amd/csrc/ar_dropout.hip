@@ -607,8 +607,8 @@ void fillDraw(DropCall* a, double p, uint64_t seed, uint64_t offset, const uint6
 int dropRanks(size_t cols) { return cols <= (size_t)1 << 26 ? kDropRanks : 1; }
 
 // This launch's rows and their slices; returns the grid's slices.
-int fillDropRows(DropArgs<kDropRanks>* a, const size_t* rows, const uint64_t* firstRow, int nranks, int first, size_t cols,
-                 bool sums) {
+int fillDropRows(DropArgs<kDropRanks>* a, const size_t* rows, const uint64_t* firstRow, int nranks, int first,
+                 size_t cols, bool sums) {
   const int most = dropRanks(cols);
   a->nranks = nranks - first < most ? nranks - first : most;
   uint64_t next = 0;

@@ -51,9 +51,9 @@ inline bool strideOk(size_t stride, size_t cols) { return stride >= cols && stri
 
 inline bool aligned(const void* p, int esz) { return p != nullptr && (uintptr_t)p % (uintptr_t)esz == 0; }
 
-inline int64_t rowsOfLaunch(const size_t* rows, int nranks, int first, int ranks = kOpRanks) {
+inline int64_t rowsOfLaunch(const size_t* rows, int nranks, int first) {
   int64_t n = 0;
-  for (int r = first; r < nranks && r < first + ranks; ++r) n += (int64_t)rows[r];
+  for (int r = first; r < nranks && r < first + kOpRanks; ++r) n += (int64_t)rows[r];
   return n;
 }
 
