@@ -131,7 +131,8 @@ __device__ __forceinline__ Token tokenOf(const PolCall& a, float logp, float old
   if (hasRef) {
     const float2 less = expLess((float)((double)ref - (double)logp));
     t.kl = less.y;
-    t.dlogp -= (float)a.klCoef * less.x;
+    // of coefficient 0 it is only reported, and may be infinite
+    if (a.klCoef != 0.0) t.dlogp -= (float)a.klCoef * less.x;
   }
   return t;
 }
@@ -228,7 +229,7 @@ __device__ __forceinline__ void putStats(const PolCall& a, double sums) {
   const double weights = laneOf(sums, 0), loss = laneOf(sums, 1), klSum = laneOf(sums, 2), clipped = laneOf(sums, 3);
   if (threadIdx.x > 0) return;
   const double part = partOf(a, weights), policy = loss * part, kl = klSum * part;
-  a.stats[0] = (float)(policy + a.klCoef * kl);
+  a.stats[0] = (float)(a.klCoef != 0.0 ? policy + a.klCoef * kl : policy);
   a.stats[1] = (float)policy;
   a.stats[2] = (float)kl;
   a.stats[3] = (float)(clipped * part);

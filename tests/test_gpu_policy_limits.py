@@ -1,0 +1,46 @@
+"""The policy loss where a number is past what 32 bits hold and at the ends of its arguments' ranges: in one
+workgroup, in two passes, and with the denominator known beforehand."""
+import math
+
+import pytest
+import test_gpu_policy as pol
+import torch
+from test_gpu_policy import B, _named  # noqa: F401  (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+FORMS = [([600, 8], {}), ([9000, 100], {}), ([9000, 100], dict(denominator=64.0)), ([40, 2] * 9, {}), ([700] * 18, {})]
+forms = pytest.mark.parametrize("tokens,kw", FORMS, ids=["few", "two passes", "known", "few of 18 ranks", "18 ranks"])
+
+
+def inputs(tokens, seed):
+    """Tokens 0 to 7 of the first rank have a weight."""
+    data = pol.inputs(tokens, seed)
+    data[4][0][:8] = 1.0
+    return data
+
+
+def same(a, b):
+    return torch.equal(a[0], b[0]) and all(torch.equal(x, y) for x, y in zip(a[1], b[1]))
+
+
+@forms
+def test_a_kl_of_coefficient_0_is_only_reported(B, tokens, kw):  # noqa: F811
+    """However large it is: the loss and the gradient are those without a reference."""
+    data = inputs(tokens, 1)
+    logp, old, ref, adv, w = data
+    ref[0][0], ref[0][1], ref[0][2] = logp[0][0] + 200.0, logp[0][1] + 88.8, 3e38
+    want = pol.run(B, data, ref=False, **kw)
+    stats, out = pol.run(B, data, kl=0.0, **kw)
+    assert stats[2].item() == math.inf
+    assert torch.equal(stats[[0, 1, 3, 4]], want[0][[0, 1, 3, 4]]) and all(torch.equal(a, b) for a, b in zip(out, want[1]))
+    pol.check(want, data, ref=False, **kw)
+    # with a coefficient it counts
+    stats, out = pol.run(B, data, kl=0.5, **kw)
+    assert stats[0].item() == math.inf and out[0][0].item() == -math.inf
+    # a token that the policy's mask rules out
+    logp[0][3], logp[0][4], adv[0][3], adv[0][4] = -math.inf, -math.inf, 1.0, -1.0
+    want = pol.run(B, data, ref=False, **kw)
+    stats, out = pol.run(B, data, kl=0.0, **kw)
+    assert torch.isfinite(want[0]).all() and all(torch.isfinite(t).all() for t in out)
+    assert torch.equal(stats[[0, 1, 3, 4]], want[0][[0, 1, 3, 4]]) and all(torch.equal(a, b) for a, b in zip(out, want[1]))
