@@ -805,6 +805,8 @@ arResult_t arTokenLogprobBackward(const float* dlogp, const void* const* logits,
  * g = 0 where A > 0 and ratio > 1 + clipHigh or A < 0 and ratio < 1 - clipLow
  * (clipped), else -A ratio.
  *  logp, old, advantage  (host arrays of nranks device pointers) tokens[r] floats.
+ *            With an advantage of 0 a token's loss and g are 0, whatever its ratio is,
+ *            also where that is infinite.
  *  ref       (host array, or NULL: no KL term, klCoef must be 0).
  *  weight    (host array, or NULL: 1) >= 0.  A token of weight 0 is left out:
  *            nothing else of it is looked at, and its dlogp is 0.

@@ -123,7 +123,11 @@ __device__ __forceinline__ Token tokenOf(const PolCall& a, float logp, float old
   Token t;
   const double change = (double)logp - (double)old;
   const bool up = advantage > 0.0f && change > a.logHigh, down = advantage < 0.0f && change < a.logLow;
-  const float ratio = expFast((float)change);
+  // An advantage of 0 takes no part, not of an infinite ratio either.  Without a
+  // branch: 8 x 262144 tokens 16.3 us, 19.0 with one.
+  const float e = expFast((float)change);
+  const bool idle = (advantage == 0.0f) & (e == INFINITY);
+  const float ratio = idle ? 0.0f : e;
   t.clipped = up || down;
   t.loss = -advantage * (up ? a.high : down ? a.low : ratio);
   t.dlogp = t.clipped ? 0.0f : -advantage * ratio;

@@ -44,3 +44,23 @@ def test_a_kl_of_coefficient_0_is_only_reported(B, tokens, kw):  # noqa: F811
     stats, out = pol.run(B, data, kl=0.0, **kw)
     assert torch.isfinite(want[0]).all() and all(torch.isfinite(t).all() for t in out)
     assert torch.equal(stats[[0, 1, 3, 4]], want[0][[0, 1, 3, 4]]) and all(torch.equal(a, b) for a, b in zip(out, want[1]))
+
+
+@forms
+def test_an_advantage_of_0_takes_no_part(B, tokens, kw):  # noqa: F811
+    """Whatever the ratio is; but a log-probability that is no number is not hidden."""
+    data = inputs(tokens, 2)
+    logp, old, ref, adv, w = data
+    adv[0][:6] = torch.tensor([0.0, -0.0, 0.0, 0.0, 0.0, 0.0])
+    near = [t.clone() for t in logp]
+    near[0][:6] = old[0][:6]
+    logp[0][:4] = old[0][:4] + torch.tensor([200.0, 800.0, 88.8, 3e38])
+    want = pol.run(B, (near, old, ref, adv, w), ref=False, **kw)
+    pol.check(want, (near, old, ref, adv, w), ref=False, **kw)
+    assert same(pol.run(B, data, ref=False, **kw), want)
+    rare = [t.clone() for t in old]
+    rare[0][4] = -math.inf
+    assert same(pol.run(B, (logp, rare, ref, adv, w), ref=False, **kw), want)
+    logp[0][5] = math.nan
+    stats, out = pol.run(B, data, ref=False, **kw)
+    assert torch.isnan(stats[1]) and torch.isnan(out[0][5]) and sum(torch.isnan(t).sum().item() for t in out) == 1
