@@ -808,6 +808,8 @@ arResult_t arTokenLogprobBackward(const float* dlogp, const void* const* logits,
  *            With an advantage of 0 a token's loss and g are 0, whatever its ratio is,
  *            also where that is infinite.
  *  ref       (host array, or NULL: no KL term, klCoef must be 0).
+ *            A token that either logp or ref holds at -inf has an infinite kl, one that
+ *            both do none (NaN).
  *  weight    (host array, or NULL: 1) >= 0.  A token of weight 0 is left out:
  *            nothing else of it is looked at, and its dlogp is 0.
  *  dlogp     (host array, or NULL) tokens[r] floats; dlogp[r] may be logp[r].

@@ -106,8 +106,10 @@ __device__ __forceinline__ float expFast(float x) { return __builtin_amdgcn_exp2
 
 // exp(d) - 1 and exp(d) - 1 - d, below |d| = 1 from the exponential's series
 // through d^12 (what is left out is 2^-31 of the result): there they are
-// differences of nearly equal numbers.
+// differences of nearly equal numbers.  An infinite d counts as the largest
+// number: its exponential outgrows it.
 __device__ __forceinline__ float2 expLess(float d) {
+  d = __builtin_elementwise_minimum(d, 0x1.fffffep127f);   // NaN stays
   constexpr double kOver[13] = {0, 0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320,
                                 1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600};
   float s = (float)kOver[12];

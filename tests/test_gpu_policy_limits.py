@@ -64,3 +64,20 @@ def test_an_advantage_of_0_takes_no_part(B, tokens, kw):  # noqa: F811
     logp[0][5] = math.nan
     stats, out = pol.run(B, data, ref=False, **kw)
     assert torch.isnan(stats[1]) and torch.isnan(out[0][5]) and sum(torch.isnan(t).sum().item() for t in out) == 1
+
+
+@forms
+def test_an_infinite_difference_has_an_infinite_kl(B, tokens, kw):  # noqa: F811
+    """A token that the mask of the policy or of the reference rules out."""
+    for where in (0, 2):
+        data = inputs(tokens, 3)
+        data[where][0][2] = -math.inf
+        data[3][0][2] = 1.0
+        stats, out = pol.run(B, data, kl=0.5, **kw)
+        assert stats[2].item() == math.inf and stats[0].item() == math.inf and torch.isfinite(stats[[1, 3, 4]]).all()
+        assert out[0][2].item() == -math.inf if where == 0 else torch.isfinite(out[0][2])
+        out[0][2] = 0.0
+        assert all(torch.isfinite(t).all() for t in out)
+        data[0][0][2] = data[2][0][2] = -math.inf   # by both: no difference
+        stats, out = pol.run(B, data, kl=0.5, **kw)
+        assert torch.isnan(stats[[0, 2]]).all() and torch.isnan(out[0][2])
