@@ -827,8 +827,10 @@ arResult_t arTokenLogprobBackward(const float* dlogp, const void* const* logits,
  *  workspace, workspaceBytes  see above; may be NULL / 0 where
  *            arPolicyLossWorkspace reports 0.
  * Which tokens are clipped is decided in 64 bits, so that it does not depend on
- * roundings; all sums are in 64 bits; a token's terms are formed in 32 (a ratio
- * past 3.4e38 is infinite), a small kl with all its bits.
+ * roundings; all sums are in 64 bits; a token's terms, g and kl are formed in 32
+ * (a ratio past 3.4e38 is infinite; one of exp(d) is off by up to 2^-24 (2.5 |d| + 4)
+ * of itself), a small kl with all its bits; gradScale w / D is in 64 bits and
+ * dlogp rounded once more, so that a scale common to all weights does not matter.
  * Outputs must not overlap any other buffer.  Errors: as arTokenLogprob.
  */
 arResult_t arPolicyLoss(const float* const* logp, const float* const* old, const float* const* ref,

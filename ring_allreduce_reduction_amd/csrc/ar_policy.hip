@@ -8,8 +8,10 @@
 //   L = sum w (loss + beta kl) / W,  W = the sum of all weights or given,
 //   dL/dl = w / W (-A r [not clipped] + beta (1 - exp(f - l))).
 // The mean is over all ranks, so the gradient's factor is a sum over every
-// token: the first pass leaves the sums and the gradients short of that factor,
-// the second multiplies them by it.  Whether a ratio passes a bound is decided
+// token: the first pass leaves the sums and the gradients short of that factor
+// and of their weights, the second multiplies them by both (reading the weights
+// again: 8 x 262144 tokens 16.9 us, 16.3 where the first pass applied them in 32
+// bits, which weights far from 1 leave).  Whether a ratio passes a bound is decided
 // by differences in 64 bits against the bounds' logarithms, since these are
 // numbers that may nearly agree; the sums are in 64 bits; what lies between is
 // formed in 32, kl by its series where it is a difference of nearly equal
@@ -62,6 +64,7 @@ struct PolCall {
 template <int RANKS>
 struct PolGradArgs : PolCall {
   float* dlogp[RANKS];                 // null pointers: not wanted
+  const float* weight[RANKS];          // null pointers: 1
   int start[RANKS + 1];                // rank r has tokens [start[r], start[r + 1]) of the launch
   int blockStart[RANKS + 1];           // and workgroups [blockStart[r], blockStart[r + 1])
 };
@@ -72,7 +75,6 @@ struct PolArgs : PolGradArgs<RANKS> {
   const float* old[RANKS];
   const float* ref[RANKS];             // null pointers: no KL term
   const float* advantage[RANKS];
-  const float* weight[RANKS];          // null pointers: 1
 
   // Those of another size, whose ranks fit.
   template <int OTHER>
@@ -211,8 +213,8 @@ __device__ __forceinline__ double laneOf(double v, int lane) {
   return __builtin_bit_cast(double, Halves{__builtin_amdgcn_readlane(b[0], lane), __builtin_amdgcn_readlane(b[1], lane)});
 }
 
-// Adds a token up and returns its gradient short of the common factor.  One of
-// weight 0 is left out, whatever its other values are.
+// Adds a token up and returns its gradient short of its weight and the common
+// factor.  One of weight 0 is left out, whatever its other values are.
 __device__ __forceinline__ float addToken(const PolCall& a, float logp, float old, float advantage, bool hasRef,
                                           float ref, float weight, double (&s)[kPolSums]) {
   const Token t = tokenOf(a, logp, old, advantage, hasRef, ref);
@@ -222,7 +224,7 @@ __device__ __forceinline__ float addToken(const PolCall& a, float logp, float ol
   s[1] = fma(w, (double)(counts ? t.loss : 0.0f), s[1]);
   s[2] = fma(w, (double)(counts ? t.kl : 0.0f), s[2]);
   s[3] += t.clipped ? w : 0.0;
-  return counts ? weight * t.dlogp : 0.0f;
+  return counts ? t.dlogp : 0.0f;
 }
 
 __device__ __forceinline__ double partOf(const PolCall& a, double weights) {
@@ -242,10 +244,10 @@ __device__ __forceinline__ void putStats(const PolCall& a, double sums) {
   a.stats[4] = (float)weights;
 }
 
-// A gradient and the factor it was short of; 0 where nothing counts, whatever
-// the gradient is.
-__device__ __forceinline__ float timesFactor(float d, double factor) {
-  return factor != 0.0 ? (float)((double)d * factor) : 0.0f;
+// A gradient and what it was short of, in 64 bits, since all weights and their
+// sum may be far from 1; 0 where nothing counts, whatever the gradient is.
+__device__ __forceinline__ float timesFactor(float d, float weight, double factor) {
+  return factor != 0.0 ? (float)((double)d * (double)weight * factor) : 0.0f;
 }
 
 // A workgroup's rank, and a thread's share of that rank's tokens: every
@@ -301,13 +303,13 @@ __global__ void __launch_bounds__(kPolBlock) policySums(const PolArgs<RANKS> a) 
         for (int e = 0; e < kPolVec; ++e) d[e] = addToken(a, l[e], o[e], v[e], ref != nullptr, f[e], w[e], s);
         if (known)
 #pragma unroll
-          for (int e = 0; e < kPolVec; ++e) d[e] = timesFactor(d[e], factor);
+          for (int e = 0; e < kPolVec; ++e) d[e] = timesFactor(d[e], w[e], factor);
         if (dlogp) storeVec<float, kPolVec>(dlogp + i, d);
       },
       [&](int64_t i) {
-        const float d = addToken(a, logp[i], old[i], advantage[i], ref != nullptr, ref ? ref[i] : 0.0f,
-                                 weight ? weight[i] : 1.0f, s);
-        if (dlogp) dlogp[i] = known ? timesFactor(d, factor) : d;
+        const float w = weight ? weight[i] : 1.0f;
+        const float d = addToken(a, logp[i], old[i], advantage[i], ref != nullptr, ref ? ref[i] : 0.0f, w, s);
+        if (dlogp) dlogp[i] = known ? timesFactor(d, w, factor) : d;
       });
   const double sums = blockSums<kPolBlock>(s, lds);
   if (threadIdx.x < kPolSums) a.partial[(size_t)threadIdx.x * a.partials + blockIdx.x] = sums;
@@ -331,28 +333,32 @@ __global__ void __launch_bounds__(kPolBlock) policyGrad(const PolGradArgs<RANKS>
   __shared__ double lds[kPolBlock / kWave];
   const PolPlace at = polPlace(a);
   float* dlogp = a.dlogp[at.rank];
+  const float* weight = a.weight[at.rank];   // there are some, or their sum was known before
   // a thread's first gradients are on their way while the sums are joined
-  Vec ahead[kPolAhead];
+  Vec ahead[kPolAhead], weightAhead[kPolAhead];
 #pragma unroll
   for (int k = 0; k < kPolAhead; ++k) {
-    ahead[k] = (Vec)0.0f;
-    if (at.first + k * at.step < at.whole) ahead[k] = loadVec<float, kPolVec>(dlogp + at.first + k * at.step);
+    ahead[k] = weightAhead[k] = (Vec)0.0f;
+    const int64_t i = at.first + k * at.step;
+    if (i >= at.whole) continue;
+    ahead[k] = loadVec<float, kPolVec>(dlogp + i);
+    weightAhead[k] = loadVec<float, kPolVec>(weight + i);
   }
   double weights = 0.0;
   for (int i = threadIdx.x; i < a.partials; i += kPolBlock) weights += a.partial[i];
   weights = blockSum64(weights, lds);
   const double factor = a.gradScale * partOf(a, weights);
-  const auto put = [&](int64_t i, Vec d) {
+  const auto put = [&](int64_t i, Vec d, const Vec& w) {
 #pragma unroll
-    for (int e = 0; e < kPolVec; ++e) d[e] = timesFactor(d[e], factor);
+    for (int e = 0; e < kPolVec; ++e) d[e] = timesFactor(d[e], w[e], factor);
     storeVec<float, kPolVec>(dlogp + i, d);
   };
 #pragma unroll
   for (int k = 0; k < kPolAhead; ++k)
-    if (at.first + k * at.step < at.whole) put(at.first + k * at.step, ahead[k]);
+    if (at.first + k * at.step < at.whole) put(at.first + k * at.step, ahead[k], weightAhead[k]);
   forTokens(
-      at, kPolAhead, [&](int64_t i) { put(i, loadVec<float, kPolVec>(dlogp + i)); },
-      [&](int64_t i) { dlogp[i] = timesFactor(dlogp[i], factor); });
+      at, kPolAhead, [&](int64_t i) { put(i, loadVec<float, kPolVec>(dlogp + i), loadVec<float, kPolVec>(weight + i)); },
+      [&](int64_t i) { dlogp[i] = timesFactor(dlogp[i], weight[i], factor); });
 }
 
 // Few tokens: one workgroup, one launch, the gradients kept in registers until
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(kPolFewBlock) policyFew(const PolArgs<RANKS> a
   const double factor = a.gradScale * partOf(a, laneOf(sums, 0));
 #pragma unroll
   for (int k = 0; k < kPolFewEach; ++k)
-    if (any[k] && dlogp[k]) *dlogp[k] = timesFactor(d[k], factor);
+    if (any[k] && dlogp[k]) *dlogp[k] = timesFactor(d[k], weight[k], factor);
 }
 
 // Shares a launch's tokens out among its workgroups, one partial sum each, or,

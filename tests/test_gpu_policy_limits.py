@@ -81,3 +81,22 @@ def test_an_infinite_difference_has_an_infinite_kl(B, tokens, kw):  # noqa: F811
         data[0][0][2] = data[2][0][2] = -math.inf   # by both: no difference
         stats, out = pol.run(B, data, kl=0.5, **kw)
         assert torch.isnan(stats[[0, 2]]).all() and torch.isnan(out[0][2])
+
+
+@forms
+@pytest.mark.parametrize("power", [120, -120])
+def test_the_weights_scale_does_not_matter(B, tokens, kw, power):  # noqa: F811
+    """A power of two common to all weights, and to a given denominator, moves no bit, though a weight times its
+    token's gradient is past what 32 bits hold."""
+    data = inputs(tokens, 4)
+    for t in data[3]:
+        t.mul_(2.0 ** (power // 10))
+    want = pol.run(B, data, **kw)
+    pol.check(want, data, **kw)
+    far = data[:4] + ([t * 2.0 ** power for t in data[4]],)
+    if "denominator" in kw:
+        kw = dict(denominator=kw["denominator"] * 2.0 ** power)
+    stats, out = pol.run(B, far, **kw)
+    assert torch.equal(stats[:4], want[0][:4]) and stats[4] == want[0][4] * 2.0 ** power   # in 32 bits: past them infinite
+    assert all(torch.equal(a, b) for a, b in zip(out, want[1]))
+    assert same((stats, out), pol.run(B, far, inplace=True, **kw))
