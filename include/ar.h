@@ -818,7 +818,7 @@ arResult_t arTokenLogprobBackward(const float* dlogp, const void* const* logits,
  *  clipLow, clipHigh  0..1, and >= 0 (may be infinite).
  *  klCoef    finite, >= 0.  With 0 the KL term of a given ref is only reported: L and
  *            dlogp are those without it, however large it is.
- *  denominator  D, finite and > 0, or 0: the sum of all weights.  Where D is 0
+ *  denominator  D, 2^-1022 or more and finite, or 0: the sum of all weights.  Where D is 0
  *            (no token has a weight) L and every dlogp are 0.
  *  gradScale finite; a loss scale.
  *  stats     (device) five floats: L, the mean of loss, the mean of kl, the

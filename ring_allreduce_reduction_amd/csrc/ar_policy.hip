@@ -232,6 +232,12 @@ __device__ __forceinline__ double partOf(const PolCall& a, double weights) {
   return over != 0.0 ? 1.0 / over : 0.0;
 }
 
+// The gradients' common factor, held at the largest number, so that it leaves a
+// gradient of 0 at 0 (and makes any other infinite).
+__device__ __forceinline__ double factorOf(double f) {
+  return fabs(f) == INFINITY ? copysign(0x1.fffffffffffffp1023, f) : f;
+}
+
 // Called by the workgroup's threads with what blockSums gave them.
 __device__ __forceinline__ void putStats(const PolCall& a, double sums) {
   const double weights = laneOf(sums, 0), loss = laneOf(sums, 1), klSum = laneOf(sums, 2), clipped = laneOf(sums, 3);
@@ -290,7 +296,7 @@ __global__ void __launch_bounds__(kPolBlock) policySums(const PolArgs<RANKS> a) 
   double s[kPolSums] = {0.0, 0.0, 0.0, 0.0};
   typedef FloatVec<kPolVec> Vec;
   const bool known = a.over > 0.0;
-  const double factor = known ? a.gradScale / a.over : 1.0;
+  const double factor = known ? factorOf(a.gradScale / a.over) : 1.0;
   forTokens(
       at, 0,
       [&](int64_t i) {
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(kPolBlock) policyGrad(const PolGradArgs<RANKS>
   double weights = 0.0;
   for (int i = threadIdx.x; i < a.partials; i += kPolBlock) weights += a.partial[i];
   weights = blockSum64(weights, lds);
-  const double factor = a.gradScale * partOf(a, weights);
+  const double factor = factorOf(a.gradScale * partOf(a, weights));
   const auto put = [&](int64_t i, Vec d, const Vec& w) {
 #pragma unroll
     for (int e = 0; e < kPolVec; ++e) d[e] = timesFactor(d[e], w[e], factor);
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(kPolFewBlock) policyFew(const PolArgs<RANKS> a
     if (any[k]) d[k] = addToken(a, logp[k], old[k], advantage[k], hasRef, ref[k], weight[k], s);
   const double sums = blockSums<kPolFewBlock>(s, lds);
   putStats(a, sums);
-  const double factor = a.gradScale * partOf(a, laneOf(sums, 0));
+  const double factor = factorOf(a.gradScale * partOf(a, laneOf(sums, 0)));
 #pragma unroll
   for (int k = 0; k < kPolFewEach; ++k)
     if (any[k] && dlogp[k]) *dlogp[k] = timesFactor(d[k], weight[k], factor);
@@ -466,7 +472,7 @@ arResult_t policyLoss(const float* const* logp, const float* const* old, const f
   if (!rowsOk(tokens, nranks, &s) || !aligned(stats, 4)) return arInvalidArgument;
   if (!(clipLow >= 0.0 && clipLow <= 1.0) || !(clipHigh >= 0.0)) return arInvalidArgument;
   if (!(klCoef >= 0.0) || !std::isfinite(klCoef) || !std::isfinite(gradScale)) return arInvalidArgument;
-  if (!(denominator >= 0.0) || !std::isfinite(denominator)) return arInvalidArgument;
+  if (denominator != 0.0 && !(denominator > 0.0 && std::isnormal(denominator))) return arInvalidArgument;
   if (klCoef != 0.0 && ref == nullptr) return arInvalidArgument;
   if (groupOpen()) return arInvalidUsage;
   if (s.total > 0 && (logp == nullptr || old == nullptr || advantage == nullptr)) return arInvalidArgument;

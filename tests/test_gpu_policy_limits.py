@@ -100,3 +100,23 @@ def test_the_weights_scale_does_not_matter(B, tokens, kw, power):  # noqa: F811
     assert torch.equal(stats[:4], want[0][:4]) and stats[4] == want[0][4] * 2.0 ** power   # in 32 bits: past them infinite
     assert all(torch.equal(a, b) for a, b in zip(out, want[1]))
     assert same((stats, out), pol.run(B, far, inplace=True, **kw))
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("tokens", [[600, 8], [9000, 100]], ids=["few", "two passes"])
+def test_a_factor_past_64_bits(B, tokens, sign):  # noqa: F811
+    """gradScale / D is infinite: a gradient of 0 stays 0, others are infinite; with the weights' sum for D too."""
+    data = inputs(tokens, 5)
+    data[3][0][0], data[0][0][1], data[3][0][1] = 0.0, data[1][0][1] + 1.0, 1.0   # no advantage; clipped
+    small = data[:4] + ([t * 2.0 ** -140 for t in data[4]],)
+    for d, kw in ((data, dict(denominator=2.3e-308, scale=sign * 1e10)), (small, dict(scale=sign * 1e300))):
+        stats, out = pol.run(B, d, ref=False, **kw)
+        assert not torch.isnan(stats).any() and out[0][0] == 0 and out[0][1] == 0
+        for r, t in enumerate([v.cpu() for v in out]):
+            assert not torch.isnan(t).any() and (t[d[4][r] == 0] == 0).all()
+            if "denominator" in kw:
+                live = t[(d[4][r] > 0) & (t != 0)]
+                assert torch.isinf(live).all() and len(live) > len(t) // 3
+    none = data[:4] + ([torch.zeros_like(t) for t in data[4]],)
+    stats, out = pol.run(B, none, denominator=2.3e-308, scale=sign * 1e10)
+    assert (stats == 0).all() and all((t == 0).all() for t in out)
