@@ -816,8 +816,8 @@ arResult_t arTokenLogprobBackward(const float* dlogp, const void* const* logits,
  *  tokens    (host, nranks) at most 2^31-1 together; a rank may have 0 (its
  *            pointers are not looked at then).
  *  clipLow, clipHigh  0..1, and >= 0 (may be infinite).
- *  klCoef    finite, >= 0.  With 0 the KL term of a given ref is only reported: L and
- *            dlogp are those without it, however large it is.
+ *  klCoef    0..3.4e38 (dlogp uses it in 32 bits, at least 2^-149).  With 0 the KL term of a given ref
+ *            is only reported: L and dlogp are those without it, however large it is.
  *  denominator  D, 2^-1022 or more and finite, or 0: the sum of all weights.  Where D is 0
  *            (no token has a weight) L and every dlogp are 0.
  *  gradScale finite; a loss scale.

@@ -57,6 +57,7 @@ struct PolCall {
   double over;                         // what the sums are divided by, where the host knows it; else 0
   double logLow, logHigh;              // log(1 - low), log(1 + high)
   float low, high;                     // 1 - low, 1 + high
+  float klGrad;                        // klCoef in 32 bits, 0 only where it is
   bool hasRef;
 };
 
@@ -140,7 +141,7 @@ __device__ __forceinline__ Token tokenOf(const PolCall& a, float logp, float old
     const float2 less = expLess((float)((double)ref - (double)logp));
     t.kl = less.y;
     // of coefficient 0 it is only reported, and may be infinite
-    if (a.klCoef != 0.0) t.dlogp -= (float)a.klCoef * less.x;
+    if (a.klGrad != 0.0f) t.dlogp -= a.klGrad * less.x;
   }
   return t;
 }
@@ -471,7 +472,7 @@ arResult_t policyLoss(const float* const* logp, const float* const* old, const f
   Shape s;
   if (!rowsOk(tokens, nranks, &s) || !aligned(stats, 4)) return arInvalidArgument;
   if (!(clipLow >= 0.0 && clipLow <= 1.0) || !(clipHigh >= 0.0)) return arInvalidArgument;
-  if (!(klCoef >= 0.0) || !std::isfinite(klCoef) || !std::isfinite(gradScale)) return arInvalidArgument;
+  if (!(klCoef >= 0.0 && klCoef <= 0x1.fffffep127) || !std::isfinite(gradScale)) return arInvalidArgument;
   if (denominator != 0.0 && !(denominator > 0.0 && std::isnormal(denominator))) return arInvalidArgument;
   if (klCoef != 0.0 && ref == nullptr) return arInvalidArgument;
   if (groupOpen()) return arInvalidUsage;
@@ -505,6 +506,7 @@ arResult_t policyLoss(const float* const* logp, const float* const* old, const f
   a.logLow = std::log1p(-clipLow);
   a.logHigh = std::log1p(clipHigh);
   a.klCoef = klCoef;
+  a.klGrad = klCoef > 0.0 && klCoef < 0x1p-149 ? 0x1p-149f : (float)klCoef;
   a.denominator = denominator;
   a.gradScale = gradScale;
   a.over = denominator > 0.0 ? denominator : weight == nullptr ? (double)s.total : 0.0;

@@ -120,3 +120,18 @@ def test_a_factor_past_64_bits(B, tokens, sign):  # noqa: F811
     none = data[:4] + ([torch.zeros_like(t) for t in data[4]],)
     stats, out = pol.run(B, none, denominator=2.3e-308, scale=sign * 1e10)
     assert (stats == 0).all() and all((t == 0).all() for t in out)
+
+
+@forms
+def test_the_smallest_and_largest_coefficients(B, tokens, kw):  # noqa: F811
+    """One below 32 bits' range still meets an exponential past it; the largest one no difference at all."""
+    data = inputs(tokens, 6)
+    logp, old, ref, adv, w = data
+    want = pol.run(B, data, ref=False, **kw)
+    ref[0][0] = logp[0][0] + 200.0
+    stats, out = pol.run(B, data, kl=1e-60, **kw)
+    assert stats[0].item() == math.inf and out[0][0].item() == -math.inf
+    assert torch.equal(stats[1], want[0][1]) and torch.equal(out[0][1:], want[1][0][1:])
+    same_ref = (logp, old, logp, adv, w)
+    stats, out = pol.run(B, same_ref, kl=3.4e38, **kw)
+    assert stats[2] == 0 and same((stats, out), want)
