@@ -779,7 +779,7 @@ arResult_t arTokenLogprobWorkspace(size_t rows, const size_t* cols, int nranks, 
 /*
  * arTokenLogprobBackward -- the gradient of the logits from that of logp:
  *   dlogits[j] = scale * dlogp * ([j = t] - exp(scale * (x[j] - top) - logSum)),
- * formed in 32 bits and rounded once.
+ * formed in 32 bits and rounded once; scale * dlogp may be past them.
  *  dlogp     (device) `rows` floats.  Rows whose dlogp is 0 (a token that was
  *            clipped) and ignored rows receive zeros; their logits are not read.
  *  top, logSum  what arTokenLogprob wrote.

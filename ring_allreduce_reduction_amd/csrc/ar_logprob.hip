@@ -367,8 +367,12 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpBackArg
        row += (int64_t)gridDim.y * ROWS) {
     const int64_t t = a.targets[row], place = t - a.colStart[p.rank];
     const int at = place >= 0 && place < p.to ? (int)place : -1;   // the target's column here
-    const float d = a.dlogp[row] * a.scale, base = baseOf(a.top[row]), logSum = a.logSum[row] * kLog2e;
+    const float dlogp = a.dlogp[row], base = baseOf(a.top[row]), logSum = a.logSum[row] * kLog2e;
+    // their product where 32 bits hold it, else 2^-127 of it; NaN past the vocabulary
+    const bool far = fabsf(dlogp * a.scale) == INFINITY;
+    const float d = far ? (dlogp * 0x1p-64f) * (a.scale * 0x1p-63f) : dlogp * a.scale;
     const float g = t < 0 ? 0.0f : t < a.vocabulary || d == 0.0f ? d : NAN;
+    const float back = far ? 0x1p127f : 1.0f;
     const T* x = (const T*)a.x[p.rank] + row * a.xStride[p.rank];
     T* dx = (T*)b.dx[p.rank] + row * b.dxStride[p.rank];
     const Part part = partOf<T, V>(dx, p.from, p.to);
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpBackArg
     const int skip = THREADS >= kWave ? (int)((uintptr_t)(dx + part.first) % 128 / 16) : 0;
     const auto element = [&](float v, int c) {
       const float q = __builtin_amdgcn_exp2f(fmaf(v - base, a.scaleLog2e, -logSum));
-      return (T)(g * ((c == at ? 1.0f : 0.0f) - q));
+      return (T)(g * ((c == at ? 1.0f : 0.0f) - q) * back);
     };
     if (g == 0.0f)
       forPart<V, THREADS * V>(
