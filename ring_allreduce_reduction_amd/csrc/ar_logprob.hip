@@ -370,8 +370,7 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpBackArg
     const float dlogp = a.dlogp[row], base = baseOf(a.top[row]), logSum = a.logSum[row] * kLog2e;
     // their product where 32 bits hold it, else 2^-127 of it; NaN past the vocabulary
     const bool far = fabsf(dlogp * a.scale) == INFINITY;
-    const float d = far ? (dlogp * 0x1p-64f) * (a.scale * 0x1p-63f) : dlogp * a.scale;
-    const float g = t < 0 ? 0.0f : t < a.vocabulary || d == 0.0f ? d : NAN;
+    const float g = t >= a.vocabulary ? NAN : far ? (dlogp * 0x1p-64f) * (a.scale * 0x1p-63f) : dlogp * a.scale;
     const float back = far ? 0x1p127f : 1.0f;
     const T* x = (const T*)a.x[p.rank] + row * a.xStride[p.rank];
     T* dx = (T*)b.dx[p.rank] + row * b.dxStride[p.rank];
@@ -383,7 +382,7 @@ __global__ void __launch_bounds__(kLpBlock) tokenLogprobBackward(const LpBackArg
       const float q = __builtin_amdgcn_exp2f(fmaf(v - base, a.scaleLog2e, -logSum));
       return (T)(g * ((c == at ? 1.0f : 0.0f) - q) * back);
     };
-    if (g == 0.0f)
+    if (t < 0 || dlogp == 0.0f)
       forPart<V, THREADS * V>(
           part, thread, [&](int c) { store(dx + c, (Vec)(T)0.0f); }, [&](int c) { dx[c] = (T)0.0f; }, skip, THREADS * V);
     else

@@ -1,4 +1,4 @@
-"""The gradient of token log-probabilities where the scale times dlogp is past what 32 bits hold."""
+"""The gradient of token log-probabilities where the scale times dlogp is past or below what 32 bits hold."""
 import math
 
 import pytest
@@ -37,3 +37,18 @@ def test_a_scale_times_dlogp_past_32_bits(B, dt, widths, inplace):  # noqa: F811
         rest = out[i].clone()
         rest[t[i]] = rest[best] = 0.0
         assert (rest == 0).all()
+
+
+@pytest.mark.parametrize("widths", [[50, 25], [9000, 0, 193]], ids=str)
+def test_a_scale_times_dlogp_below_32_bits(B, widths):  # noqa: F811
+    """Rounds to 0; but a row without a distribution and a target past the vocabulary still give NaN, and rows whose
+    dlogp is 0 zeros."""
+    n, scale = sum(widths), 2.0 ** -100
+    whole = torch.randn(6, n, generator=torch.Generator().manual_seed(n))
+    whole[1, 20] = whole[4, 20] = math.nan
+    t = torch.tensor([3, 4, n, -1, 4, n])
+    d = torch.tensor([1e-20, 1e-20, -1e-20, 1e-20, 0.0, 0.0])
+    xs = [v.contiguous() for v in whole.split(widths, 1)]
+    logp, top, log_sum = lp.run_forward(B, xs, t, scale)
+    out = torch.cat([o.cpu() for o in lp.run_backward(B, d, xs, t, top.cpu(), log_sum.cpu(), scale)], 1)
+    assert torch.isnan(out[1:3]).all() and (out[[0, 3, 4, 5]] == 0).all()
