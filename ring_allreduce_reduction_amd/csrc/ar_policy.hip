@@ -10,12 +10,15 @@
 // The mean is over all ranks, so the gradient's factor is a sum over every
 // token: the first pass leaves the sums and the gradients short of that factor
 // and of their weights, the second multiplies them by both (reading the weights
-// again: 8 x 262144 tokens 16.9 us, 16.3 where the first pass applied them in 32
-// bits, which weights far from 1 leave).  Whether a ratio passes a bound is decided
+// again: 8 x 262144 tokens 16.5-16.9 us, 16.0-16.4 where the first pass applied
+// them in 32 bits, which weights far from 1 leave).  Whether a ratio passes a bound is decided
 // by differences in 64 bits against the bounds' logarithms, since these are
 // numbers that may nearly agree; the sums are in 64 bits; what lies between is
 // formed in 32, kl by its series where it is a difference of nearly equal
 // numbers.
+//
+// Times in comments are of calls in a replayed graph; a call from the host takes
+// up to 1.6 us longer where it is short.
 #include <cmath>
 #include <new>
 #include <vector>
@@ -28,24 +31,23 @@ namespace {
 constexpr int kPolBlock = 256;
 constexpr int kPolSums = 4;            // weights, weighted loss, kl, clipped tokens
 // Workgroups, and partial sums, of a launch at most, and where they do with a
-// vector a thread: 8 x 262144 tokens 16.9 us with 2 a CU, 20.2 with 1, 17.7 with
-// 4, 20.9 with 8, whose sums cost as much as their tokens; 8 x 100000 10.2, 11.4,
-// 9.4 and 9.4.  Two vectors a thread in flight in the first pass cost a tenth.
+// vector a thread: 8 x 262144 tokens 16.5 us with 2 a CU, 20.4 with 1, 17.0 with
+// 4, 19.6 with 8, whose sums cost as much as their tokens; 8 x 75000 8.7 with 4 a
+// CU and 9.4 with 2, x 100000 10.0 and 10.2, without weights 8.7 and 8.1.  Two
+// vectors a thread in flight in the first pass cost a tenth.
 constexpr int kPolGrid = 2 * kOpsCUs, kPolOnce = 4 * kOpsCUs;
 constexpr int kPolVec = 4;             // tokens of a thread at a time
-// Vectors of a thread that the second pass has on their way while it joins the
-// sums: with one 17.7 us, with two 17.1, with eight 17.0.
-constexpr int kPolAhead = 4;
 constexpr int kPolFewBlock = 1024;
 constexpr int kPolFewEach = 5;
 // Tokens of one workgroup's launch: its wavefronts' parts of 64, less what the
-// ranks leave of their last ones.  8 x 64 tokens 3.8 us (6.6 in two launches), x
-// 256 5.0 (6.4), x 512 6.3 (6.6); 6000 of one rank 7.6 (6.2).
+// ranks leave of their last ones.  8 x 64 tokens 3.7 us (6.0 in two launches), x
+// 256 4.8 (5.9), x 512 6.3 (6.1); 6000 of one rank 7.5 (5.9).
 constexpr int kPolFew = kPolFewBlock * kPolFewEach - kOpRanks * kWave;
 
 // Ranks of a launch at most.  Up to kOpRanks of them travel in arguments of
-// that size, which take less time to hand over (1250 tokens of 4 ranks 4.4 us,
-// 4.6 with twice the size; 20 ranks 6.5, 18 in two launches and a third).
+// that size, which take the host less time to hand over (1250 tokens of 4 ranks,
+// calls from the host, 4.8 us, 5.2 with twice the size; 20 ranks 5.9, 18 in two
+// launches and a third).
 constexpr int kPolRanks = 2 * kOpRanks;
 
 struct PolCall {
@@ -129,7 +131,7 @@ __device__ __forceinline__ Token tokenOf(const PolCall& a, float logp, float old
   const double change = (double)logp - (double)old;
   const bool up = advantage > 0.0f && change > a.logHigh, down = advantage < 0.0f && change < a.logLow;
   // An advantage of 0 takes no part, not of an infinite ratio either.  Without a
-  // branch: 8 x 262144 tokens 16.3 us, 19.0 with one.
+  // branch: 8 x 262144 tokens 16.4 us, 19.0 with one.
   const float e = expFast((float)change);
   const bool idle = (advantage == 0.0f) & (e == INFINITY);
   const float ratio = idle ? 0.0f : e;
@@ -341,15 +343,14 @@ __global__ void __launch_bounds__(kPolBlock) policyGrad(const PolGradArgs<RANKS>
   const PolPlace at = polPlace(a);
   float* dlogp = a.dlogp[at.rank];
   const float* weight = a.weight[at.rank];   // there are some, or their sum was known before
-  // a thread's first gradients are on their way while the sums are joined
-  Vec ahead[kPolAhead], weightAhead[kPolAhead];
-#pragma unroll
-  for (int k = 0; k < kPolAhead; ++k) {
-    ahead[k] = weightAhead[k] = (Vec)0.0f;
-    const int64_t i = at.first + k * at.step;
-    if (i >= at.whole) continue;
-    ahead[k] = loadVec<float, kPolVec>(dlogp + i);
-    weightAhead[k] = loadVec<float, kPolVec>(weight + i);
+  // a thread's first vector is on its way while the sums are joined (8 x 262144
+  // tokens 16.5 us, with its first four 16.5, eight 16.5; x 1 M 49.6, 49.7, 50.4; x
+  // 12500 6.3, 6.5, 6.6)
+  const bool any = at.first < at.whole;
+  Vec ahead = (Vec)0.0f, weightAhead = (Vec)0.0f;
+  if (any) {
+    ahead = loadVec<float, kPolVec>(dlogp + at.first);
+    weightAhead = loadVec<float, kPolVec>(weight + at.first);
   }
   double weights = 0.0;
   for (int i = threadIdx.x; i < a.partials; i += kPolBlock) weights += a.partial[i];
@@ -360,11 +361,9 @@ __global__ void __launch_bounds__(kPolBlock) policyGrad(const PolGradArgs<RANKS>
     for (int e = 0; e < kPolVec; ++e) d[e] = timesFactor(d[e], w[e], factor);
     storeVec<float, kPolVec>(dlogp + i, d);
   };
-#pragma unroll
-  for (int k = 0; k < kPolAhead; ++k)
-    if (at.first + k * at.step < at.whole) put(at.first + k * at.step, ahead[k], weightAhead[k]);
+  if (any) put(at.first, ahead, weightAhead);
   forTokens(
-      at, kPolAhead, [&](int64_t i) { put(i, loadVec<float, kPolVec>(dlogp + i), loadVec<float, kPolVec>(weight + i)); },
+      at, 1, [&](int64_t i) { put(i, loadVec<float, kPolVec>(dlogp + i), loadVec<float, kPolVec>(weight + i)); },
       [&](int64_t i) { dlogp[i] = timesFactor(dlogp[i], weight[i], factor); });
 }
 
