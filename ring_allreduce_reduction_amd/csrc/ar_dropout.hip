@@ -8,6 +8,9 @@
 // Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) gives 128 bits for
 // 8 columns of a row, 16 a column: k = 1 where they are T = round(65536 p) or
 // more, and s = 65536 / (65536 - T), so that the mean is x + bias exactly.
+//
+// Times in comments are of calls in a replayed graph; a call from the host takes
+// about 1 us longer where it is short.
 #include <cmath>
 #include <new>
 #include <vector>
@@ -34,8 +37,9 @@ struct DropCut {
 };
 
 // Ranks of a launch at most.  Up to kOpRanks of them travel in arguments of
-// that size, which take less time to hand over (4 ranks' 64 rows of 768 fp32 4.1
-// us, 4.6 with twice the size; 20 ranks' 6.0, 8.2 in two launches).
+// that size, which take the host less time to hand over (calls from it: 4 ranks'
+// 64 rows of 768 fp32 4.3 us, 4.4 with twice the size; 8 ranks' 8 rows of 8192
+// backward 6.1, 6.3; 20 ranks' 64 of 768 4.9, 8.2 in two launches).
 constexpr int kDropRanks = 2 * kOpRanks;
 
 struct DropCall {

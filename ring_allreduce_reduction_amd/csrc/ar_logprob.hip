@@ -8,6 +8,9 @@
 // type's lowest value, and rows of nothing else, neither overflow nor cancel;
 // M and ln S are kept apart for the same reason.  One pass: a thread keeps the
 // largest value it has met and the sum relative to it.
+//
+// Times in comments are of calls in a replayed graph; a call from the host takes
+// up to 2.2 us longer where it is short.
 #include <cmath>
 #include <new>
 #include <type_traits>
@@ -23,8 +26,9 @@ constexpr int kLpVecs = 4;       // of a thread in flight
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 // Ranks of a launch at most.  Up to kOpRanks of them travel in arguments of
-// that size, which take less time to hand over (one token, 8 ranks: 6.3 us, 6.8
-// with twice the size; 20 ranks 7.6, 10.4 in two launches and a join).
+// that size, which take the host a little less time to hand over (one token of 8 x
+// 16000, calls from the host: 7.8 us, 7.9 with twice the size; 20 ranks 7.6, 10.4
+// in two launches and a join).
 constexpr int kLpRanks = 2 * kOpRanks;
 
 struct LpCall {
@@ -416,8 +420,8 @@ struct LpCut {
 };
 
 // Pieces need a second launch, so they are for few rows of a long vocabulary:
-// 64 rows x 8 x 16000 bf16 9.3 us in pieces, 10.9 a workgroup a row; 128 rows
-// 12.3, 12.4; 300 20.6, 19.3; one row x 8 x 4000 6.7, 5.4; x 8000 6.8, 7.0.  A
+// 64 rows x 8 x 16000 bf16 8.4 us in pieces, 10.7 a workgroup a row; 128 rows
+// 10.9, 11.8; 200 15.0, 12.4; one row x 8 x 4000 5.6, 4.7; x 8000 5.7, 6.5.  A
 // piece is 8192 columns, or down to 2048 where they are few (backward 96 rows x 4
 // x 8003 fp32 6.2 us, 6.8 without; more than two a CU gained nothing).
 LpCut lpCut(const size_t* cols, int nranks, size_t rows) {
@@ -510,7 +514,8 @@ struct LpRows {
   // 2056 383, 450; 50000 x 8 x 2600 354, 379; 40000 x 8 x 3000 327, 321) and ask for
   // more rows (1200 x 8 x 2000 13.5, 11.6; 8192 46.6, 47.3); one to three gain less
   // (16500 x 1 x 1316 12.4, 14.9; 5000 x 3 x 1500 15.0, 12.9; 40000 x 2 x 2800 79.8,
-  // 71.8).
+  // 71.8).  fp32 goes by its vectors of 16 bytes too (4200 x 8 x 481 15.1, 21.1; x 1361
+  // 32.1, 33.5; x 1521 39.1, 39.1; 8300 x 1 x 721 6.2, 7.4).
   static bool narrow(const LpArgs<kLpRanks>& a) {
     constexpr int V = kVec<DT>;
     const int64_t columns = (a.colStart[a.nranks] - a.colStart[0]) / a.nranks;
@@ -583,7 +588,9 @@ struct LpBackward {
     // 2.1 GB of logits in 8 shards, bf16: of 100 columns 1290 us with 16 threads a
     // row, 2026 with 32; 250 1174, 1124, 1707 with 64; 520 1310, 897, 1031; 800 697
     // with 32, 687; 1032 903, 787, 1002 with 128; 1600 663 with 64, 686; 2000 738, 671,
-    // 1037 with 256; 3000 652 with 128, 708; 4000 685, 666; 5000 726, 691.
+    // 1037 with 256; 3000 652 with 128, 708; 4000 685, 666; 5000 726, 691.  fp32 by its
+    // vectors of 16 bytes too (2000 rows x 8 x 93 5.2 with 16, 5.7 with 32; 441 12.1,
+    // 12.5 with 64; 953 21.0, 21.1 with 128; 1681 33.8, 33.1 with 256).
     if (widest <= 24 * V) return launch<16>(b, stream, st);
     if (widest <= 112 * V) return launch<32>(b, stream, st);
     if (widest <= 240 * V) return launch<64>(b, stream, st);
