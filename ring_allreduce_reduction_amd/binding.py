@@ -667,8 +667,8 @@ def arPolicyLossWorkspace(tokens):
 def arPolicyLoss(logps, olds, advantages, stats, refs=None, weights=None, dlogps=None, clipLow=0.2, clipHigh=0.2,
                  klCoef=0.0, denominator=0.0, gradScale=1.0, workspace=None, stream=None):
     """The clipped policy loss with a KL term, its mean over every rank's tokens, and its gradient dlogps (may be
-    logps, or None).  Lists of one float32 tensor per rank, one value a token; weights 0 leave tokens out.  stats:
-    five floats, the loss, its policy and KL parts, the clipped share, the sum of the weights.  denominator 0: the
+    logps, or None).  Lists of one float32 tensor per rank, one value a token; weights 0 leave tokens out; with refs
+    and a klCoef of 0 the KL part is only reported.  stats: five floats, the loss, its policy and KL parts, the clipped share, the sum of the weights.  denominator 0: the
     sum of the weights.  workspace: a device tensor of arPolicyLossWorkspace bytes that no other running call uses;
     None allocates one where it is needed."""
     call = _torch_calls().policy_loss
