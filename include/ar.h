@@ -816,8 +816,9 @@ arResult_t arTokenLogprobBackward(const float* dlogp, const void* const* logits,
  *  tokens    (host, nranks) at most 2^31-1 together; a rank may have 0 (its
  *            pointers are not looked at then).
  *  clipLow, clipHigh  0..1, and >= 0 (may be infinite).
- *  klCoef    0..3.4e38 (dlogp uses it in 32 bits, at least 2^-149).  With 0 the KL term of a given ref
- *            is only reported: L and dlogp are those without it, however large it is.
+ *  klCoef    0..3.4e38 (dlogp uses it in 32 bits, at least 2^-149).  With 0 the KL
+ *            term of a given ref is only reported: L and dlogp are those without
+ *            it, however large it is.
  *  denominator  D, 2^-1022 or more and finite, or 0: the sum of all weights.  Where D is 0
  *            (no token has a weight) L and every dlogp are 0.
  *  gradScale finite; a loss scale.
@@ -828,9 +829,10 @@ arResult_t arTokenLogprobBackward(const float* dlogp, const void* const* logits,
  *            arPolicyLossWorkspace reports 0.
  * Which tokens are clipped is decided in 64 bits, so that it does not depend on
  * roundings; all sums are in 64 bits; a token's terms, g and kl are formed in 32
- * (a ratio past 3.4e38 is infinite; one of exp(d) is off by up to 2^-24 (2.5 |d| + 4)
- * of itself), a small kl with all its bits; gradScale w / D is in 64 bits and
- * dlogp rounded once more, so that a scale common to all weights does not matter.
+ * (a ratio exp(d) past 3.4e38 is infinite, others are off by up to 2^-24 (2.5 |d| +
+ * 4) of themselves), a small kl with all its bits; gradScale w / D is in 64 bits
+ * and dlogp rounded once more, so that a scale common to all weights does not
+ * matter.
  * Outputs must not overlap any other buffer.  Errors: as arTokenLogprob.
  */
 arResult_t arPolicyLoss(const float* const* logp, const float* const* old, const float* const* ref,

@@ -39,7 +39,7 @@ struct DropCut {
 // Ranks of a launch at most.  Up to kOpRanks of them travel in arguments of
 // that size, which take the host less time to hand over (calls from it: 4 ranks'
 // 64 rows of 768 fp32 4.3 us, 4.4 with twice the size; 8 ranks' 8 rows of 8192
-// backward 6.1, 6.3; 20 ranks' 64 of 768 4.9, 8.2 in two launches).
+// backward 6.1, 6.3; 20 ranks' through the binding 6.0, 8.2 in two launches).
 constexpr int kDropRanks = 2 * kOpRanks;
 
 struct DropCall {

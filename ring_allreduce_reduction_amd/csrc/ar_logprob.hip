@@ -27,8 +27,8 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417
 
 // Ranks of a launch at most.  Up to kOpRanks of them travel in arguments of
 // that size, which take the host a little less time to hand over (one token of 8 x
-// 16000, calls from the host: 7.8 us, 7.9 with twice the size; 20 ranks 7.6, 10.4
-// in two launches and a join).
+// 16000, calls from the host: 7.8 us, 7.9 with twice the size; 20 ranks through the
+// binding 7.6, 10.4 in two launches and a join).
 constexpr int kLpRanks = 2 * kOpRanks;
 
 struct LpCall {

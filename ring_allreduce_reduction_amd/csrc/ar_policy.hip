@@ -11,11 +11,11 @@
 // token: the first pass leaves the sums and the gradients short of that factor
 // and of their weights, the second multiplies them by both (reading the weights
 // again: 8 x 262144 tokens 16.5-16.9 us, 16.0-16.4 where the first pass applied
-// them in 32 bits, which weights far from 1 leave).  Whether a ratio passes a bound is decided
-// by differences in 64 bits against the bounds' logarithms, since these are
-// numbers that may nearly agree; the sums are in 64 bits; what lies between is
-// formed in 32, kl by its series where it is a difference of nearly equal
-// numbers.
+// them in 32 bits, which weights far from 1 leave).  Whether a ratio passes a
+// bound is decided by differences in 64 bits against the bounds' logarithms, since
+// these are numbers that may nearly agree; the sums are in 64 bits; what lies
+// between is formed in 32, kl by its series where it is a difference of nearly
+// equal numbers.
 //
 // Times in comments are of calls in a replayed graph; a call from the host takes
 // up to 1.6 us longer where it is short.
@@ -46,8 +46,8 @@ constexpr int kPolFew = kPolFewBlock * kPolFewEach - kOpRanks * kWave;
 
 // Ranks of a launch at most.  Up to kOpRanks of them travel in arguments of
 // that size, which take the host less time to hand over (1250 tokens of 4 ranks,
-// calls from the host, 4.8 us, 5.2 with twice the size; 20 ranks 5.9, 18 in two
-// launches and a third).
+// calls from the host, 4.8 us, 5.2 with twice the size; 20 ranks through the
+// binding 6.5, 18 in two launches and a third).
 constexpr int kPolRanks = 2 * kOpRanks;
 
 struct PolCall {
